@@ -136,6 +136,116 @@ int llm_op_gemm_f16(const void *A, const void *B, int32_t M, int32_t N, int32_t 
 int llm_op_gemm_quant(int32_t fmt, const void *A, const void *w, const void *s, int32_t M, int32_t N,
                       int32_t K, float *C, void *stream);
 
+/* ---- The 8-bit K/V cache ----------------------------------------------------
+ * A paged cache that holds K and V in 8 bits with one fp32 scale for each block
+ * of one page (16 tokens) and one head, K and V apart: value = code * scale.
+ * The pages are laid out as the engine's bf16 pools ("How To Construct Your
+ * Personal LLM Runtime From Scratch", §3: 16-token pages reached through a page
+ * table); 8 bits a number halve what a long-context step reads.
+ *
+ * All calls take sequences by three numbers: row_start, int32 [n_seqs + 1] on
+ * the device, the first row of each sequence among the call's rows
+ * (nondecreasing, row_start[0] >= 0; sequence b has rows row_start[b] ..
+ * row_start[b + 1] - 1); kv_len, int32 [n_seqs] on the device, each sequence's
+ * length with those rows in it, so that its rows are its last tokens, at
+ * positions kv_len[b] - rows .. kv_len[b] - 1; and n_rows on the host, the rows
+ * that the arrays hold.  Rows behind row_start[n_seqs] are left as they are.  The
+ * same three serve a step's append and then its attention.
+ *
+ * The calls are asynchronous on `stream`, allocate nothing and can be captured
+ * into a graph.  Lengths and tables are read on the device, where every index is
+ * checked before it is used: err, an int32 on the device or NULL, becomes
+ * LLM_ERR_DEVICE if it was 0 and a sequence's numbers or a page are out of range
+ * (a sequence with kv_len outside [0, 16 * table_stride], in append and read
+ * also one with more rows than kv_len, is left out: nothing of it is read or
+ * written, its attention rows are zero; a page outside [0, n_pool_pages) is left
+ * out).  No call clears it.  Errors returned: LLM_ERR_ARG before any launch,
+ * LLM_ERR_CUDA.                                                               */
+#define LLM_KV8_INT8 1 /* codes: int8 in [-127, 127]                            */
+#define LLM_KV8_E4M3 2 /* codes: 8-bit floats (4 exponent, 3 mantissa bits), finite */
+
+/* Types of the dense rows of these calls. */
+#define LLM_DTYPE_F32 0
+#define LLM_DTYPE_F16 1
+#define LLM_DTYPE_BF16 2
+
+/* A cache, described on the host; what it points to is on the device, and the
+ * caller's.  Codes 16-byte aligned; n_pool_pages * n_kv_heads * 16 <= 2^31 - 1. */
+typedef struct llm_kv8_cache {
+    int32_t format;             /* LLM_KV8_*                                      */
+    int32_t n_kv_heads;         /* Hkv, 1..1024                                   */
+    int32_t head_dim;           /* d: 64 or 128                                   */
+    int32_t n_pool_pages;       /* pages in the pools                             */
+    void *k_codes, *v_codes;    /* 8-bit [n_pool_pages][Hkv][16][d]               */
+    float *k_scale, *v_scale;   /* [n_pool_pages][Hkv]                            */
+    const int32_t *page_table;  /* [n_seqs][table_stride], logical -> physical page */
+    int32_t n_seqs;             /* 1..4096                                        */
+    int32_t table_stride;       /* logical pages of a sequence at most, 1..2^27 - 1 */
+} llm_kv8_cache;
+
+/* RMS norm of every query and key head and the rotation to its position, in one
+ * pass ("从头开始手写一个Qwen的Naive CUDA Kernel推理引擎(一)", "RMSNorm", "Rope"):
+ *   y = x / sqrt(mean(x^2) + eps) * gain             (without gains: y = x)
+ *   out[i] = y[i] cos a - y[i + d/2] sin a,  out[i + d/2] = y[i + d/2] cos a + y[i] sin a,
+ *   a = pos * rope_base^(-2i/d),  i < d/2.
+ * q, k: rows of `dtype`, q_stride and k_stride elements apart, with the heads of a
+ * row side by side (so both may lie in the rows of one fused projection); gains:
+ * bf16 [d], both or neither NULL; pos: int32 [n]; q_out [n][Hq][d], k_out
+ * [n][Hkv][d] of the same type, dense (q_out may be q where q_stride is Hq * d, and
+ * k_out k likewise).  Computed in fp32 and rounded once; the angle is reduced in
+ * 64-bit integers, so far positions lose nothing.  Rows 16-byte aligned (pointers
+ * and strides), d in {64, 128}, eps >= 0, rope_base > 0 and finite, n >= 1.       */
+int llm_op_qk_norm_rope(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *q_gain, const void *k_gain, float eps, float rope_base,
+                        const int32_t *pos, int32_t n, int32_t Hq, int32_t Hkv, int32_t d, void *q_out,
+                        void *k_out, void *stream);
+
+/* Quantise rows of K and V into the cache.  k, v: rows of `dtype`, strides in
+ * elements, the Hkv heads of a row side by side, 16-byte aligned (pointers and
+ * strides).  For each page and head that the rows touch, with m = max|x| over its
+ * new rows and s' = m / 127 (int8) or m / 448 (e4m3) in fp32:
+ *   a page that held no token before: scale = s';
+ *   a page that held some: scale = max(scale, s'), and where it grew the codes
+ *   already there become round(code * (old scale / scale));
+ *   new codes = round(x / scale), 0 where scale is 0;
+ * each operation in fp32, round half to even to the code's type, saturating.  A
+ * block that is given a NaN or an infinity has a NaN scale from then on, and all
+ * that is read from it is NaN.  Slots behind a sequence's last token keep their
+ * codes.  Sequences of one call must not share a page that it writes.             */
+int llm_op_kv8_append(const llm_kv8_cache *cache, int32_t dtype, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, const int32_t *row_start, const int32_t *kv_len,
+                      int32_t n_rows, int32_t *err, void *stream);
+
+/* Tokens of the cache back as dense rows: code * scale in fp32, rounded once to
+ * `dtype`.  Rows and strides as for llm_op_kv8_append; rows whose page is out of
+ * range are left as they are.                                                     */
+int llm_op_kv8_read(const llm_kv8_cache *cache, int32_t dtype, const int32_t *row_start,
+                    const int32_t *kv_len, int32_t n_rows, void *k_out, int64_t k_stride, void *v_out,
+                    int64_t v_stride, int32_t *err, void *stream);
+
+/* Bytes of workspace that llm_op_kv8_attention needs with this cache's heads on
+ * the current device; the same for every n_rows, n_seqs and table_stride.          */
+int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32_t n_rows, int64_t *bytes);
+
+/* Causal grouped-query attention over the cache ("FlashQwen", stage 7): the row of
+ * sequence b at position p, query head h with K/V head g = h / (Hq/Hkv):
+ *   out[h] = sum_t softmax_t(q_h . K[g][t] / sqrt(d)) V[g][t]  over t <= p,
+ *   lse[h] = log sum_t exp(q_h . K[g][t] / sqrt(d)).
+ * One row per sequence is a decode step; more are drafted tokens or a prompt.  A
+ * row at a negative position (more rows than kv_len) sees nothing: out 0, lse
+ * -infinity.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
+ * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
+ * 16-byte aligned.  Sums and softmax statistics are held in fp32; with fp32 rows
+ * the products carry 22 bits of q and of the weights, with 16-bit rows q exactly
+ * and 11 bits of the weights at least.  Results do not depend on the run.
+ * Hq % Hkv == 0, Hq/Hkv <= 8.  workspace: device, 256-byte aligned, zero-filled
+ * once before its first use; every call leaves it ready for the next.  Calls that
+ * may run at the same time (two streams, two graphs) need workspaces of their own. */
+int llm_op_kv8_attention(const llm_kv8_cache *cache, int32_t dtype, const void *q, int64_t q_stride,
+                         const int32_t *row_start, const int32_t *kv_len, int32_t n_rows, int32_t Hq,
+                         void *out, float *lse, void *workspace, int64_t workspace_bytes, int32_t *err,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

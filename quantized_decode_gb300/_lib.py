@@ -51,6 +51,21 @@ class llm_weights(ctypes.Structure):
                 ("layers", ctypes.POINTER(llm_layer_weights))]
 
 
+LLM_KV8_INT8 = 1
+LLM_KV8_E4M3 = 2
+LLM_DTYPE_F32 = 0
+LLM_DTYPE_F16 = 1
+LLM_DTYPE_BF16 = 2
+
+
+class llm_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("format", "n_kv_heads", "head_dim", "n_pool_pages")] + \
+               [(n, vp) for n in ("k_codes", "v_codes", "k_scale", "v_scale", "page_table")] + \
+               [("n_seqs", i32), ("table_stride", i32)]
+
+
+_kv8 = ctypes.POINTER(llm_kv8_cache)
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "llm_build_id": (ctypes.c_char_p, []),
@@ -114,6 +129,11 @@ SIGNATURES = {
     "llm_op_dequant_f16": (i32, [i32, vp, vp, i32, i32, vp, vp]),
     "llm_op_gemm_f16": (i32, [vp, vp, i32, i32, i32, vp, vp]),
     "llm_op_gemm_quant": (i32, [i32, vp, vp, vp, i32, i32, i32, vp, vp]),
+    "llm_op_qk_norm_rope": (i32, [i32, vp, i64, vp, i64, vp, vp, f32, f32, vp, i32, i32, i32, i32, vp, vp, vp]),
+    "llm_op_kv8_append": (i32, [_kv8, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp]),
+    "llm_op_kv8_read": (i32, [_kv8, i32, vp, vp, i32, vp, i64, vp, i64, vp, vp]),
+    "llm_op_kv8_attention_workspace": (i32, [_kv8, i32, i32, ctypes.POINTER(i64)]),
+    "llm_op_kv8_attention": (i32, [_kv8, i32, vp, i64, vp, vp, i32, i32, vp, vp, vp, i64, vp, vp]),
 }
 
 _lib = None
