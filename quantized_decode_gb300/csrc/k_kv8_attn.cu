@@ -34,7 +34,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kLeastPages = 16;  // per CTA
 constexpr float kLoScale = 2048.f, kLoInv = 1.f / 2048.f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kShift = 14.f;   // weights are held times 2^14: fp16 keeps those down to 2^-28 normal
+constexpr int kGroupJoin = 8, kMaxJoin = 20;  // partial results joined at once
 
 QD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -53,13 +53,6 @@ QD_DEV void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
     const float2 f = __half22float2(h);
     hi = h2_as_u32(h);
     lo = h2_as_u32(__floats2half2_rn((a - f.x) * kLoScale, (b - f.y) * kLoScale));
-}
-// Product with a zero accumulator.
-QD_DEV void mma16816_z(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Code pairs to fp16 pairs.  int8: b ^ 0x80 = c + 128 under the exponent of 1024, minus 1152.
 template <int FMT>
@@ -116,14 +109,15 @@ QD_DEV void lds_words(const uint8_t *p, uint32_t (&w)[N / 4]) {
 }
 
 // Shared memory of a CTA; the merge buffer lies over the queues, which are empty by then.
-template <int D, int MT, int STAGES>
+template <int D, int MT>
 struct Smem {
-    static constexpr int kPageBytes = 2 * kKv8Page * D;  // K and V codes of one page and head
-    static constexpr int kQueue = kWarps * STAGES * kPageBytes;
+    static constexpr int kPair = 2 * kKv8Page * D;       // K (or V) codes of two pages of one head
+    static constexpr int kQueue = 3 * kPair;             // of a warp: two pairs of K, one of V
     static constexpr int kRows = 8 * MT;
     static constexpr int kMerge = kWarps * kRows * (D + 2) * 4;
+    static constexpr int kWork = kWarps * kQueue > kMerge ? kWarps * kQueue : kMerge;
     static constexpr int kFrag = MT * (D / 16) * 32 * 16;  // A fragments of q
-    static constexpr int kBytes = (kQueue > kMerge ? kQueue : kMerge) + kFrag;
+    static constexpr int kBytes = kWork + kFrag;
 };
 
 // 16 consecutive elements of a q row as floats.
@@ -169,26 +163,26 @@ QD_DEV Kv8Seq attn_seq(const Kv8AttnArgs &a, int b) {
     return s;
 }
 
-template <int D, int FMT, int MT, int STAGES>
+template <int D, int FMT, int MT>
 __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const __grid_constant__ Kv8AttnArgs a) {
-    using S = Smem<D, MT, STAGES>;
+    using S = Smem<D, MT>;
     constexpr int KS = D / 16;      // contraction steps of q . code
     constexpr int NT = D / 8;       // output tiles of 8 dims
     constexpr int KP = D / 64;      // 16-byte pieces of a token's K that a lane holds
     constexpr int VB = D / 8;       // bytes of a token's V that a lane holds (16 or 8)
-    constexpr int R = S::kRows;
-    constexpr int kVAt = 2 * KP * 512;  // V pieces of a queue slot behind the K pieces
+    constexpr int R = S::kRows, Q4 = D / 4;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_fac[R];
-    __shared__ float4 s_page[kWarps][STAGES];  // k scale, v scale, valid
+    __shared__ float4 s_page[kWarps][3][2];  // of a pair's pages: k scale, v scale, physical page or -1 (as bits)
+    __shared__ float2 s_ml[kMaxJoin][R];
     __shared__ int s_last;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs;
-    uint4 *frag = reinterpret_cast<uint4 *>(smem + S::kBytes - S::kFrag);
+    uint4 *frag = reinterpret_cast<uint4 *>(smem + S::kWork);
     float *merge_o = reinterpret_cast<float *>(smem);                                // [kWarps][R][D]
     float2 *merge_ml = reinterpret_cast<float2 *>(smem + (size_t)kWarps * R * D * 4);  // [kWarps][R]
-    uint8_t *queue = smem + (size_t)warp * STAGES * S::kPageBytes;
+    uint8_t *queue = smem + (size_t)warp * S::kQueue;
     const uint32_t queue_at = (uint32_t)__cvta_generic_to_shared(queue);
 
     // ---- the line of pages: its length and its longest segment (every warp for itself)
@@ -250,10 +244,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
         const int seen = max(0, s.kv - s.rows + min((tile * R + R - 1) / G, s.rows - 1) + 1);
         const int pe = min(p1, (seen + kKv8Page - 1) / kKv8Page);
 
-        // ---- this warp's pages: p0 + warp, then every kWarps-th.  Lane i knows page number i of a
-        // batch of 32; the next batch's entries are on their way while a batch is worked on.
+        // ---- this warp's pages: p0 + warp, then every kWarps-th, taken in pairs.  Lane i knows page
+        // number i of a batch of 32; the next batch's entries are on their way while a batch is worked on.
         const int first = p0 + warp;
-        const int n_mine = pe > first ? (pe - first + kWarps - 1) / kWarps : 0;
+        const int n_mine = pe > first ? (pe - first + kWarps - 1) / kWarps : 0, n_pairs = (n_mine + 1) / 2;
         const int32_t *table = a.c.page_table + (int64_t)b * a.c.table_stride;
         auto entry = [&](int j) { return j < n_mine ? __ldg(table + first + j * kWarps) : -1; };
         auto valid = [&](int ph) { return ph >= 0 && ph < a.c.n_pool_pages; };
@@ -261,43 +255,56 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
         int phys = entry(lane), phys_next = entry(32 + lane);
         if (lane < n_mine && !valid(phys)) kv8_report(a.err);
         float ks_l = scale_of(a.c.k_scale, phys), vs_l = scale_of(a.c.v_scale, phys), ks_next = 0.f, vs_next = 0.f;
-        int fetched = 0, fill = 0;  // pages fetched, the stage that the next one goes to
-        auto fetch = [&]() {
-            const int j = fetched++, in_batch = j & 31;
-            if (j < n_mine) {
+        // K of pair i into buffer i % 2, its scales and page numbers into ring place i % 3
+        auto fetch_k = [&](int i) {
+            if (i < n_pairs) {
+                const int in_batch = (2 * i) & 31;
                 if (in_batch == 16) {
                     ks_next = scale_of(a.c.k_scale, phys_next);
                     vs_next = scale_of(a.c.v_scale, phys_next);
                 }
-                if (in_batch == 0 && j > 0) {
+                if (in_batch == 0 && i > 0) {
                     phys = phys_next;
                     ks_l = ks_next;
                     vs_l = vs_next;
-                    if (j + lane < n_mine && !valid(phys)) kv8_report(a.err);
-                    phys_next = entry(j + 32 + lane);
+                    if (2 * i + lane < n_mine && !valid(phys)) kv8_report(a.err);
+                    phys_next = entry(2 * i + 32 + lane);
                 }
-                const int ph = __shfl_sync(kFullMask, phys, in_batch);
-                __syncwarp();  // every lane has read what this stage held
-                if (lane == in_batch) s_page[warp][fill] = make_float4(ks_l, vs_l, valid(phys) ? 1.f : 0.f, 0.f);
-                if (valid(ph)) {
-                    const int64_t at = ((int64_t)ph * Hkv + head) * (kKv8Page * D);
-                    const uint8_t *kp = (const uint8_t *)a.c.k_codes + at + (4 * (g >> 1) + (g & 1)) * D + 16 * c;
-                    const uint8_t *vp = (const uint8_t *)a.c.v_codes + at + 4 * c * D + VB * g;
-                    const uint32_t dst = queue_at + fill * S::kPageBytes;
+                if ((lane & ~1) == in_batch)
+                    s_page[warp][i % 3][lane & 1] = make_float4(ks_l, vs_l, __int_as_float(valid(phys) ? phys : -1), 0.f);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int ph = __shfl_sync(kFullMask, phys, in_batch + x);
+                    if (!valid(ph)) continue;
+                    const uint8_t *kp = (const uint8_t *)a.c.k_codes + ((int64_t)ph * Hkv + head) * (kKv8Page * D) +
+                                        (4 * (g >> 1) + (g & 1)) * D + 16 * c;
+                    const uint32_t dst = queue_at + (i & 1) * S::kPair + x * (kKv8Page * D) + lane * 16;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int i = 0; i < KP; ++i)
-                            cp_async<16>(dst + (t * KP + i) * 512 + lane * 16, kp + 2 * t * D + 64 * i);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) cp_async<VB>(dst + kVAt + r * 32 * VB + lane * VB, vp + r * D);
+                        for (int p = 0; p < KP; ++p) cp_async<16>(dst + (t * KP + p) * 512, kp + 2 * t * D + 64 * p);
                 }
-                if (++fill == STAGES) fill = 0;
             }
             cp_async_commit();
         };
+        auto fetch_v = [&](int i) {  // after a __syncwarp behind fetch_k(i)
+            if (i < n_pairs) {
 #pragma unroll
-        for (int j = 0; j < STAGES - 1; ++j) fetch();
+                for (int x = 0; x < 2; ++x) {
+                    const int ph = __float_as_int(s_page[warp][i % 3][x].z);
+                    if (ph < 0) continue;
+                    const uint8_t *vp = (const uint8_t *)a.c.v_codes + ((int64_t)ph * Hkv + head) * (kKv8Page * D) + 4 * c * D + VB * g;
+                    const uint32_t dst = queue_at + 2 * S::kPair + x * (kKv8Page * D) + lane * VB;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) cp_async<VB>(dst + r * 32 * VB, vp + r * D);
+                }
+            }
+            cp_async_commit();
+        };
+        fetch_k(0);
+        __syncwarp();
+        fetch_v(0);
+        fetch_k(1);
 
         // ---- q of the tile as A fragments: warp t prepares row tile t
         if (warp < MT) {
@@ -330,16 +337,8 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
             if (c == 0) s_fac[warp * 8 + g] = __uint_as_float((uint32_t)(127 + ex) << 23) * kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
         }
         __syncthreads();
-        uint32_t qf[MT == 1 ? KS : 1][4];
-        if (MT == 1) {
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint4 f = frag[k * 32 + lane];
-                qf[k % (MT == 1 ? KS : 1)][0] = f.x; qf[k % (MT == 1 ? KS : 1)][1] = f.y;
-                qf[k % (MT == 1 ? KS : 1)][2] = f.z; qf[k % (MT == 1 ? KS : 1)][3] = f.w;
-            }
-        }
-        float fac[MT], m[MT], l[MT], o[MT][NT][2];
+        // o: the mma's own accumulators, upper and lower rows apart, in units of vref (a power of two)
+        float fac[MT], m[MT], l[MT], o[MT][NT][4], vref = 0.f, vinv = INFINITY;
         int limit[MT], shortest = INT32_MAX;  // tokens that row g of a row tile sees; rows that are not there have q = 0
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -350,95 +349,147 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
             m[t] = -INFINITY;
             l[t] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[t][n][0] = o[t][n][1] = 0.f;
+            for (int n = 0; n < NT; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
         }
         shortest = __reduce_min_sync(kFullMask, shortest);
 
-        // ---- the pages
-        int stage = 0;
+        // ---- pairs of pages
 #pragma unroll 1
-        for (int j = 0; j < n_mine; ++j) {
-            cp_async_wait<STAGES - 2>();
+        for (int i = 0; i < n_pairs; ++i) {
+            cp_async_wait<2>();
             __syncwarp();
-            const float4 pg = s_page[warp][stage];
-            const uint8_t *slot = queue + stage * S::kPageBytes;
-            const int t0 = (first + j * kWarps) * kKv8Page;
-            const bool cut = t0 + kKv8Page > shortest;  // some row does not see all of the page
-            if (pg.z != 0.f) {
-                float sc[MT][4];
+            const uint8_t *kq = queue + (i & 1) * S::kPair + lane * 16, *vq = queue + 2 * S::kPair + lane * VB;
+            float sc[MT][2][4];
 #pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2) {
-                    float acc[MT][4];
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+                for (int x = 0; x < 2; ++x) sc[t][x][0] = sc[t][x][1] = sc[t][x][2] = sc[t][x][3] = 0.f;
+            {
+                float acc[MT][2][2][4];
 #pragma unroll
-                    for (int i = 0; i < KP; ++i) {
-                        uint32_t w[4];
-                        lds_words<16>(slot + (t2 * KP + i) * 512 + lane * 16, w);
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            uint32_t b0, b1;
-                            decode_quad<FMT>(w[x], b0, b1);
-                            if (MT == 1) {
-                                mma16816(acc[0], qf[(4 * i + x) % (MT == 1 ? KS : 1)], b0, b1);
-                            } else {
+                    for (int e = 0; e < 16; ++e) acc[t][e >> 3][(e >> 2) & 1][e & 3] = 0.f;
 #pragma unroll
-                                for (int t = 0; t < MT; ++t) {
-                                    const uint4 f = frag[(t * KS + 4 * i + x) * 32 + lane];
-                                    const uint32_t af[4] = {f.x, f.y, f.z, f.w};
-                                    mma16816(acc[t], af, b0, b1);
-                                }
-                            }
+                for (int p = 0; p < KP; ++p) {
+                    uint32_t w[2][2][4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int t2 = 0; t2 < 2; ++t2) lds_words<16>(kq + x * (kKv8Page * D) + (t2 * KP + p) * 512, w[x][t2]);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t af[MT][4];
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            const uint4 f = frag[(t * KS + 4 * p + y) * 32 + lane];
+                            af[t][0] = f.x; af[t][1] = f.y; af[t][2] = f.z; af[t][3] = f.w;
                         }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int t2 = 0; t2 < 2; ++t2) {
+                                uint32_t b0, b1;
+                                decode_quad<FMT>(w[x][t2][y], b0, b1);
+#pragma unroll
+                                for (int t = 0; t < MT; ++t) mma16816(acc[t][x][t2], af[t], b0, b1);
+                            }
                     }
+                }
+                // the scores of tokens 4 c .. 4 c + 3 of each page
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float ks = s_page[warp][i % 3][x].x;
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
-                        const float k = fac[t] * pg.x;
-                        sc[t][2 * t2] = fmaf(acc[t][2], kLoInv, acc[t][0]) * k;
-                        sc[t][2 * t2 + 1] = fmaf(acc[t][3], kLoInv, acc[t][1]) * k;
+                        const float k = fac[t] * ks;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float(&q)[4] = acc[t][x][e >> 1];
+                            sc[t][x][e] = fmaf(q[2 + (e & 1)], kLoInv, q[e & 1]) * k;
+                        }
                     }
                 }
-                // weights of tokens t0 + 4 c .. + 3
+            }
+            const float4 pg[2] = {s_page[warp][i % 3][0], s_page[warp][i % 3][1]};
+            fetch_k(i + 2);
+
+            // ---- weights.  Tokens that a row does not see, or whose page is not there, have none.
+            const int t0 = (first + 2 * i * kWarps) * kKv8Page, t1 = t0 + kWarps * kKv8Page;
+            const bool ok0 = __float_as_int(pg[0].z) >= 0, ok1 = __float_as_int(pg[1].z) >= 0;
+            const bool cut = t1 + kKv8Page > shortest || !ok0 || !ok1;
+            float alpha[MT];
+            bool same = true;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                if (cut) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (!ok0 || t0 + 4 * c + e >= limit[t]) sc[t][0][e] = -INFINITY;
+                        if (!ok1 || t1 + 4 * c + e >= limit[t]) sc[t][1][e] = -INFINITY;
+                    }
+                }
+                float top = fmaxf(fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][0][2], sc[t][0][3])),
+                                  fmaxf(fmaxf(sc[t][1][0], sc[t][1][1]), fmaxf(sc[t][1][2], sc[t][1][3])));
+                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+                top = fmaxf(fmaxf(top, __shfl_xor_sync(kFullMask, top, 2)), m[t]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                alpha[t] = ex2(m[t] - ref);
+                same = same && m[t] == top;
+                m[t] = top;
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sc[t][x][e] = ex2(sc[t][x][e] - ref);
+                        sum += sc[t][x][e];
+                    }
+                l[t] = fmaf(l[t], alpha[t], sum);
+            }
+            cp_async_wait<1>();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // the page's V scale, relative to vref; vref follows it where they are 2^8 apart
+                const float vs = pg[x].y;
+                const float ratio = vs * vinv;
+                float move = 1.f;
+                if (vs > 0.f && vs < INFINITY && !(ratio <= 256.f && ratio >= 0.00390625f)) {
+                    const int e = min(max((int)(__float_as_uint(vs) >> 23) - 127, -126), 126);
+                    const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vref * 7.8886091e-31f);  // 2^-100
+                    move = vref / to;
+                    vref = to;
+                    vinv = 1.f / to;
+                }
+                if (x == 0 ? !__all_sync(kFullMask, same && move == 1.f) : move != 1.f) {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const float k = x == 0 ? alpha[t] * move : move;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[t][n][e] *= k;
+                    }
+                }
+                const float rel = vs == 0.f ? 0.f : vs * vinv;
                 uint32_t pf[MT][4];
-                float alpha[MT], vs[MT];
-                bool same = true;
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    vs[t] = pg.y;
-                    if (cut) {
+                    float w[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (t0 + 4 * c + k >= limit[t]) sc[t][k] = -INFINITY;
-                        if (t0 >= limit[t]) vs[t] = 0.f;  // a scale that is NaN is not this row's
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = sc[t][x][e] * rel;
+                        // a scale that is NaN is not the business of a row that does not see the token
+                        if (cut && (!(x ? ok1 : ok0) || (x ? t1 : t0) + 4 * c + e >= limit[t])) w[e] = 0.f;
                     }
-                    float top = fmaxf(fmaxf(sc[t][0], sc[t][1]), fmaxf(sc[t][2], sc[t][3]));
-                    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-                    top = fmaxf(fmaxf(top, __shfl_xor_sync(kFullMask, top, 2)), m[t]);
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    alpha[t] = ex2(m[t] - ref);
-                    same = same && m[t] == top;
-                    m[t] = top;
-                    float p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) p[k] = ex2(sc[t][k] - ref + kShift);
-                    l[t] = fmaf(l[t], alpha[t], (p[0] + p[1]) + (p[2] + p[3]));
-                    split2(p[0], p[1], pf[t][0], pf[t][1]);
-                    split2(p[2], p[3], pf[t][2], pf[t][3]);
-                }
-                if (!__all_sync(kFullMask, same)) {
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            o[t][n][0] *= alpha[t];
-                            o[t][n][1] *= alpha[t];
-                        }
+                    split2(w[0], w[1], pf[t][0], pf[t][1]);
+                    split2(w[2], w[3], pf[t][2], pf[t][3]);
                 }
                 uint32_t v[4][VB / 4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    lds_words<VB>(slot + kVAt + r * 32 * VB + lane * VB, v[r]);
-                    if (t0 + kKv8Page > seen && t0 + 4 * c + r >= seen) {  // slots that hold nothing yet
+                    lds_words<VB>(vq + x * (kKv8Page * D) + r * 32 * VB, v[r]);
+                    if (cut && (!(x ? ok1 : ok0) || (x ? t1 : t0) + 4 * c + r >= seen)) {  // slots that hold nothing
 #pragma unroll
                         for (int w = 0; w < VB / 4; ++w) v[r][w] = 0u;
                     }
@@ -448,106 +499,120 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
                     uint32_t b0[4], b1[4];
                     decode_across<FMT>(v[0][w], v[1][w], v[2][w], v[3][w], b0, b1);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int y = 0; y < 4; ++y)
 #pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            float acc[4];
-                            mma16816_z(acc, pf[t], b0[x], b1[x]);
-                            float(&ot)[2] = o[t][4 * w + x];
-                            ot[0] = fmaf(fmaf(acc[2], kLoInv, acc[0]), vs[t], ot[0]);
-                            ot[1] = fmaf(fmaf(acc[3], kLoInv, acc[1]), vs[t], ot[1]);
-                        }
+                        for (int t = 0; t < MT; ++t) mma16816(o[t][4 * w + y], pf[t], b0[y], b1[y]);
                 }
             }
-            if (++stage == STAGES) stage = 0;
-            fetch();
+            __syncwarp();
+            fetch_v(i + 1);
         }
         cp_async_wait<0>();
         __syncthreads();  // the queues are empty: the merge buffer may lie over them
 
-        // ---- the warps' results together
+        // ---- the warps' results together, each divided by its own sum so that none leaves fp32's range
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             l[t] += __shfl_xor_sync(kFullMask, l[t], 1);
             l[t] += __shfl_xor_sync(kFullMask, l[t], 2);
             const int row = t * 8 + g;
+            const float k = l[t] == 0.f ? 0.f : vref / l[t];
             if (c == 0) merge_ml[warp * R + row] = make_float2(m[t], l[t]);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int n = 0; n < NT; n += 4)
                     *reinterpret_cast<float4 *>(merge_o + (size_t)(warp * R + row) * D + (2 * c + h) * VB + n) =
-                        make_float4(o[t][n][h], o[t][n + 1][h], o[t][n + 2][h], o[t][n + 3][h]);
+                        make_float4(fmaf(o[t][n][2 + h], kLoInv, o[t][n][h]) * k, fmaf(o[t][n + 1][2 + h], kLoInv, o[t][n + 1][h]) * k,
+                                    fmaf(o[t][n + 2][2 + h], kLoInv, o[t][n + 2][h]) * k,
+                                    fmaf(o[t][n + 3][2 + h], kLoInv, o[t][n + 3][h]) * k);
         }
         __syncthreads();
 
-        // sums of n partial results of a row, n at most a few hundred, always in the same order
+        // n results of a row, always in the same order; each is an average with the weight l 2^m
         auto joined = [&](int n, auto ml_at, auto o_at, float &top, float &sum) {
             top = -INFINITY;
             for (int i = 0; i < n; ++i) top = fmaxf(top, ml_at(i).x);
             const float ref = top == -INFINITY ? 0.f : top;
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
             sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < n; ++i) {
                 const float2 ml = ml_at(i);
-                const float w = ex2(ml.x - ref);
+                const float w = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - ref);
                 const float4 v = o_at(i);
-                sum = fmaf(ml.y, w, sum);
+                sum += w;
                 r.x = fmaf(v.x, w, r.x);
                 r.y = fmaf(v.y, w, r.y);
                 r.z = fmaf(v.z, w, r.z);
                 r.w = fmaf(v.w, w, r.w);
             }
-            return r;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            return make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
         };
-        auto write_out = [&](int row, int d4, float4 r, float top, float sum) {
+        auto write_out = [&](int row, int d4, const float4 &r, float top, float sum) {
             const int rr = tile * R + row, i = rr / G, h = head * G + rr % G;
             if (i >= s.rows) return;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t at = (int64_t)(s.row0 + i) * a.Hq + h;
-            store_out4(a, at * D + 4 * d4, make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv));
-            if (d4 == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + (log2f(sum) - kShift)) * 0.69314718f;
+            store_out4(a, at * D + 4 * d4, r);
+            if (d4 == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
         };
-        constexpr int Q4 = D / 4;
-        const bool mine = p0 == 0 && p1 == pages;
         constexpr int64_t kPart = (int64_t)R * (D + 2);
-        float *part = a.parts + (2 * (int64_t)blockIdx.x + (p0 > 0 ? 0 : 1)) * kPart;
+        auto part_at = [&](int64_t slot) { return a.parts + slot * kPart; };
+        auto write_part = [&](float *part, int row, int d4, const float4 &r, float top, float sum) {
+            __stcg(reinterpret_cast<float4 *>(part + row * D + 4 * d4), r);
+            if (d4 == 0) __stcg(reinterpret_cast<float2 *>(part + R * D + 2 * row), make_float2(top, sum));
+        };
+        const bool mine = p0 == 0 && p1 == pages;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (p0 > 0 ? 0 : 1);
         for (int e = threadIdx.x; e < R * Q4; e += kThreads) {
             const int row = e / Q4, d4 = e % Q4;
             float top, sum;
             const float4 r = joined(
                 kWarps, [&](int w) { return merge_ml[w * R + row]; },
                 [&](int w) { return *reinterpret_cast<const float4 *>(merge_o + (size_t)(w * R + row) * D + 4 * d4); }, top, sum);
-            if (mine) {
-                write_out(row, d4, r, top, sum);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(part + row * D + 4 * d4), r);
-                if (d4 == 0) __stcg(reinterpret_cast<float2 *>(part + R * D + 2 * row), make_float2(top, sum));
-            }
+            if (mine) write_out(row, d4, r, top, sum);
+            else write_part(part_at(slot), row, d4, r, top, sum);
         }
         if (!mine) {
-            // ---- the CTAs that share the segment; the last to arrive joins their results
+            // ---- the CTAs c0 .. c1 share the segment.  Groups of kGroupJoin of them are joined by
+            // their last to arrive, the groups by the last of those: two short chains instead of one long.
             const int64_t begin = base + (int64_t)seg * pages;
-            const int c0 = (int)(begin / share), c1 = (int)((begin + pages - 1) / share);
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                s_last = atomicAdd(a.counters + c0, 1) == c1 - c0;
+            const int c0 = (int)(begin / share), n = (int)((begin + pages - 1) / share) - c0 + 1;
+            const int per = n <= kMaxJoin ? n : max(kGroupJoin, (n + kMaxJoin - 1) / kMaxJoin);  // <= kMaxJoin, and as many groups
+            auto slot_of = [&](int i) { return 2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0); };
+            auto arrive = [&](int32_t *counter, int of) {  // whether this CTA is the last of `of`
                 __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                auto part_of = [&](int i) { return a.parts + (2 * (int64_t)(c0 + i) + (i == 0 ? 1 : 0)) * kPart; };
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    const int before = atomicAdd(counter, 1);
+                    s_last = before == of - 1;
+                    if (s_last) *counter = 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            // results first, first + step, ... (n of them) to the output or to result `first`
+            auto join = [&](int first, int step, int n, bool final) {
+                for (int e = threadIdx.x; e < n * R; e += kThreads)
+                    s_ml[e / R][e % R] = __ldcg(reinterpret_cast<const float2 *>(part_at(slot_of(first + e / R * step)) + R * D) + e % R);
+                __syncthreads();
                 for (int e = threadIdx.x; e < R * Q4; e += kThreads) {
                     const int row = e / Q4, d4 = e % Q4;
                     float top, sum;
                     const float4 r = joined(
-                        c1 - c0 + 1, [&](int i) { return __ldcg(reinterpret_cast<const float2 *>(part_of(i) + R * D + 2 * row)); },
-                        [&](int i) { return __ldcg(reinterpret_cast<const float4 *>(part_of(i) + row * D + 4 * d4)); }, top, sum);
-                    write_out(row, d4, r, top, sum);
+                        n, [&](int i) { return s_ml[i][row]; },
+                        [&](int i) { return __ldcg(reinterpret_cast<const float4 *>(part_at(slot_of(first + i * step)) + row * D + 4 * d4)); },
+                        top, sum);
+                    if (final) write_out(row, d4, r, top, sum);
+                    else write_part(part_at(slot_of(first)), row, d4, r, top, sum);
                 }
-                if (threadIdx.x == 0) a.counters[c0] = 0;
+            };
+            const int me = (int)blockIdx.x - c0, group = me / per, groups = (n + per - 1) / per;
+            if (arrive(a.counters + slot_of(group * per), min(per, n - group * per))) {
+                join(group * per, 1, min(per, n - group * per), groups == 1);
+                if (groups > 1 && arrive(a.counters + kKv8Counters / 2 + slot_of(0), groups)) join(0, per, groups, true);
             }
         }
         __syncthreads();  // the merge buffer becomes queues again
@@ -555,12 +620,10 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) k_kv8_attend(const 
     }
 }
 
-constexpr int kWorstRows = 32;
-
-template <int D, int FMT, int MT, int STAGES>
+template <int D, int FMT, int MT>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
-    using S = Smem<D, MT, STAGES>;
-    auto kernel = k_kv8_attend<D, FMT, MT, STAGES>;
+    using S = Smem<D, MT>;
+    auto kernel = k_kv8_attend<D, FMT, MT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
     const int G = a.Hq / a.c.n_kv_heads;
@@ -576,20 +639,19 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
 template <int D, int FMT>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
     const int64_t rows = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads);  // of a K/V head, in all sequences
-    if (rows <= (int64_t)8 * a.c.n_seqs) return attend<D, FMT, 1, 3>(s, n_sm, a);
-    if (rows <= (int64_t)16 * a.c.n_seqs) return attend<D, FMT, 2, 6>(s, n_sm, a);
-    return attend<D, FMT, 4, 6>(s, n_sm, a);
+    if (rows <= (int64_t)8 * a.c.n_seqs) return attend<D, FMT, 1>(s, n_sm, a);
+    return attend<D, FMT, 2>(s, n_sm, a);
 }
 
 }  // namespace
 
 int64_t kv8_attention_workspace(int n_sm, int d) {
-    const int64_t slots = 2 * 2 * (int64_t)n_sm * 8, wide = 2 * (int64_t)n_sm * kWorstRows;  // rows of partial results
-    return kKv8Counters * 4 + (slots > wide ? slots : wide) * (d + 2) * 4;
+    // rows of partial results: two places for each CTA, two CTAs of 8 rows or one of 16 on an SM
+    return kKv8Counters * 4 + 2 * 2 * (int64_t)n_sm * 8 * (d + 2) * 4;
 }
 
 cudaError_t launch_kv8_attention(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
-    if (2 * n_sm > kKv8Counters) return cudaErrorInvalidConfiguration;
+    if (4 * n_sm > kKv8Counters / 2 || 2 * n_sm > kMaxJoin * kMaxJoin) return cudaErrorInvalidConfiguration;
     if (a.c.format == LLM_KV8_INT8)
         return a.c.head_dim == 128 ? attend<128, LLM_KV8_INT8>(s, n_sm, a) : attend<64, LLM_KV8_INT8>(s, n_sm, a);
     return a.c.head_dim == 128 ? attend<128, LLM_KV8_E4M3>(s, n_sm, a) : attend<64, LLM_KV8_E4M3>(s, n_sm, a);

@@ -44,12 +44,13 @@ struct Kv8AttnArgs {
 };
 
 constexpr int kKv8MaxGqa = 8;
-constexpr int kKv8Counters = 2048;  // >= CTAs of any attention launch
+constexpr int kKv8Counters = 4096;  // two for each of the two places that a CTA of the largest launch has
 
 cudaError_t launch_qk_norm_rope(cudaStream_t s, int dtype, int d, const RopeArgs &a);
 cudaError_t launch_kv8_append(cudaStream_t s, int dtype, const Kv8RowsArgs &a);
 cudaError_t launch_kv8_read(cudaStream_t s, int dtype, const Kv8RowsArgs &a);
 int64_t kv8_attention_workspace(int n_sm, int d);
 cudaError_t launch_kv8_attention(cudaStream_t s, int n_sm, const Kv8AttnArgs &a);
+cudaError_t launch_kv8_prompt(cudaStream_t s, const Kv8AttnArgs &a);
 
 }  // namespace qd
