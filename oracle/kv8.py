@@ -94,11 +94,12 @@ def read(cache, table, row_start, kv_len, rows):
 
 
 def attention(cache, table, row_start, kv_len, q):
-    """q: [rows][Hq][d] -> out, lse, and per (row, head) the two sums that bounds on the error are made of:
-    the weighted sum of |V| (same shape as out) and the largest sum of |q_i k_i| / sqrt(d) over the keys."""
+    """q: [rows][Hq][d] -> out, lse, and per (row, head) the sums that bounds on the error are made of: the
+    weighted sum of |V| and the plain sum of |V| (same shape as out), and the largest sum of |q_i k_i| / sqrt(d)
+    over the keys."""
     rows, Hq, d = q.shape
     Hkv = cache["k"].shape[1]
-    out, absv = np.zeros((rows, Hq, d)), np.zeros((rows, Hq, d))
+    out, absv, sumv = (np.zeros((rows, Hq, d)) for _ in range(3))
     lse, absqk = np.full((rows, Hq), -np.inf), np.zeros((rows, Hq))
     for b, row0, n, kv in sequences(row_start, kv_len):
         pages = table[b, :-(-kv // PAGE)]
@@ -119,8 +120,9 @@ def attention(cache, table, row_start, kv_len, q):
                     w /= w.sum()
                     out[row0 + i, h] = w @ V[:seen]
                     absv[row0 + i, h] = w @ np.abs(V[:seen])
+                    sumv[row0 + i, h] = np.abs(V[:seen]).sum(0)
                     absqk[row0 + i, h] = (np.abs(K[:seen]) @ np.abs(x)).max() / np.sqrt(d)
-    return out, lse, absv, absqk
+    return out, lse, absv, sumv, absqk
 
 
 def norm_rope(x, gain, eps, base, pos):

@@ -50,6 +50,7 @@ cudaError_t launch_qk_norm_rope(cudaStream_t s, int dtype, int d, const RopeArgs
 cudaError_t launch_kv8_append(cudaStream_t s, int dtype, const Kv8RowsArgs &a);
 cudaError_t launch_kv8_read(cudaStream_t s, int dtype, const Kv8RowsArgs &a);
 int64_t kv8_attention_workspace(int n_sm, int d);
+bool kv8_few_rows(const Kv8AttnArgs &a);  // launch_kv8_attention, or launch_kv8_prompt
 cudaError_t launch_kv8_attention(cudaStream_t s, int n_sm, const Kv8AttnArgs &a);
 cudaError_t launch_kv8_prompt(cudaStream_t s, const Kv8AttnArgs &a);
 
