@@ -33,7 +33,7 @@ namespace {
 template <int D, int NT, bool HL>
 struct Cfg {
     static constexpr int kWarps = NT > 1 ? 8 : (HL ? 12 : 16), kThreads = kWarps * 32, kRows = 8 * NT;
-    static constexpr int kLeast = 2 * kWarps;   // pages of a part at least
+    static constexpr int kLeast = 2 * kWarps;   // pages of a part at least (for 4096 tokens of 4 heads: once 13.4 us, twice 12.8, four times 14.8)
     static constexpr int kRow = D + 4;          // floats of a row in the merge buffer
     static constexpr int kMerge = kWarps * kRows * kRow * 4;
     static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * (HL ? 16 : 8);  // B fragments of q
@@ -68,29 +68,33 @@ QD_DEV void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = h2_as_u32(h);
     lo = h2_as_u32(__floats2half2_rn(a - f.x, b - f.y));
 }
-// Four consecutive codes to the fp16 pairs (0, 1) and (2, 3).  int8: b ^ 0x80 = c + 128 under the exponent
-// of 1024, minus 1152.
+// Code pairs to fp16 pairs.  int8: b ^ 0x80 = c + 128 under the exponent of 1024, minus 1152.  The pairs are those
+// that one mask takes out of a word (bytes 0 and 2, and after a shift 1 and 3): for K that only permutes the
+// contraction.  (The shift as a multiplication, off the busier integer pipe, measured slower: 114 us for 107.)
+QD_DEV uint32_t codes_to_f16(uint32_t w) {  // bytes 0 and 2
+    return h2_as_u32(__hsub2(u32_as_h2(lop3_and_xor(w, 0x00ff00ffu, 0x64806480u)), __floats2half2_rn(1152.f, 1152.f)));
+}
+QD_DEV void e4m3_to_f16(uint32_t w, uint32_t &p01, uint32_t &p23) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(p01), "=r"(p23)
+        : "r"(w));
+}
+// Four consecutive codes to two pairs: of bytes (0, 2) and (1, 3) for int8, (0, 1) and (2, 3) for e4m3.
 template <int FMT>
-QD_DEV void decode_quad(uint32_t w, uint32_t &p01, uint32_t &p23) {
+QD_DEV void decode_quad(uint32_t w, uint32_t &pa, uint32_t &pb) {
     if (FMT == LLM_KV8_INT8) {
-        const uint32_t x = w ^ 0x80808080u;
-        const __half2 k = __floats2half2_rn(1152.f, 1152.f);
-        p01 = h2_as_u32(__hsub2(u32_as_h2(prmt(x, 0x64646464u, 0x4140u)), k));
-        p23 = h2_as_u32(__hsub2(u32_as_h2(prmt(x, 0x64646464u, 0x4342u)), k));
+        pa = codes_to_f16(w);
+        pb = codes_to_f16(w >> 8);
     } else {
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(p01), "=r"(p23)
-            : "r"(w));
+        e4m3_to_f16(w, pa, pb);
     }
 }
 // Bytes j of two words (two tokens) to the fp16 pairs of dims j = 0 .. 3.
 template <int FMT>
 QD_DEV void decode_across(uint32_t w0, uint32_t w1, uint32_t (&p)[4]) {
     if (FMT == LLM_KV8_INT8) {
-        const __half2 k = __floats2half2_rn(1152.f, 1152.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            p[j] = h2_as_u32(__hsub2(u32_as_h2(lop3_and_xor(prmt(w0, w1, (uint32_t)(j | (4 + j) << 8)), 0x00ff00ffu, 0x64806480u)), k));
+        decode_quad<FMT>(prmt(w0, w1, 0x5410u), p[0], p[1]);
+        decode_quad<FMT>(prmt(w0, w1, 0x7632u), p[2], p[3]);
     } else {
         decode_quad<FMT>(prmt(w0, w1, 0x5140u), p[0], p[1]);
         decode_quad<FMT>(prmt(w0, w1, 0x7362u), p[2], p[3]);
@@ -109,27 +113,28 @@ QD_DEV void load_codes(const uint8_t *p, uint32_t (&w)[N / 4]) {
     }
 }
 
-// 16 consecutive elements of a q row as floats.
-QD_DEV void load_q16(const Kv8AttnArgs &a, int64_t at, float (&v)[16]) {
-    if (a.dtype == LLM_DTYPE_F32) {
-        const uint4 *p = reinterpret_cast<const uint4 *>((const float *)a.q + at);
+// A lane's share of a q row as loaded, 16 consecutive elements for each 64 dims, and those as floats.
+template <int D, bool HL>
+struct QRaw {
+    uint4 v[D / 64][HL ? 4 : 2];
+};
+QD_DEV void unpack16(int, const uint4 (&u)[4], float (&v)[16]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float f[4];
-            RowType<float>::unpack(__ldg(p + i), f);
+    for (int i = 0; i < 4; ++i) {
+        float f[4];
+        RowType<float>::unpack(u[i], f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * i + e] = f[e];
-        }
-    } else {
-        const uint4 *p = reinterpret_cast<const uint4 *>((const uint16_t *)a.q + at);
+        for (int e = 0; e < 4; ++e) v[4 * i + e] = f[e];
+    }
+}
+QD_DEV void unpack16(int dtype, const uint4 (&u)[2], float (&v)[16]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float f[8];
-            if (a.dtype == LLM_DTYPE_F16) RowType<__half>::unpack(__ldg(p + i), f);
-            else RowType<__nv_bfloat16>::unpack(__ldg(p + i), f);
+    for (int i = 0; i < 2; ++i) {
+        float f[8];
+        if (dtype == LLM_DTYPE_F16) RowType<__half>::unpack(u[i], f);
+        else RowType<__nv_bfloat16>::unpack(u[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[8 * i + e] = f[e];
-        }
+        for (int e = 0; e < 8; ++e) v[8 * i + e] = f[e];
     }
 }
 // Four consecutive output elements.
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
     constexpr int NB = HL ? 2 : 1;  // Bs of a product
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_fac[R];
-    __shared__ float2 s_ml[kWarps > kMaxJoin ? kWarps : kMaxJoin][R];
+    __shared__ float2 s_ml[kWarps][R];
     __shared__ int s_last;
     float *merge_o = reinterpret_cast<float *>(smem);                    // [kWarps][R][kRow]
     uint32_t *frag = reinterpret_cast<uint32_t *>(smem + C::kMerge);     // [NT][D / 16][NB][2][32]: only for NT > 1
@@ -284,7 +289,54 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             return ph < a.c.n_pool_pages ? max(ph, -1) : -1;
         };
         auto scale_of = [&](const float *pool, int ph) { return ph >= 0 ? __ldg(pool + (int64_t)ph * Hkv + head) : 0.f; };
-        int phys = checked(entry(lane)), phys_next = entry(32 + lane);
+        int phys = entry(lane), phys_next = entry(32 + lane);
+
+        // ---- q as B fragments: lane (g, c) has row g's dims 64 i + 16 c + 4 y .. + 3 for step 4 i + y, in decode_quad's pairs
+        uint32_t qf[NT == 1 ? D / 16 : 1][NB][2];
+        auto read_q = [&](int t) {
+            QRaw<D, HL> raw;
+            const int r = tile * R + 8 * t + g, i = r / G;
+            constexpr int kSize = HL ? 4 : 2;  // bytes of an element, and 16-byte pieces of 16
+            const uint8_t *at = (const uint8_t *)a.q + ((int64_t)(s.row0 + i) * a.q_stride + (int64_t)(head * G + r % G) * D + 16 * c) * kSize;
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+#pragma unroll
+                for (int x = 0; x < kSize; ++x) {
+                    raw.v[p][x] = make_uint4(0, 0, 0, 0);
+                    if (8 * t + g < n_live) raw.v[p][x] = __ldg(reinterpret_cast<const uint4 *>(at + 64 * p * kSize) + x);
+                }
+            return raw;
+        };
+        auto prepare_q = [&](const QRaw<D, HL> &raw, auto put) {
+            float v[KP][16], top = 0.f;
+#pragma unroll
+            for (int p = 0; p < KP; ++p) {
+                unpack16(a.dtype, raw.v[p], v[p]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[p][e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127 - 12, -125), 125);
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t hi, lo;
+                        constexpr bool kApart = FMT == LLM_KV8_INT8;  // the pairs of decode_quad
+                        split2(v[p][4 * y + (kApart ? z : 2 * z)] * down, v[p][4 * y + (kApart ? z + 2 : 2 * z + 1)] * down, hi, lo);
+                        put(4 * p + y, 0, z, hi);
+                        if (HL) put(4 * p + y, 1, z, lo);
+                    }
+            // q . code to a base-2 score: 2^e log2(e) / sqrt(d)
+            return __uint_as_float((uint32_t)(127 + ex) << 23) * kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
+        };
+        const QRaw<D, HL> raw = read_q(NT == 1 ? 0 : warp);  // on its way while the pages are looked up
+
+        phys = checked(phys);
         uint32_t kw[2][KP][4], vw[4][VB / 4];
         const int64_t head_at = (int64_t)head * (kKv8Page * D), page_step = (int64_t)Hkv * (kKv8Page * D);
         const uint8_t *k_at = (const uint8_t *)a.c.k_codes + head_at + g * D + 16 * c;
@@ -303,6 +355,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
 #pragma unroll
             for (int r = 0; r < 4; ++r) load_codes<VB>(p + ((r & 1) + 8 * (r >> 1)) * D, vw[r]);
         };
+        // a page's 128-byte lines, one for each lane, into L2
+        const bool ahead_v = lane >= D / 8;
+        const uint8_t *ahead_at = (const uint8_t *)(ahead_v ? a.c.v_codes : a.c.k_codes) + head_at + (lane - (ahead_v ? D / 8 : 0)) * 128;
+        auto ahead = [&](int ph) {
+            if (ph >= 0 && lane < D / 4) prefetch_l2(ahead_at + ph * page_step);
+        };
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -314,49 +372,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
         int ph = __shfl_sync(kFullMask, phys, 0);
         load_k(ph);
         load_v(ph);
+        ahead(__shfl_sync(kFullMask, phys, 1));
         float ks_l = scale_of(a.c.k_scale, phys), vs_l = scale_of(a.c.v_scale, phys), ks_next = 0.f, vs_next = 0.f;
 
-        // ---- q as B fragments: lane (g, c) has row g's dims 64 i + 16 c + 4 y + {0, 1 | 2, 3} for step 4 i + y
-        uint32_t qf[NT == 1 ? D / 16 : 1][NB][2];
-        auto prepare_q = [&](int t, auto put) {
-            const int r = tile * R + 8 * t + g, i = r / G;
-            float v[KP][16], top = 0.f;
-#pragma unroll
-            for (int p = 0; p < KP; ++p) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[p][e] = 0.f;
-                if (8 * t + g < n_live)
-                    load_q16(a, (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(head * G + r % G) * D + 64 * p + 16 * c, v[p]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(v[p][e]));
-            }
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127 - 12, -125), 125);
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-            for (int p = 0; p < KP; ++p)
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        uint32_t hi, lo;
-                        split2(v[p][4 * y + 2 * z] * down, v[p][4 * y + 2 * z + 1] * down, hi, lo);
-                        put(4 * p + y, 0, z, hi);
-                        if (HL) put(4 * p + y, 1, z, lo);
-                    }
-            // q . code to a base-2 score: 2^e log2(e) / sqrt(d)
-            return __uint_as_float((uint32_t)(127 + ex) << 23) * kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
-        };
         float fac[NT][2], m[NT][2], l[NT][2], o[NT][OT][4];
         int limit[NT][2], shortest = INT32_MAX;  // tokens that rows 2 c, 2 c + 1 of a tile see; those not there have q = 0
         if (NT == 1) {
-            const float f = prepare_q(0, [&](int k, int x, int z, uint32_t w) { qf[k % (NT == 1 ? D / 16 : 1)][x][z] = w; });
+            const float f = prepare_q(raw, [&](int k, int x, int z, uint32_t w) { qf[k % (NT == 1 ? D / 16 : 1)][x][z] = w; });
             fac[0][0] = __shfl_sync(kFullMask, f, 8 * c);
             fac[0][1] = __shfl_sync(kFullMask, f, 8 * c + 4);
         } else {
             if (warp < nt) {
-                const float f = prepare_q(warp, [&](int k, int x, int z, uint32_t w) { frag[(((warp * (D / 16) + k) * NB + x) * 2 + z) * 32 + lane] = w; });
+                const float f = prepare_q(raw, [&](int k, int x, int z, uint32_t w) { frag[(((warp * (D / 16) + k) * NB + x) * 2 + z) * 32 + lane] = w; });
                 if (c == 0) s_fac[warp * 8 + g] = f;
             }
             __syncthreads();
@@ -398,6 +425,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                 phys_next = entry(j + 33 + lane);
             }
             ph = __shfl_sync(kFullMask, phys, (at + 1) & 31);
+            const int ph2 = __shfl_sync(kFullMask, phys, (at + 2) & 31);
+            if (at < 30 || at == 31) ahead(ph2);
             // ---- scores of tokens g, g + 8 and rows 2 c, 2 c + 1
             float acc[NT][NB][4];
 #pragma unroll
@@ -546,22 +575,35 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             }
         }
         __syncthreads();
-        auto joined = [&](int n, auto ml_at, auto o_at, float &top, float &sum) {  // always in the same order
+        // n partial results of an element, 8 at a time, always in the same order
+        auto joined = [&](int n, auto ml_at, auto o_at, float &top, float &sum) {
             top = -INFINITY;
-            for (int i = 0; i < n; ++i) top = fmaxf(top, ml_at(i).x);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
             sum = 0.f;
-#pragma unroll 8
-            for (int i = 0; i < n; ++i) {
-                const float2 ml = ml_at(i);
-                const float w = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - ref);
-                const float4 v = o_at(i);
-                sum += w;
-                r.x = fmaf(v.x, w, r.x);
-                r.y = fmaf(v.y, w, r.y);
-                r.z = fmaf(v.z, w, r.z);
-                r.w = fmaf(v.w, w, r.w);
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float2 ml[8];
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ml[i] = i0 + i < n ? ml_at(i0 + i) : make_float2(-INFINITY, 0.f);
+                    v[i] = i0 + i < n ? o_at(i0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                float to = top;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to = fmaxf(to, ml[i].x);
+                const float ref = to == -INFINITY ? 0.f : to, k = ex2(top - ref);
+                top = to;
+                sum *= k;
+                r = make_float4(r.x * k, r.y * k, r.z * k, r.w * k);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float w = ml[i].y == 0.f ? 0.f : ml[i].y * ex2(ml[i].x - ref);
+                    sum += w;
+                    r.x = fmaf(v[i].x, w, r.x);
+                    r.y = fmaf(v[i].y, w, r.y);
+                    r.z = fmaf(v[i].z, w, r.z);
+                    r.w = fmaf(v[i].w, w, r.w);
+                }
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             return make_float4(r.x * inv, r.y * inv, r.z * inv, r.w * inv);
@@ -576,6 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
         // of this segment's part k: places of one tile's parts are `tiles` apart, as its items are
         auto place_of = [&](int k) { return place + (head * parts + k) * tiles + tile; };
         auto part_at = [&](int k) { return a.parts + (int64_t)place_of(k) * kPart; };
+        auto group_at = [&](int k) { return a.parts + (int64_t)(a.places + place_of(k)) * kPart; };  // from part k on
         auto write_part = [&](float *to, int row, int d4, const float4 &r, float top, float sum) {
             __stcg(reinterpret_cast<float4 *>(to + row * D + 4 * d4), r);
             if (d4 == 0) __stcg(reinterpret_cast<float2 *>(to + R * D + 2 * row), make_float2(top, sum));
@@ -605,28 +648,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                 __syncthreads();
                 return s_last != 0;
             };
-            // parts k0, k0 + step, ... (n of them) to the output or to part k0's place
-            auto join = [&](int k0, int step, int n, bool final) {
-                const float *from = part_at(k0);
+            // results k0, k0 + step, ... (n of them) to the output or to the group's place
+            auto join = [&](const float *from, int k0, int step, int n, bool final) {
                 const int64_t stride = (int64_t)step * tiles * kPart;
-                for (int e = threadIdx.x; e < n * n_live; e += kThreads) {
-                    const int i = e / n_live, row = e - i * n_live;
-                    s_ml[i][row] = __ldcg(reinterpret_cast<const float2 *>(from + i * stride + R * D) + row);
-                }
-                __syncthreads();
                 for (int e = threadIdx.x; e < n_live * Q4; e += kThreads) {
                     const int row = e / Q4, d4 = e % Q4;
                     float top, sum;
                     const float4 r = joined(
-                        n, [&](int i) { return s_ml[i][row]; },
+                        n, [&](int i) { return __ldcg(reinterpret_cast<const float2 *>(from + i * stride + R * D) + row); },
                         [&](int i) { return __ldcg(reinterpret_cast<const float4 *>(from + i * stride + row * D + 4 * d4)); }, top, sum);
                     if (final) write_out(row, d4, r, top, sum);
-                    else write_part(part_at(k0), row, d4, r, top, sum);
+                    else write_part(group_at(k0), row, d4, r, top, sum);
                 }
             };
             if (arrive(a.counters + place_of(group * per), n)) {
-                join(group * per, 1, n, groups == 1);
-                if (groups > 1 && arrive(a.counters + kKv8Counters / 2 + place_of(0), groups)) join(0, per, groups, true);
+                join(part_at(group * per), group * per, 1, n, groups == 1);
+                if (groups > 1 && arrive(a.counters + kKv8Counters / 2 + place_of(0), groups)) join(group_at(0), 0, per, groups, true);
             }
         }
         __syncthreads();  // the merge buffer is free again
@@ -656,8 +693,8 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
 
 int64_t kv8_attention_workspace(int n_sm, int d) {
     // a segment cut into c >= 2 parts has more than (c - 1) share pages, so there are at most two parts for each
-    // CTA's share, each with a place of up to 32 rows
-    return kKv8Counters * 4 + 2 * (int64_t)n_sm * 32 * (d + 2) * 4;
+    // CTA's share, each with a place of up to 32 rows, and another for its group
+    return kKv8Counters * 4 + 2 * 2 * (int64_t)n_sm * 32 * (d + 2) * 4;
 }
 
 bool kv8_few_rows(const Kv8AttnArgs &a) {

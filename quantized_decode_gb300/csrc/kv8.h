@@ -40,6 +40,7 @@ struct Kv8AttnArgs {
     float *lse;
     int32_t *counters;  // kKv8Counters, zero between calls
     float *parts;       // partial results behind them
+    int places;         // of parts; as many for groups of them follow
     int32_t *err;
 };
 
