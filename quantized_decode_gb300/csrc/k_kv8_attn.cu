@@ -40,7 +40,6 @@ struct Cfg {
     static constexpr int kBytes = kMerge + kQ;
 };
 constexpr int kGroupJoin = 8, kMaxJoin = 20;  // partial results joined at once
-constexpr float kLog2e = 1.4426950408889634f;
 // weights are exp2(s - m) rel 2^kLift, s <= m + kLag, rel <= kWindow: at most 2^15
 constexpr float kLag = 4.f, kLift = 7.f, kWindow = 16.f;
 
@@ -54,11 +53,6 @@ QD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_
 QD_DEV uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-QD_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // a, b -> fp16 pair and the fp16 pair of the remainders
@@ -148,13 +142,6 @@ QD_DEV void store_out4(const Kv8AttnArgs &a, int64_t at, const float4 &v) {
         *reinterpret_cast<uint2 *>((uint16_t *)a.out + at) =
             make_uint2(RowType<__nv_bfloat16>::two(v.x, v.y), RowType<__nv_bfloat16>::two(v.z, v.w));
     }
-}
-
-// A sequence as the attention takes it: one whose length is out of range sees nothing.
-QD_DEV Kv8Seq attn_seq(const Kv8AttnArgs &a, int b) {
-    Kv8Seq s = kv8_seq(__ldg(a.row_start + b), __ldg(a.row_start + b + 1), __ldg(a.kv_len + b), a.n_rows, a.c.table_stride);
-    if (s.kv < 0 || (int64_t)s.kv > (int64_t)a.c.table_stride * kKv8Page) s.kv = 0;
-    return s;
 }
 
 QD_DEV int parts_of(int pages, int share) { return (int)((unsigned)(pages + share - 1) / (unsigned)share); }

@@ -114,4 +114,19 @@ QD_DEV int kv8_find_seq(const int32_t *row_start, int n_seqs, int64_t item) {
     return lo;
 }
 
+// ---- attention
+constexpr float kLog2e = 1.4426950408889634f;
+QD_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A sequence as the attention takes it: one whose length is out of range sees nothing.
+QD_DEV Kv8Seq attn_seq(const Kv8AttnArgs &a, int b) {
+    Kv8Seq s = kv8_seq(__ldg(a.row_start + b), __ldg(a.row_start + b + 1), __ldg(a.kv_len + b), a.n_rows, a.c.table_stride);
+    if (s.kv < 0 || (int64_t)s.kv > (int64_t)a.c.table_stride * kKv8Page) s.kv = 0;
+    return s;
+}
+
 }  // namespace qd

@@ -1,0 +1,314 @@
+// kv8_tc.cuh - parts of the tcgen05 attention over the 8-bit cache: codes on their way by TMA, their fp16
+// form in shared memory, the split of V's scales, TMEM accesses and the MN-major operand descriptor.
+//
+// A block is 128 tokens, 8 pages.  Its K and its V lie in shared memory as [token][dim] fp16 rows in panels
+// of 64 dims (128-byte rows, 128-byte swizzle): K is the K-major B operand of the scores, V the MN-major B
+// operand of the output.
+#pragma once
+
+#include "kv8.cuh"
+#include "ptx.cuh"
+
+namespace qd {
+
+constexpr int kTile = 128;             // rows of an MMA tile, and tokens of a block
+constexpr int kBlockPages = kTile / kKv8Page;
+constexpr int kPanel = kTile * 128;    // bytes of 128 rows of 64 fp16
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+// Wait for the phase of `parity`, kWaitNs at most.  The timer is looked at once in a while only: reading
+// it takes longer than a hand-over between two warps.
+QD_DEV bool tc_wait(uint64_t *bar, uint32_t parity) {
+    if (ptx::mbar_test(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (ptx::mbar_test(bar, parity)) return true;
+        if ((i & 1023u) == 0) {
+            const uint64_t t = ptx::gtimer();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kWaitNs) return false;
+        }
+    }
+}
+// 16 consecutive 32-bit TMEM columns of the warp's lanes from registers (no wait)
+QD_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+QD_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 64 consecutive fp32 columns of the warp's lanes.  The wait names the registers, so that no use moves above it.
+QD_DEV void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t r[64];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+                 "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+                   "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+                   "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+                   "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+                   "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+                 :
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Two fp32 operations in one instruction.
+QD_DEV float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+QD_DEV float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// columns taddr .. + n - 1 (n a multiple of 32) of the warp's lanes times a factor of each lane
+QD_DEV void tmem_scale(uint32_t taddr, int n, float k) {
+#pragma unroll 1
+    for (int i = 0; i < n; i += 32) {
+        float v[32];
+        ptx::tmem_ld32(taddr + i, v);
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+            uint32_t w[16];
+#pragma unroll
+            for (int z = 0; z < 16; ++z) w[z] = __float_as_uint(v[e + z] * k);
+            tmem_st16(taddr + i + e, w);
+        }
+    }
+}
+
+// Descriptor of an MN-major operand in a block's rows: 8-token groups 1024 bytes apart (SBO), 64-dim
+// panels kPanel apart (LBO).  A step of 16 tokens is 2048 bytes.
+QD_DEV uint64_t desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(kPanel >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kIdescBMn = 1u << 16;  // instruction descriptor: B is MN-major
+
+// Sixteen codes (four words) to fp16 times 2^-k (h2 holds 2^-k twice), as two 16-byte chunks.
+template <int FMT>
+QD_DEV void codes_f16(const uint4 &u, __half2 h2, bool scaled, uint4 &lo, uint4 &hi) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t o[8];
+    if (FMT == LLM_KV8_INT8) {
+        // b ^ 0x80 = c + 128 under the exponent of 1024; (1152 + c) h - 1152 h is exact
+        const __half2 off = __hmul2(h2, __floats2half2_rn(-1152.f, -1152.f));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = w[i] ^ 0x80808080u;
+            o[2 * i] = h2_as_u32(__hfma2(u32_as_h2(prmt(x, 0x64646464u, 0x4140u)), h2, off));
+            o[2 * i + 1] = h2_as_u32(__hfma2(u32_as_h2(prmt(x, 0x64646464u, 0x4342u)), h2, off));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+                : "r"(w[i]));
+        if (scaled) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = h2_as_u32(__hmul2(u32_as_h2(o[i]), h2));
+        }
+    }
+    lo = make_uint4(o[0], o[1], o[2], o[3]);
+    hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// What the softmax has to know of a block's pages.  V's scale is split: vs / vref = r 2^-k; 2^-k goes into
+// V's fp16 values (exact for k <= 15), log2 r into the exponent of the weights, and a page's share of their sum
+// is divided by r again.
+constexpr int kRecs = 8;
+struct BlockRec {
+    float ks[kBlockPages], lr[kBlockPages], ir[kBlockPages], mul[kBlockPages];  // K scale, log2 r, 1 / r, 2^-k
+    float move, vref;  // factor of the output when vref changed with this block; vref
+    uint32_t ok;       // pages that are there
+    uint32_t scaled;   // some mul is not 1
+};
+
+// The split of a block's V scales against vref, which all lanes keep alike; lane p % 8 holds page p.
+// vref is a power of two that follows the scales where they leave [2^-14, 2^6] of it.
+struct VSplit {
+    float r, mul, move;  // mul = 2^-k, 0 for a scale of 0
+};
+QD_DEV VSplit split_scale(float vs, float &vref) {
+    VSplit o;
+    float top = vs > 0.f && vs < INFINITY ? vs : 0.f;
+#pragma unroll
+    for (int i = 1; i < kBlockPages; i <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, i));
+    o.move = 1.f;
+    if (top > 0.f && (vref == 0.f || top > vref * 64.f || top < vref * 6.1035156e-05f)) {  // 2^-14
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
+        const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vref * 8.6736174e-19f);  // 2^-60
+        o.move = vref == 0.f ? 1.f : vref / to;
+        vref = to;
+    }
+    o.r = vs == 0.f ? 1.f : vs / vref;
+    o.mul = vs == 0.f ? 0.f : 1.f;
+    if (o.r < 1.f) {
+        const int k = min(127 - (int)(__float_as_uint(o.r) >> 23), 15);
+        o.mul = __uint_as_float((uint32_t)(127 - k) << 23);
+        o.r *= __uint_as_float((uint32_t)(127 + k) << 23);
+    }
+    return o;
+}
+
+// ---- codes on their way: a ring of UNITS places in shared memory, each the K or the V codes of a block of one
+// head ([page][16][D] bytes).  Copies are the TMA engine's, so many are in flight without registers.
+template <int UNITS>
+struct CodeRing {
+    uint64_t full[UNITS], empty[UNITS], rec_full[kRecs];
+    BlockRec rec[kRecs];
+    QD_DEV void init(int converters) {
+        for (int i = 0; i < UNITS; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], converters);
+        }
+        for (int i = 0; i < kRecs; ++i) ptx::mbar_init(&rec_full[i], 1);
+    }
+};
+QD_DEV void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(ptx::smem_u32(bar))
+                 : "memory");
+}
+
+// One warp: the copies and records of the nb blocks from `table` on (the first block's entries), n_done blocks
+// after the ring's first.  `left`: tokens from there on that any row sees.  `wait(bar, phase)`: by the whole warp, false
+// once something timed out.  issued: units whose copies were started, since the ring's first.
+template <int D, int UNITS, typename Wait>
+QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int nb, int left, int n_done, CodeRing<UNITS> &ring,
+                       uint8_t *units, int &issued, Wait wait) {
+    constexpr uint32_t kPage = kKv8Page * D, kUnit = kBlockPages * kPage;
+    const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads;
+    // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
+    auto entry = [&](int j) {
+        const int p = j * kBlockPages + (lane & 7);
+        return j < nb && p * kKv8Page < left ? max(-1, __ldg(table + p)) : -2;
+    };
+    auto checked = [&](int ph) {
+        if (ph != -1 && ph < a.c.n_pool_pages) return ph;
+        if (lane < kBlockPages) kv8_report(a.err);
+        return -1;
+    };
+    auto scale_of = [&](const float *pool, int ph) { return ph >= 0 ? __ldg(pool + (int64_t)ph * Hkv + head) : 0.f; };
+    int ph = checked(entry(0)), ph_next = entry(1);
+    float ks = scale_of(a.c.k_scale, ph), vs = scale_of(a.c.v_scale, ph), vref = 0.f;
+    for (int j = 0; j < nb; ++j) {
+        const int n = n_done + j;
+        const uint32_t ok = __ballot_sync(kFullMask, ph >= 0) & 0xffu;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t u = 2 * (uint32_t)n + x, place = u % UNITS, use = u / UNITS;
+            if (use > 0 && !wait(&ring.empty[place], use - 1)) return;
+            if (lane == 0) ptx::mbar_expect_tx(&ring.full[place], kPage * __popc(ok));
+            __syncwarp();
+            issued = (int)u + 1;
+            if (lane < kBlockPages && ph >= 0)
+                bulk_load(ptx::smem_u32(units) + place * kUnit + lane * kPage,
+                          (const uint8_t *)(x ? a.c.v_codes : a.c.k_codes) + ((int64_t)ph * Hkv + head) * kPage, kPage, &ring.full[place]);
+        }
+        const int next = checked(ph_next);
+        ph_next = entry(j + 2);
+        const float ks_next = scale_of(a.c.k_scale, next), vs_next = scale_of(a.c.v_scale, next);
+        // The unit waited for above held block n - 3 at the latest in both kernels' rings, so the softmax is
+        // done with block n - kRecs
+        const VSplit v = split_scale(vs, vref);
+        BlockRec &rec = ring.rec[n % kRecs];
+        if (lane < kBlockPages) {
+            rec.ks[lane] = ks;
+            rec.lr[lane] = log2f(v.r);
+            rec.ir[lane] = 1.f / v.r;
+            rec.mul[lane] = v.mul;
+        }
+        const bool scaled = __any_sync(kFullMask, v.mul != 1.f && ph >= 0);
+        if (lane == 0) {
+            rec.move = v.move;
+            rec.vref = vref;
+            rec.ok = ok;
+            rec.scaled = scaled;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ring.rec_full[n % kRecs]);
+        ph = next;
+        ks = ks_next;
+        vs = vs_next;
+    }
+}
+
+// NT threads turn a block's codes into fp16 rows.  Piece i of a thread is 16 dims of one token; a warp reads 512
+// consecutive bytes.
+template <int D, int NT>
+struct Pieces {
+    static constexpr int kCount = kTile * D / 16 / NT;   // pieces of a thread
+    static constexpr int kRun = NT / D;                  // pages that a step of the threads covers
+    static_assert(kRun >= 1 && kRun * kCount == kBlockPages, "every piece of a block once");
+    int tid;
+    QD_DEV int page(int i) const { return kRun * i + tid / D; }
+    QD_DEV int in_page() const { return tid % D; }       // 16-byte piece of the page
+    QD_DEV int row() const { return in_page() / (D / 16); }
+    QD_DEV int dim() const { return 16 * (in_page() % (D / 16)); }
+
+    // left: tokens of the block that are there; whatever lies in the slots behind them, and in pages that are not
+    // there, becomes 0
+    template <int FMT>
+    QD_DEV void convert(const uint8_t *unit, uint8_t *dst, const BlockRec &rec, bool is_v, int left, uint64_t *empty) const {
+        const int lane = threadIdx.x & 31, c = (dim() >> 3) & 7;
+        // eight lanes write a row: those of the second panel the other chunk first, on other banks
+        const bool swap = dim() >= 64, scaled = is_v && rec.scaled != 0, whole = left >= kTile && rec.ok == 0xffu;
+        uint4 w[kCount];
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) w[i] = *reinterpret_cast<const uint4 *>(unit + (kRun * i * D + tid) * 16);
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i)
+                if (!((rec.ok >> page(i)) & 1u) || page(i) * kKv8Page + row() >= left) w[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            uint4 c0, c1;
+            codes_f16<FMT>(w[i], __float2half2_rn(scaled ? rec.mul[page(i)] : 1.f), scaled, c0, c1);
+            const int r = page(i) * kKv8Page + row();
+            uint8_t *p = dst + (dim() >> 6) * kPanel + r * 128;
+            *reinterpret_cast<uint4 *>(p + (((c + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? c1 : c0;
+            *reinterpret_cast<uint4 *>(p + (((c + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? c0 : c1;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty);  // the codes have been read
+    }
+};
+
+}  // namespace qd
