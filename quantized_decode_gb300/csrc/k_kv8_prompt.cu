@@ -23,7 +23,14 @@
 // into the same accumulator.
 #include "kv8_tc.cuh"
 
+#ifndef MAXU
+#define MAXU 1
+#endif
+#ifndef WU
+#define WU 1
+#endif
 namespace qd {
+constexpr int kMaxU = MAXU, kWU = WU;
 
 namespace {
 
@@ -68,15 +75,15 @@ QD_DEV void load_q8(const Kv8AttnArgs &a, int64_t at, bool live, float (&v)[8]) 
     }
 }
 
-// Weights are exp2(s - m) 2^kLift r with s <= m + kLag and r <= 2^6: at most 2^15.  Rows of 16 bits lag far
+// Weights are exp2(s - m) 2^kLift r with s <= m + kLag and r <= 2^4: at most 2^15.  Rows of 16 bits lag far
 // and rarely rescale; those of fp32 lift the weights instead, so that the second fp16 half keeps its 11 bits
-// down to 2^-22 of the largest (fp16 has no normal numbers below 2^-14).
+// down to 2^-21 of the largest (fp16 has no normal numbers below 2^-14).
 template <int HL>
 struct Weights {
-    static constexpr float kLag = HL == 2 ? 1.f : 8.f, kLift = HL == 2 ? 8.f : 1.f;
+    static constexpr float kLag = HL == 2 ? 4.f : 8.f, kLift = HL == 2 ? 7.f : 3.f;
 };
 
-// One row's softmax of a block, by each lane of a warp: scores at s_at in TMEM, weights in their place, m and l
+// One row's softmax of a block in two passes, by each lane of a warp: scores at s_at in TMEM, weights in their place, m and l
 // brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on (counted from
 // the block's first), and pages that are not there, have no weight.
 template <int D, int HL, bool CUT>
@@ -90,14 +97,15 @@ QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, flo
             if (e >= vis) x[e] = -INFINITY;
     };
     float most = -INFINITY;
+#pragma unroll kMaxU
+    for (int c = 0; c < 4; ++c) {  // two pages
+        float x[32];
+        ptx::tmem_ld32(s_at + 32 * c, x);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float x[64];
-        tmem_ld64(s_at + 64 * half, x);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            float *y = x + p * kKv8Page;
-            hide(y, 4 * half + p);
+        for (int z = 0; z < 2; ++z) {
+            const int p = 2 * c + z;
+            float *y = x + z * kKv8Page;
+            hide(y, p);
             float a = fmaxf(y[0], y[1]), b = fmaxf(y[2], y[3]);  // three operands to an instruction
 #pragma unroll
             for (int e = 4; e < kKv8Page; e += 4) {
@@ -105,7 +113,7 @@ QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, flo
                 b = fmaxf(fmaxf(b, y[e + 2]), y[e + 3]);
             }
             a = fmaxf(a, b);
-            most = fmaxf(most, CUT && a == -INFINITY ? a : a * (fac * rec.ks[4 * half + p]));
+            most = fmaxf(most, CUT && a == -INFINITY ? a : a * (fac * rec.ks[p]));
         }
     }
     const bool grow = most > m + kLag || (m == -INFINITY && most > m);
@@ -118,8 +126,8 @@ QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, flo
     }
     const float ref = (m == -INFINITY ? 0.f : m) - kLift;
     uint32_t lo[HL == 2 ? 4 : 1][16];  // remainders wait until the scores in their place have been read
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {  // two pages
+#pragma unroll(HL == 2 ? 4 : kWU)
+    for (int c = 0; c < 4; ++c) {
         float x[32];
         ptx::tmem_ld32(s_at + 32 * c, x);
         uint32_t hi[16];
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         const int64_t rr = r0 + t * kTile + r;
         const int tok = (int)min(rr / G, (int64_t)INT32_MAX), h = head * G + (int)(rr % G);
         const bool live = t < nt && rr < (int64_t)s.rows * G;
-        const int limit = live ? max(0, s.kv - s.rows + tok + 1) : 0;
+        const int limit = live ? max(0, s.kv - s.rows + tok + 1) : INT32_MAX;  // rows that are not there: q of 0
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
         if (t < nt && nb > 0) {
             // ---- q: the row's largest element to [2^12, 2^13), fp16 (and the remainder) into the swizzled rows
@@ -368,23 +376,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             // ================= MMA =================
             const uint32_t id_s = umma_idesc_f16_f32(kTile, kTile);
             const uint32_t id_o = umma_idesc_f16_f32(kTile, D) | kIdescBMn;
+            const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
             auto scores = [&](int t, int st) {
-#pragma unroll 1
-                for (int x = 0; x < HL; ++x)
+                const uint32_t d = s_at(t), qd = q_at + t * (C::kQ >> 4), kd = k_at + st * (C::kKv >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32);
-                        umma_f16(s_at(t), umma_desc_sw128(smem_u32(sq) + t * C::kQ + x * C::kP * kPanel + at),
-                                 umma_desc_sw128(smem_u32(sk) + st * C::kKv + at), id_s, (x | kk) != 0 ? 1u : 0u);
-                    }
+                for (int kk = 0; kk < HL * D / 16; ++kk) {
+                    const uint32_t at = (uint32_t)((kk % (D / 16) >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                    const uint32_t x = (uint32_t)(kk / (D / 16) * C::kP * kPanel) >> 4;
+                    if (kk == 0) mma_ss<false>(d, qd, kd, id_s);
+                    else mma_ss<true>(d, qd + x + at, kd + at, id_s);
+                }
             };
             auto weigh = [&](int t, int st, bool more) {
-#pragma unroll 1
-                for (int x = 0; x < HL; ++x)
+                const uint32_t d = o_at(t), p = s_at(t), vd = v_at + st * (C::kKv >> 4);
+                if (more) mma_ts<true>(d, p, vd, id_o);
+                else mma_ts<false>(d, p, vd, id_o);
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_f16_ts(o_at(t), s_at(t) + x * 64 + kk * 8, desc_mn(smem_u32(sv) + st * C::kKv + kk * 2048), id_o,
-                                    (more || (x | kk) != 0) ? 1u : 0u);
+                for (int kk = 1; kk < HL * kTile / 16; ++kk)
+                    mma_ts<true>(d, p + (kk >> 3) * 64 + (kk & 7) * 8, vd + (kk & 7) * (2048 >> 4), id_o);
             };
             bool go = wait(&b.q_full, 0) && wait(&b.k_full[0], 0);
             if (go) {

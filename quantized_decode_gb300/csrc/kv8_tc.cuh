@@ -72,6 +72,22 @@ QD_DEV void tmem_ld64(uint32_t taddr, float (&v)[64]) {
     for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 columns, in two steps: the values are there once tmem_ld16_wait has passed, which names the registers so that no
+// use moves above it.
+QD_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+QD_DEV void tmem_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // Two fp32 operations in one instruction.
 QD_DEV float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -105,16 +121,30 @@ QD_DEV void tmem_scale(uint32_t taddr, int n, float k) {
     }
 }
 
-// Descriptor of an MN-major operand in a block's rows: 8-token groups 1024 bytes apart (SBO), 64-dim
-// panels kPanel apart (LBO).  A step of 16 tokens is 2048 bytes.
-QD_DEV uint64_t desc_mn(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(kPanel >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Descriptors of the operands in such rows, as two words: the high one is the same for both (8-row or 8-token groups
+// 1024 bytes apart, version 1, 128-byte swizzle), the low one the address in 16-byte units and for the MN-major
+// form the distance of two 64-dim panels.  A step of 16 dims of a K-major operand is 32 bytes, of 16 tokens of the
+// MN-major one 2048.
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+QD_DEV uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | 1u << 16; }
+QD_DEV uint32_t desc_mn(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (uint32_t)(kPanel >> 4) << 16; }
+// D (+)= A B with A from shared or tensor memory; the descriptors' low words.  The thread that issues shares its
+// scheduler with busy warps, so an MMA costs it few instructions.
+template <bool ADD>
+QD_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "n"(ADD ? 1 : 0)
+        : "memory");
+}
+template <bool ADD>
+QD_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %4};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(kDescHi), "n"(ADD ? 1 : 0)
+        : "memory");
 }
 constexpr uint32_t kIdescBMn = 1u << 16;  // instruction descriptor: B is MN-major
 
@@ -159,7 +189,7 @@ struct BlockRec {
 };
 
 // The split of a block's V scales against vref, which all lanes keep alike; lane p % 8 holds page p.
-// vref is a power of two that follows the scales where they leave [2^-14, 2^6] of it.
+// vref is a power of two that follows the scales where they leave [2^-14, 2^4] of it.
 struct VSplit {
     float r, mul, move;  // mul = 2^-k, 0 for a scale of 0
 };
@@ -169,7 +199,7 @@ QD_DEV VSplit split_scale(float vs, float &vref) {
 #pragma unroll
     for (int i = 1; i < kBlockPages; i <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, i));
     o.move = 1.f;
-    if (top > 0.f && (vref == 0.f || top > vref * 64.f || top < vref * 6.1035156e-05f)) {  // 2^-14
+    if (top > 0.f && (vref == 0.f || top > vref * 16.f || top < vref * 6.1035156e-05f)) {  // 2^-14
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
         const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vref * 8.6736174e-19f);  // 2^-60
         o.move = vref == 0.f ? 1.f : vref / to;
@@ -291,6 +321,8 @@ struct Pieces {
         uint4 w[kCount];
 #pragma unroll
         for (int i = 0; i < kCount; ++i) w[i] = *reinterpret_cast<const uint4 *>(unit + (kRun * i * D + tid) * 16);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(empty);  // the codes have been read: the next block's may come
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < kCount; ++i)
@@ -307,7 +339,6 @@ struct Pieces {
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty);  // the codes have been read
     }
 };
 
