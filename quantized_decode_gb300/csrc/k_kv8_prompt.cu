@@ -3,14 +3,14 @@
 //
 // A CTA takes 256 (row, query head) pairs of one K/V head as two tiles of 128 and goes through the
 // keys in blocks of 128 tokens (8 pages):
-//   warps 0-3, 4-7   softmax of tile 0 and of tile 1: a thread owns a row (a TMEM lane), reads its 128
-//                    scores, keeps the running maximum and sum, writes the fp16 weights back over the
-//                    scores in TMEM, where they are the A operand of the second product
-//   warps 8-15       codes -> fp16 in shared memory, once for both tiles: K and V both as [token][dim] rows with
+//   warps 0-15       softmax, eight for each tile: two threads own a row (a TMEM lane), each 64 of its scores;
+//                    they agree on the maximum, keep sums of their own and write the fp16 weights back over
+//                    their scores in TMEM, where they are the A operand of the second product
+//   warps 16-23      codes -> fp16 in shared memory, once for both tiles: K and V both as [token][dim] rows with
 //                    the 128-byte swizzle, K the K-major and V the MN-major B operand
-//   warp 16          issues the MMAs (one thread) and owns the 512 TMEM columns: two score
+//   warp 24          issues the MMAs (one thread) and owns the 512 TMEM columns: two score
 //                    tiles and two outputs of 128 columns each
-//   warp 17          copies the next block's codes (TMA) and prepares its scales
+//   warp 25          copies the next block's codes (TMA) and prepares its scales
 // While one tile's softmax runs, the tensor cores work for the other: for each block they do
 // O += P V (t, j) and S = Q K (t, j + 1), tile after tile, in order, so the next scores may take the
 // place of weights that are still read by the product issued before.
@@ -23,18 +23,11 @@
 // into the same accumulator.
 #include "kv8_tc.cuh"
 
-#ifndef MAXU
-#define MAXU 1
-#endif
-#ifndef WU
-#define WU 1
-#endif
 namespace qd {
-constexpr int kMaxU = MAXU, kWU = WU;
 
 namespace {
 
-constexpr int kThreads = 640, kConvert = 8;
+constexpr int kThreads = 896, kSoftmax = 16, kConvert = 8;  // warps of each kind
 constexpr int kUnits = 2;              // of codes: the next block's K and V
 constexpr int kQExp = 12;              // q is scaled so that a row's largest element is in [2^12, 2^13)
 
@@ -44,13 +37,14 @@ struct Cfg {
     static constexpr int kStages = HL == 2 ? 1 : 2;      // of K and of V
     static constexpr int kQ = HL * kP * kPanel;          // bytes of a tile of q
     static constexpr int kKv = kP * kPanel;
-    static constexpr int kBytes = 1024 + 2 * kQ + 2 * kStages * kKv + kUnits * kTile * D;
+    static constexpr int kTiles = 2 * kQ + 2 * kStages * kKv + kUnits * kTile * D;
 };
 
 struct Bars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done;
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], agree[2][4], done;
     CodeRing<kUnits> codes;
     uint32_t tmem;
+    float half[2][2][kTile];  // by tile and half: what the two threads of a row tell each other
     int abort;
 };
 
@@ -83,29 +77,31 @@ struct Weights {
     static constexpr float kLag = HL == 2 ? 4.f : 8.f, kLift = HL == 2 ? 7.f : 3.f;
 };
 
-// One row's softmax of a block in two passes, by each lane of a warp: scores at s_at in TMEM, weights in their place, m and l
-// brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on (counted from
-// the block's first), and pages that are not there, have no weight.
-template <int D, int HL, bool CUT>
-QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, float fac, int limit, float vmove, bool have_o, float &m, float &l) {
+// Half a row's softmax of a block, by each lane of a warp: 64 scores at s_at in TMEM (pages p0 .. p0 + 3), weights in
+// their place (remainders 32 columns behind), m and l brought up to date, this half of the output at o_at rescaled
+// where that is due.  agree(x): the larger of both halves' x.  CUT: tokens from `limit` on (counted from the
+// half's first), and pages that are not there, have no weight.  The loops are not unrolled: warps at different
+// work share an instruction cache, and longer code measured slower.
+template <int D, int HL, bool CUT, typename Agree>
+QD_DEV void block_weights(const BlockRec &rec, int p0, uint32_t s_at, uint32_t o_at, float fac, int limit, float vmove, bool have_o, float &m,
+                          float &l, Agree agree) {
     constexpr float kLag = Weights<HL>::kLag, kLift = Weights<HL>::kLift;
-    auto hide = [&](float *x, int p) {  // of page p
+    auto hide = [&](float *x, int p) {  // of the half's page p
         if (!CUT) return;
-        const int vis = (rec.ok >> p) & 1u ? limit - p * kKv8Page : 0;
+        const int vis = (rec.ok >> (p0 + p)) & 1u ? limit - p * kKv8Page : 0;
 #pragma unroll
         for (int e = 0; e < kKv8Page; ++e)
             if (e >= vis) x[e] = -INFINITY;
     };
     float most = -INFINITY;
-#pragma unroll kMaxU
-    for (int c = 0; c < 4; ++c) {  // two pages
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {  // two pages
         float x[32];
         ptx::tmem_ld32(s_at + 32 * c, x);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            const int p = 2 * c + z;
             float *y = x + z * kKv8Page;
-            hide(y, p);
+            hide(y, 2 * c + z);
             float a = fmaxf(y[0], y[1]), b = fmaxf(y[2], y[3]);  // three operands to an instruction
 #pragma unroll
             for (int e = 4; e < kKv8Page; e += 4) {
@@ -113,28 +109,29 @@ QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, flo
                 b = fmaxf(fmaxf(b, y[e + 2]), y[e + 3]);
             }
             a = fmaxf(a, b);
-            most = fmaxf(most, CUT && a == -INFINITY ? a : a * (fac * rec.ks[p]));
+            most = fmaxf(most, CUT && a == -INFINITY ? a : a * (fac * rec.ks[p0 + 2 * c + z]));
         }
     }
+    most = agree(most);
     const bool grow = most > m + kLag || (m == -INFINITY && most > m);
     if (__any_sync(kFullMask, grow) || vmove != 1.f) {
         const float to = grow ? most : m;
         const float k = m == to ? 1.f : ex2(m - to);
         m = to;
         l *= k;
-        if (have_o) tmem_scale(o_at, D, k * vmove);
+        if (have_o) tmem_scale(o_at, D / 2, k * vmove);
     }
     const float ref = (m == -INFINITY ? 0.f : m) - kLift;
-    uint32_t lo[HL == 2 ? 4 : 1][16];  // remainders wait until the scores in their place have been read
-#pragma unroll(HL == 2 ? 4 : kWU)
-    for (int c = 0; c < 4; ++c) {
+    uint32_t lo[2][16];  // remainders wait until the scores in their place have been read
+#pragma unroll(HL == 2 ? 2 : 1)
+    for (int c = 0; c < 2; ++c) {
         float x[32];
         ptx::tmem_ld32(s_at + 32 * c, x);
         uint32_t hi[16];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const int p = 2 * c + y;
-            hide(x + 16 * y, p);
+            const int p = p0 + 2 * c + y;
+            hide(x + 16 * y, 2 * c + y);
             const float kf = fac * rec.ks[p], off = rec.lr[p] - ref;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -160,14 +157,9 @@ QD_DEV void block_weights(const BlockRec &rec, uint32_t s_at, uint32_t o_at, flo
             if (!(CUT && s == 0.f)) l = fmaf(s, rec.ir[p], l);
         }
         tmem_st16(s_at + 16 * c, hi);
-        // remainders of c go to columns 64 + 16 c: scores of pages 4, 5 (c < 2) and 6, 7
-        if (HL == 2 && c == 2) {
-            tmem_st16(s_at + 64, lo[0]);
-            tmem_st16(s_at + 80, lo[HL == 2 ? 1 : 0]);
-        }
-        if (HL == 2 && c == 3) {
-            tmem_st16(s_at + 96, lo[HL == 2 ? 2 : 0]);
-            tmem_st16(s_at + 112, lo[HL == 2 ? 3 : 0]);
+        if (HL == 2 && c == 1) {
+            tmem_st16(s_at + 32, lo[0]);
+            tmem_st16(s_at + 48, lo[1]);
         }
     }
 }
@@ -177,10 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     using namespace ptx;
     using C = Cfg<D, HL>;
     constexpr float kLift = Weights<HL>::kLift;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ Bars b;
-    uint8_t *sq = base, *sk = base + 2 * C::kQ, *sv = sk + C::kStages * C::kKv, *units = sv + C::kStages * C::kKv;
+    extern __shared__ __align__(1024) uint8_t smem[];  // nothing else is shared: no byte of the 227 KB to spare for padding
+    Bars &b = *reinterpret_cast<Bars *>(smem + C::kTiles);
+    uint8_t *sq = smem, *sk = smem + 2 * C::kQ, *sv = sk + C::kStages * C::kKv, *units = sv + C::kStages * C::kKv;
     volatile int *abort = &b.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv;
@@ -213,22 +204,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     const int nb = (seen + kTile - 1) / kTile;
 
     if (threadIdx.x == 0) {
-        mbar_init(&b.q_full, nt * 4);
+        mbar_init(&b.q_full, nt * 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.k_full[i], kConvert);
             mbar_init(&b.k_empty[i], 1);
             mbar_init(&b.v_full[i], kConvert);
             mbar_init(&b.v_empty[i], 1);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_full[i], 4);
+            mbar_init(&b.p_full[i], 8);
             mbar_init(&b.o_full[i], 1);
+            for (int q = 0; q < 4; ++q) mbar_init(&b.agree[i][q], 2);
         }
         b.codes.init(kConvert);
         mbar_init(&b.done, 1);
         b.abort = 0;
         mbar_fence_init();
     }
-    if (warp == 16) tmem_alloc(&b.tmem, 512);
+    if (warp == 24) tmem_alloc(&b.tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -246,12 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         }
         return true;
     };
+    if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
     auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
 
-    if (warp < 8) {
+    if (warp < kSoftmax) {
         // ================= softmax =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-        const int t = warp >> 2, q = warp & 3, r = 32 * q + lane;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+        const int t = warp >> 3, half = (warp >> 2) & 1, q = warp & 3, r = 32 * q + lane;
         const int64_t rr = r0 + t * kTile + r;
         const int tok = (int)min(rr / G, (int64_t)INT32_MAX), h = head * G + (int)(rr % G);
         const bool live = t < nt && rr < (int64_t)s.rows * G;
@@ -261,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             // ---- q: the row's largest element to [2^12, 2^13), fp16 (and the remainder) into the swizzled rows
             float top = 0.f;
             const int64_t at = (int64_t)(s.row0 + tok) * a.q_stride + (int64_t)h * D;
-#pragma unroll 4
+#pragma unroll 2
             for (int c = 0; c < D / 8; ++c) {
                 float v[8];
                 load_q8(a, at + 8 * c, live, v);
@@ -271,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127 - kQExp, -125), 125);
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
             const float fac = __uint_as_float((uint32_t)(127 + ex) << 23) * kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
+#pragma unroll 2
+            for (int c = half * (D / 16); c < (half + 1) * (D / 16); ++c) {
                 float v[8];
                 load_q8(a, at + 8 * c, live, v);
                 uint32_t hi[4], lo[4];
@@ -296,6 +289,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             bool fine = true;
             // a warp whose rows all see a block whole has nothing to mask
             const int shortest = __reduce_min_sync(kFullMask, limit);
+            auto other = [&](float x, int j) {  // what the row's other thread brings to its j-th call
+                b.half[t][half][r] = x;  // block j - 1's has been read: all weights of that block have arrived
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.agree[t][q]);
+                fine = wait_warp(&b.agree[t][q], (uint32_t)j) && fine;
+                return b.half[t][half ^ 1][r];
+            };
             for (int j = 0; j < nb && fine; ++j) {
                 const BlockRec &rec = b.codes.rec[j % kRecs];
                 fine = wait_warp(&b.codes.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)j);
@@ -304,8 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 const bool cut = (j + 1) * kTile > shortest || rec.ok != 0xffu;
                 const float vmove = rec.move;
                 vref = rec.vref;
-                if (cut) block_weights<D, HL, true>(rec, s_at(t) + lanes, o_at(t) + lanes, fac, limit - j * kTile, vmove, j > 0, m, l);
-                else block_weights<D, HL, false>(rec, s_at(t) + lanes, o_at(t) + lanes, fac, 0, vmove, j > 0, m, l);
+                auto agree = [&](float x) { return fmaxf(x, other(x, j)); };
+                const uint32_t sh = s_at(t) + lanes + 64 * half, oh = o_at(t) + lanes + half * (D / 2);
+                if (cut) block_weights<D, HL, true>(rec, 4 * half, sh, oh, fac, limit - j * kTile - 64 * half, vmove, j > 0, m, l, agree);
+                else block_weights<D, HL, false>(rec, 4 * half, sh, oh, fac, 0, vmove, j > 0, m, l, agree);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -314,11 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             // ---- output
             fine = fine && wait_warp(&b.o_full[t], 0);
             tc_fence_after();
+            if (fine) l += other(l, nb);
             if (fine) {
                 const float k = l == 0.f ? 0.f : vref / l;
                 const int64_t out = ((int64_t)(s.row0 + tok) * a.Hq + h) * D;
 #pragma unroll 1
-                for (int i = 0; i < D / 32; ++i) {
+                for (int i = half * (D / 64); i < (half + 1) * (D / 64); ++i) {
                     float v[32];
                     tmem_ld32(o_at(t) + lanes + 32 * i, v);
                     if (live) {
@@ -338,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                         }
                     }
                 }
-                if (live && a.lse) a.lse[(int64_t)(s.row0 + tok) * a.Hq + h] = l == 0.f ? -INFINITY : (m + (log2f(l) - kLift)) * 0.69314718f;
+                if (live && half == 0 && a.lse) a.lse[(int64_t)(s.row0 + tok) * a.Hq + h] = l == 0.f ? -INFINITY : (m + (log2f(l) - kLift)) * 0.69314718f;
             }
-        } else if (live) {  // no key at all
+        } else if (live && half == 0) {  // no key at all
             const int64_t out = ((int64_t)(s.row0 + tok) * a.Hq + h) * D;
             for (int i = 0; i < D; i += 8) {
                 const uint4 z = make_uint4(0, 0, 0, 0);
@@ -353,10 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             }
             if (a.lse) a.lse[(int64_t)(s.row0 + tok) * a.Hq + h] = -INFINITY;
         }
-    } else if (warp < 8 + kConvert) {
+    } else if (warp < kSoftmax + kConvert) {
         // ================= codes -> fp16 =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        const Pieces<D, kConvert * 32> pieces{(int)threadIdx.x - 256};
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const Pieces<D, kConvert * 32> pieces{(int)threadIdx.x - kSoftmax * 32};
         for (int j = 0; j < nb; ++j) {
             const int st = j % C::kStages, left = seen - j * kTile;
             const uint32_t use = (uint32_t)(j / C::kStages);
@@ -371,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             if (lane == 0) mbar_arrive(&b.v_full[st]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 16 && lane == 0 && nb > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 24 && lane == 0 && nb > 0) {
             // ================= MMA =================
             const uint32_t id_s = umma_idesc_f16_f32(kTile, kTile);
             const uint32_t id_o = umma_idesc_f16_f32(kTile, D) | kIdescBMn;
@@ -392,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 if (more) mma_ts<true>(d, p, vd, id_o);
                 else mma_ts<false>(d, p, vd, id_o);
 #pragma unroll
-                for (int kk = 1; kk < HL * kTile / 16; ++kk)
-                    mma_ts<true>(d, p + (kk >> 3) * 64 + (kk & 7) * 8, vd + (kk & 7) * (2048 >> 4), id_o);
+                for (int kk = 1; kk < HL * kTile / 16; ++kk)  // weights of 64 tokens, their remainders, the other 64, theirs
+                    mma_ts<true>(d, p + (kk >> 2 & 1) * 64 + (kk >> 3) * 32 + (kk & 3) * 8, vd + (kk & 7) * (2048 >> 4), id_o);
             };
             bool go = wait(&b.q_full, 0) && wait(&b.k_full[0], 0);
             if (go) {
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             umma_commit(&b.done);  // arrives once every MMA issued above has completed
             if (!tc_wait(&b.done, 0)) fail();
         }
-        if (warp == 17) {
+        if (warp == 25) {
             // ================= copies =================
             int issued = 0;
             feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride, head, nb, seen, 0, b.codes, units, issued, wait_warp);
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 24) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }
@@ -452,12 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
 template <int D, int FMT, int HL>
 cudaError_t prompt(cudaStream_t s, const Kv8AttnArgs &a) {
     auto kernel = k_kv8_prompt<D, FMT, HL>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, HL>::kBytes);
+    constexpr int kBytes = Cfg<D, HL>::kTiles + (int)sizeof(Bars);
+    static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     const int G = a.Hq / a.c.n_kv_heads;
     const int64_t items = (int64_t)a.n_rows * G / (2 * kTile) + a.c.n_seqs, grid = items * a.c.n_kv_heads;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    kernel<<<(unsigned)grid, kThreads, Cfg<D, HL>::kBytes, s>>>(a);
+    kernel<<<(unsigned)grid, kThreads, kBytes, s>>>(a);
     return cudaGetLastError();
 }
 template <int D, int FMT>

@@ -180,7 +180,7 @@ QD_DEV void codes_f16(const uint4 &u, __half2 h2, bool scaled, uint4 &lo, uint4 
 // What the softmax has to know of a block's pages.  V's scale is split: vs / vref = r 2^-k; 2^-k goes into
 // V's fp16 values (exact for k <= 15), log2 r into the exponent of the weights, and a page's share of their sum
 // is divided by r again.
-constexpr int kRecs = 8;
+constexpr int kRecs = 4;
 struct BlockRec {
     float ks[kBlockPages], lr[kBlockPages], ir[kBlockPages], mul[kBlockPages];  // K scale, log2 r, 1 / r, 2^-k
     float move, vref;  // factor of the output when vref changed with this block; vref
@@ -259,22 +259,24 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
     for (int j = 0; j < nb; ++j) {
         const int n = n_done + j;
         const uint32_t ok = __ballot_sync(kFullMask, ph >= 0) & 0xffu;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        auto copy = [&](int x) {  // K or V of block n
             const uint32_t u = 2 * (uint32_t)n + x, place = u % UNITS, use = u / UNITS;
-            if (use > 0 && !wait(&ring.empty[place], use - 1)) return;
+            if (use > 0 && !wait(&ring.empty[place], use - 1)) return false;
             if (lane == 0) ptx::mbar_expect_tx(&ring.full[place], kPage * __popc(ok));
             __syncwarp();
             issued = (int)u + 1;
             if (lane < kBlockPages && ph >= 0)
                 bulk_load(ptx::smem_u32(units) + place * kUnit + lane * kPage,
                           (const uint8_t *)(x ? a.c.v_codes : a.c.k_codes) + ((int64_t)ph * Hkv + head) * kPage, kPage, &ring.full[place]);
-        }
+            return true;
+        };
+        if (!copy(0)) return;
         const int next = checked(ph_next);
         ph_next = entry(j + 2);
         const float ks_next = scale_of(a.c.k_scale, next), vs_next = scale_of(a.c.v_scale, next);
-        // The unit waited for above held block n - 3 at the latest in both kernels' rings, so the softmax is
-        // done with block n - kRecs
+        // The unit of K waited for above held block n - 1 (UNITS is 2): its converters had waited for the scores of block
+        // n - 3 at the latest, those for the weights of n - 4, so nobody reads the record of n - kRecs any more
+        static_assert(UNITS == 2 && kRecs == 4, "the argument above");
         const VSplit v = split_scale(vs, vref);
         BlockRec &rec = ring.rec[n % kRecs];
         if (lane < kBlockPages) {
@@ -292,6 +294,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ring.rec_full[n % kRecs]);
+        if (!copy(1)) return;
         ph = next;
         ks = ks_next;
         vs = vs_next;
@@ -321,8 +324,11 @@ struct Pieces {
         uint4 w[kCount];
 #pragma unroll
         for (int i = 0; i < kCount; ++i) w[i] = *reinterpret_cast<const uint4 *>(unit + (kRun * i * D + tid) * 16);
+        // The next block's codes may come as soon as these have been read: the fence keeps the reads before the copies
+        // that follow the arrival (without it they were overtaken).
+        ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(empty);  // the codes have been read: the next block's may come
+        if (lane == 0) ptx::mbar_arrive(empty);
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < kCount; ++i)
