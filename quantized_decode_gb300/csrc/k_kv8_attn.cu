@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             for (int w = 0; w < OT; ++w) o[t][w][0] = o[t][w][1] = o[t][w][2] = o[t][w][3] = 0.f;
         }
         shortest = __reduce_min_sync(kFullMask, shortest);
-        float vref = 0.f, vinv = 0.f;
+        float vref = 0.f, vinv = 0.f, vtop = 0.f;  // vtop: the largest vref so far
 
         // ---- the pages
 #pragma unroll 1
@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             float rel = vs * vinv, move = 1.f;
             if (there && vs > 0.f && vs < INFINITY && !(rel <= kWindow && rel >= 1.f / kWindow)) {
                 const int e = min(max((int)(__float_as_uint(vs) >> 23) - 127, -126), 126);
-                const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vref * 7.8886091e-31f);  // 2^-100
+                const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vtop * 7.8886091e-31f);  // 2^-100: outputs stay finite
+                vtop = fmaxf(vtop, to);
                 move = vref / to;
                 vref = to;
                 vinv = 1.f / to;

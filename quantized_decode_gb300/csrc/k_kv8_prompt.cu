@@ -17,7 +17,8 @@
 //
 // Codes are exact in fp16.  The K scale of a page multiplies its 16 score columns inside the exponent's
 // FMA.  The V scale is split between V's fp16 values and the exponent (kv8_tc.cuh).  The maximum that the exponent
-// refers to follows the row's only when that has grown by a few powers of two, so O is rarely rescaled.
+// refers to, of what becomes a weight (so with the V scale's part), follows the row's only when that has grown by a few
+// powers of two, so O is rarely rescaled.
 //
 // Rows of fp32 keep 22 bits of q and of the weights: a second tile of remainders each, added by a second MMA
 // into the same accumulator.
@@ -69,12 +70,12 @@ QD_DEV void load_q8(const Kv8AttnArgs &a, int64_t at, bool live, float (&v)[8]) 
     }
 }
 
-// Weights are exp2(s - m) 2^kLift r with s <= m + kLag and r <= 2^4: at most 2^15.  Rows of 16 bits lag far
+// Weights are exp2(s - m) 2^kLift, s the score with log2 r, s <= m + kLag: at most 2^15.  Rows of 16 bits lag far
 // and rarely rescale; those of fp32 lift the weights instead, so that the second fp16 half keeps its 11 bits
 // down to 2^-21 of the largest (fp16 has no normal numbers below 2^-14).
 template <int HL>
 struct Weights {
-    static constexpr float kLag = HL == 2 ? 4.f : 8.f, kLift = HL == 2 ? 7.f : 3.f;
+    static constexpr float kLag = HL == 2 ? 4.f : 8.f, kLift = HL == 2 ? 11.f : 7.f;
 };
 
 // Half a row's softmax of a block, by each lane of a warp: 64 scores at s_at in TMEM (pages p0 .. p0 + 3), weights in
@@ -109,7 +110,7 @@ QD_DEV void block_weights(const BlockRec &rec, int p0, uint32_t s_at, uint32_t o
                 b = fmaxf(fmaxf(b, y[e + 2]), y[e + 3]);
             }
             a = fmaxf(a, b);
-            most = fmaxf(most, CUT && a == -INFINITY ? a : a * (fac * rec.ks[p0 + 2 * c + z]));
+            most = fmaxf(most, CUT && a == -INFINITY ? a : fmaf(a, fac * rec.ks[p0 + 2 * c + z], rec.lr[p0 + 2 * c + z]));
         }
     }
     most = agree(most);
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     const int nt = pairs_rows > kTile ? 2 : 1;
     const int last_tok = (int)min((r0 + 2 * kTile - 1) / G, (int64_t)s.rows - 1);
     const int seen = max(0, s.kv - s.rows + last_tok + 1);  // tokens that any row of the item sees
-    const int nb = (seen + kTile - 1) / kTile;
+    const int nb = kv8_blocks(seen, kTile);
 
     if (threadIdx.x == 0) {
         mbar_init(&b.q_full, nt * 8);
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 fine = wait_warp(&b.codes.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)j);
                 if (!fine) break;
                 tc_fence_after();
-                const bool cut = (j + 1) * kTile > shortest || rec.ok != 0xffu;
+                const bool cut = shortest - j * kTile < kTile || rec.ok != 0xffu;
                 const float vmove = rec.move;
                 vref = rec.vref;
                 auto agree = [&](float x) { return fmaxf(x, other(x, j)); };

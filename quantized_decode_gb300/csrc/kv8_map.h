@@ -61,15 +61,10 @@ KV8_FN Kv8Span kv8_span(const Kv8Seq &s, int64_t j) {
     return r;
 }
 
-// Attention: the rows of a sequence times the G query heads of a K/V head, token by token, are cut
-// into tiles of R.  Work is counted in pages: a sequence has tiles * Hkv segments of `pages`.
-KV8_FN int kv8_tiles(int rows, int G, int R) { return (int)(((int64_t)rows * G + R - 1) / R); }
+// Attention.  Pages of a sequence, at least one; blocks of `tokens`; whether page p of `left` tokens holds one.  Lengths
+// reach 2^31 - 16, so nothing is rounded up by an addition first.
 KV8_FN int kv8_pages(int kv) { return kv > 0 ? (kv - 1) / kKv8Page + 1 : 1; }
-
-// Pages that each CTA takes of `total`: an even share, at least `least`.
-KV8_FN int64_t kv8_share(int64_t total, int ctas, int64_t least) {
-    const int64_t s = (total + ctas - 1) / ctas;
-    return s > least ? s : least;
-}
+KV8_FN int kv8_blocks(int left, int tokens) { return left > 0 ? (left - 1) / tokens + 1 : 0; }
+KV8_FN bool kv8_page_there(int p, int left) { return left > 0 && p <= (left - 1) / kKv8Page; }
 
 }  // namespace qd

@@ -41,53 +41,6 @@ QD_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 QD_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 64 consecutive fp32 columns of the warp's lanes.  The wait names the registers, so that no use moves above it.
-QD_DEV void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-    uint32_t r[64];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-                 "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-                 "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-                   "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-                   "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-                   "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
-                   "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
-                   "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
-                   "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
-                   "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
-                 :
-                 : "memory");
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 columns, in two steps: the values are there once tmem_ld16_wait has passed, which names the registers so that no
-// use moves above it.
-QD_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-}
-QD_DEV void tmem_ld16_wait(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
 // Two fp32 operations in one instruction.
 QD_DEV float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -189,11 +142,12 @@ struct BlockRec {
 };
 
 // The split of a block's V scales against vref, which all lanes keep alike; lane p % 8 holds page p.
-// vref is a power of two that follows the scales where they leave [2^-14, 2^4] of it.
+// vref is a power of two that follows the scales where they leave [2^-14, 2^4] of it, but not below 2^-60 of the largest
+// one so far (vtop): outputs in its units stay finite.  Scales below 2^-100 of it count as 0.
 struct VSplit {
     float r, mul, move;  // mul = 2^-k, 0 for a scale of 0
 };
-QD_DEV VSplit split_scale(float vs, float &vref) {
+QD_DEV VSplit split_scale(float vs, float &vref, float &vtop) {
     VSplit o;
     float top = vs > 0.f && vs < INFINITY ? vs : 0.f;
 #pragma unroll
@@ -201,12 +155,15 @@ QD_DEV VSplit split_scale(float vs, float &vref) {
     o.move = 1.f;
     if (top > 0.f && (vref == 0.f || top > vref * 16.f || top < vref * 6.1035156e-05f)) {  // 2^-14
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -126), 126);
-        const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vref * 8.6736174e-19f);  // 2^-60
+        const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vtop * 8.6736174e-19f);  // 2^-60
         o.move = vref == 0.f ? 1.f : vref / to;
         vref = to;
+        vtop = fmaxf(vtop, to);
     }
-    o.r = vs == 0.f ? 1.f : vs / vref;
-    o.mul = vs == 0.f ? 0.f : 1.f;
+    o.r = vs / vref;
+    const bool none = vs == 0.f || o.r < 7.8886091e-31f;  // 2^-100
+    if (none) o.r = 1.f;
+    o.mul = none ? 0.f : 1.f;
     if (o.r < 1.f) {
         const int k = min(127 - (int)(__float_as_uint(o.r) >> 23), 15);
         o.mul = __uint_as_float((uint32_t)(127 - k) << 23);
@@ -246,7 +203,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
     // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
     auto entry = [&](int j) {
         const int p = j * kBlockPages + (lane & 7);
-        return j < nb && p * kKv8Page < left ? max(-1, __ldg(table + p)) : -2;
+        return j < nb && kv8_page_there(p, left) ? max(-1, __ldg(table + p)) : -2;
     };
     auto checked = [&](int ph) {
         if (ph != -1 && ph < a.c.n_pool_pages) return ph;
@@ -255,7 +212,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
     };
     auto scale_of = [&](const float *pool, int ph) { return ph >= 0 ? __ldg(pool + (int64_t)ph * Hkv + head) : 0.f; };
     int ph = checked(entry(0)), ph_next = entry(1);
-    float ks = scale_of(a.c.k_scale, ph), vs = scale_of(a.c.v_scale, ph), vref = 0.f;
+    float ks = scale_of(a.c.k_scale, ph), vs = scale_of(a.c.v_scale, ph), vref = 0.f, vtop = 0.f;
     for (int j = 0; j < nb; ++j) {
         const int n = n_done + j;
         const uint32_t ok = __ballot_sync(kFullMask, ph >= 0) & 0xffu;
@@ -277,7 +234,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
         // The unit of K waited for above held block n - 1 (UNITS is 2): its converters had waited for the scores of block
         // n - 3 at the latest, those for the weights of n - 4, so nobody reads the record of n - kRecs any more
         static_assert(UNITS == 2 && kRecs == 4, "the argument above");
-        const VSplit v = split_scale(vs, vref);
+        const VSplit v = split_scale(vs, vref, vtop);
         BlockRec &rec = ring.rec[n % kRecs];
         if (lane < kBlockPages) {
             rec.ks[lane] = ks;

@@ -256,6 +256,167 @@ def test_attention_many_sequences():
     _attend(DeviceCache(host, table), host, table, "f32", q, rows, kv)
 
 
+PROMPTS = {  # by rows and lengths: several blocks of 128 tokens, tiles and pairs of tiles that end anywhere
+    "deep": ((200,), (1500,)),
+    "from the start": ((513, 0, 300), (513, 40, 300)),
+    "behind others": ((65, 1, 129, 64), (1024, 700, 129, 2000)),
+}
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (7, 1, 128), (8, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("call", list(PROMPTS))
+def test_attention_prompts_of_many_blocks(fmt, dtype, Hq, Hkv, d, call):
+    rows, kv = PROMPTS[call]
+    rng = np.random.default_rng(len(call) + Hq + d)
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, fmt, pages, Hkv, d)
+    q = _rand(rng, (sum(rows) + 1, Hq, d), dtype, 2.0)
+    dev = DeviceCache(host, table)
+    first = _attend(dev, host, table, dtype, q, rows, kv, extra=1)
+    for _ in range(3):  # the result does not depend on the run
+        again = _attend(dev, host, table, dtype, q, rows, kv, extra=1)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "f32"), ("e4m3", "f32"), ("int8", "bf16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("rows,kv", [((1, 1), (700, 1300)), ((4, 3), (700, 90)), ((150, 40), (700, 300))])
+@pytest.mark.parametrize("spread", [10, 40])
+def test_attention_scales_far_apart(fmt, dtype, rows, kv, spread):
+    """V scales of neighbouring pages up to 2^(2 spread) apart, zeros among them: rows see what is theirs, whatever pages behind
+    them hold."""
+    rng = np.random.default_rng(28 + spread)
+    Hq, Hkv, d = 6, 2, 128
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, fmt, pages, Hkv, d)
+    host["vs"] *= np.float32(2.0) ** rng.integers(-spread, spread + 1, host["vs"].shape).astype(np.float32)
+    host["vs"][rng.random(host["vs"].shape) < 0.1] = 0
+    host["ks"][rng.random(host["ks"].shape) < 0.1] = 0
+    q = _rand(rng, (sum(rows), Hq, d), dtype, 2.0)
+    _attend(DeviceCache(host, table), host, table, dtype, q, rows, kv)
+
+
+@pytest.mark.parametrize("rows", [1, 4, 300])
+def test_attention_scales_at_the_ends_of_fp32(rows):
+    """V scales that fall by 2^240 along a sequence: the largest decide, nothing overflows on the way."""
+    rng = np.random.default_rng(29)
+    Hq, Hkv, d, kv = 4, 2, 64, 1600
+    table, pages = page_table(rng, [kv])
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    for order in (1, -1):
+        host["vs"][table[0]] = (np.float32(2.0) ** np.linspace(110, -130, 100)[::order].astype(np.float32))[:, None]
+        q = _rand(rng, (rows, Hq, d), "f32", 0.1)  # near even weights: every page counts by its scale
+        _attend(DeviceCache(host, table), host, table, "f32", q, (rows,), (kv,))
+
+
+def test_prompt_with_a_page_that_is_none():
+    rng = np.random.default_rng(30)
+    Hq, Hkv, d, rows, kv = 4, 2, 64, 200, 300
+    table, pages = page_table(rng, [kv])
+    host = host_cache(rng, "e4m3", pages, Hkv, d)
+    q = _rand(rng, (rows, Hq, d), "f32")
+    for bad in (-1, pages, 1 << 30):
+        t = table.copy()
+        t[0, 3] = bad  # tokens 48 .. 63, which every row sees
+        dev = DeviceCache(host, t)
+        out = torch.zeros(rows, Hq, d, device="cuda")
+        assert dev.attention("f32", q, ints([0, rows]), ints([kv]), out) == 0
+        assert dev.err.item() == L.LLM_ERR_DEVICE
+        # the same tokens in a sequence without that page
+        short = DeviceCache(host, np.delete(table, 3, axis=1))
+        want = torch.zeros(rows, Hq, d, device="cuda")
+        assert short.attention("f32", q, ints([0, rows]), ints([kv - 16]), want) == 0
+        assert short.err.item() == 0
+        # both within 2 (36 2^-23 A + 2^-21) + 800 2^-23 of sums w|v| below 6, with A = sum|q k| / 8 below 300
+        assert float((out - want).abs().max()) < 2 * 6 * (2 * (300 * 36 * 2.0 ** -23 + 2.0 ** -21) + 800 * 2.0 ** -23)
+
+
+def test_many_sequences_in_one_call():
+    """Append, read and prompt attention with more sequences than a warp looks at in one step, some of them empty."""
+    rng = np.random.default_rng(35)
+    n, Hq, Hkv, d = 150, 6, 3, 64
+    rows = rng.integers(0, 60, n)
+    rows[rng.random(n) < 0.2] = 0
+    kv = rows + rng.integers(0, 40, n)
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    dev = DeviceCache(host, table)
+    k, v = (_rand(rng, (int(rows.sum()), Hkv, d), "bf16") for _ in range(2))
+    rs, lens = ints(starts(rows)), ints(kv)
+    assert dev.append("bf16", k, v, rs, lens) == 0
+    kv8.append(host, table, starts(rows), kv, as_f32(k), as_f32(v))
+    got = dev.host()
+    for x in ("k", "v", "ks", "vs"):
+        np.testing.assert_array_equal(got[x], host[x])
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    assert dev.read("bf16", ko, vo, rs, lens) == 0
+    for a, ref in zip((ko, vo), kv8.read(host, table, starts(rows), kv, len(k))):
+        assert torch.equal(a.cpu(), torch.from_numpy(ref).bfloat16())
+    q = _rand(rng, (len(k), Hq, d), "f32", 2.0)
+    _attend(dev, host, table, "f32", q, tuple(int(x) for x in rows), tuple(int(x) for x in kv))
+
+
+@pytest.mark.parametrize("rows", [1, 4, 100])
+def test_pages_beyond_32_bits(rows):
+    """Pools of more than 4 GB, pages at their end: every offset is 64 bits wide."""
+    rng = np.random.default_rng(36)
+    Hq, Hkv, d, kv = 16, 8, 128, 130
+    pages = 270000  # 4.4 GB of K, as much of V
+    used = -(-kv // 16)
+    small = host_cache(rng, "int8", used, Hkv, d)
+    dev = DeviceCache(small, np.arange(used, dtype=np.int32)[None])
+    k = torch.empty(pages, Hkv, 16, d, dtype=torch.uint8, device="cuda")
+    v = torch.empty_like(k)
+    ks, vs = (torch.zeros(pages, Hkv, device="cuda") for _ in range(2))
+    for big, part in ((k, dev.k), (v, dev.v), (ks, dev.ks), (vs, dev.vs)):
+        big[pages - used:] = part
+    far = DeviceCache(small, np.arange(pages - used, pages, dtype=np.int32)[None])
+    far.k, far.v, far.ks, far.vs, far.shape = k, v, ks, vs, tuple(k.shape)
+    x = _rand(rng, (rows, 2, Hkv, d), "bf16", 3.0)
+    q = _rand(rng, (rows, Hq, d), "f32")
+    outs = []
+    for c in (dev, far):
+        rs, lens = ints([0, rows]), ints([kv])
+        out, back = torch.zeros(rows, Hq, d, device="cuda"), torch.zeros_like(x)
+        assert c.append("bf16", x[:, 0], x[:, 1], rs, lens) == 0
+        assert c.read("bf16", back[:, 0], back[:, 1], rs, lens) == 0
+        assert c.attention("f32", q, rs, lens, out) == 0
+        torch.cuda.synchronize()
+        assert c.err.item() == 0
+        outs.append((out, back))
+    assert torch.equal(far.k[pages - used:], dev.k) and torch.equal(far.vs[pages - used:], dev.vs)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_prompt_in_a_graph_on_a_side_stream():
+    """A captured prompt step, replayed with other lengths than it was captured with."""
+    rng = np.random.default_rng(37)
+    Hq, Hkv, d, rows = 8, 2, 128, (90, 140)
+    cap = (400, 300)
+    table, pages = page_table(rng, cap)
+    host = host_cache(rng, "e4m3", pages, Hkv, d)
+    dev = DeviceCache(host, table)
+    q = _rand(rng, (sum(rows), Hq, d), "bf16", 2.0)
+    rs, lens = ints(starts(rows)), ints((90, 140))
+    out, lse = torch.zeros(sum(rows), Hq, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(sum(rows), Hq, device="cuda")
+    space = new_workspace(dev, Hq, sum(rows))
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+        assert dev.attention("bf16", q, rs, lens, out, lse, stream=torch.cuda.current_stream().cuda_stream, workspace=space) == 0
+        graph.capture_end()
+    for kv in ((90, 140), cap, (91, 299)):
+        lens.copy_(ints(kv))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = kv8.attention(host, table, starts(rows), kv, as_f32(q))
+        tol, ltol = attention_bounds("bf16", *ref, max(kv))
+        assert np.all(np.abs(as_f32(out) - ref[0]) <= tol) and np.all(np.abs(lse.cpu().numpy() - ref[1]) <= ltol)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 40])
 def test_attention_rows_that_see_nothing(rows):
     rng = np.random.default_rng(23)

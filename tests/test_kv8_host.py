@@ -143,18 +143,20 @@ int main() {
         }
         if (!wild)
             for (int r = 0; r < n_rows; ++r) CHECK(met[r] == (r >= start[0] && r < start[B]));
-        // attention: equal shares cover the line once
-        long long total = 0;
+        // attention: pages and blocks within the table, for every length that it can hold
         for (int b = 0; b < B; ++b) {
             const Kv8Seq s = kv8_seq(start[b], start[b + 1], kv[b], n_rows, stride);
             CHECK(s.row0 >= 0 && s.rows >= 0 && s.row0 + s.rows <= n_rows);
             const int kvb = s.kv < 0 || s.kv > stride * 16 ? 0 : s.kv;
             CHECK(kv8_pages(kvb) >= 1 && kv8_pages(kvb) <= stride);
-            total += (long long)kv8_tiles(s.rows, 7, 8) * 4 * kv8_pages(kvb);
         }
-        const int grid = 1 + rnd(300);
-        const long long share = kv8_share(total, grid, 16);
-        CHECK(share >= 16 && share * grid >= total);
+        const int most = 2147483647 - 15;  // 2^27 - 1 pages
+        const int left = trial < 300 ? trial : (trial < 600 ? most - (trial - 300) : rnd(most + 1));
+        const long long nb = kv8_blocks(left, 128);
+        CHECK(nb * 128 >= left && (nb - 1) * 128 < left + (left == 0));
+        for (long long p = nb * 8 - 9; p < nb * 8; ++p)
+            if (p >= 0) CHECK(kv8_page_there((int)p, left) == (p * 16 < left));
+        CHECK(left == 0 || (long long)kv8_pages(left) * 16 >= left);
     }
     printf("ok\n");
     return 0;
