@@ -110,7 +110,8 @@ QD_DEV void block_weights(const BlockRec &rec, int p0, uint32_t s_at, uint32_t o
                 b = fmaxf(fmaxf(b, y[e + 2]), y[e + 3]);
             }
             a = fmaxf(a, b);
-            most = fmaxf(most, CUT && a == -INFINITY ? a : fmaf(a, fac * rec.ks[p0 + 2 * c + z], rec.lr[p0 + 2 * c + z]));
+            const BlockRec::Page &p = rec.page[p0 + 2 * c + z];
+            most = fmaxf(most, CUT && a == -INFINITY ? a : fmaf(a, fac * p.ks, p.lr));
         }
     }
     most = agree(most);
@@ -131,9 +132,9 @@ QD_DEV void block_weights(const BlockRec &rec, int p0, uint32_t s_at, uint32_t o
         uint32_t hi[16];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const int p = p0 + 2 * c + y;
+            const BlockRec::Page p = rec.page[p0 + 2 * c + y];
             hide(x + 16 * y, 2 * c + y);
-            const float kf = fac * rec.ks[p], off = rec.lr[p] - ref;
+            const float kf = fac * p.ks, off = p.lr - ref;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int e = 0; e < kKv8Page; e += 2) {
@@ -155,7 +156,7 @@ QD_DEV void block_weights(const BlockRec &rec, int p0, uint32_t s_at, uint32_t o
             }
             sum[0] = add2(sum[0], sum[1]);
             const float s = sum[0].x + sum[0].y;
-            if (!(CUT && s == 0.f)) l = fmaf(s, rec.ir[p], l);
+            if (!(CUT && s == 0.f)) l = fmaf(s, p.ir, l);
         }
         tmem_st16(s_at + 16 * c, hi);
         if (HL == 2 && c == 1) {
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
     };
     auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
-        if (*abort || !tc_wait(bar, phase & 1u)) {
+        if (!tc_wait(bar, phase & 1u, abort)) {
             fail();
             return false;
         }
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 24 && lane == 0 && nb > 0) {
+        if (warp == 24 && nb > 0) {
             // ================= MMA =================
             const uint32_t id_s = umma_idesc_f16_f32(kTile, kTile);
             const uint32_t id_o = umma_idesc_f16_f32(kTile, D) | kIdescBMn;
@@ -399,49 +400,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 for (int kk = 1; kk < HL * kTile / 16; ++kk)  // weights of 64 tokens, their remainders, the other 64, theirs
                     mma_ts<true>(d, p + (kk >> 2 & 1) * 64 + (kk >> 3) * 32 + (kk & 3) * 8, vd + (kk & 7) * (2048 >> 4), id_o);
             };
-            bool go = wait(&b.q_full, 0) && wait(&b.k_full[0], 0);
+            const bool mine = elect_lane();
+            bool go = wait_warp(&b.q_full, 0) && wait_warp(&b.k_full[0], 0);
             if (go) {
                 tc_fence_after();
-                for (int t = 0; t < nt; ++t) {
-                    scores(t, 0);
-                    umma_commit(&b.s_full[t]);
+                if (mine) {
+                    for (int t = 0; t < nt; ++t) {
+                        scores(t, 0);
+                        umma_commit(&b.s_full[t]);
+                    }
+                    umma_commit(&b.k_empty[0]);
                 }
-                umma_commit(&b.k_empty[0]);
+                __syncwarp();
             }
             for (int j = 0; j < nb && go; ++j) {
                 const int sj = j % C::kStages, sn = (j + 1) % C::kStages;
-                go = wait(&b.v_full[sj], (uint32_t)(j / C::kStages));
+                go = wait_warp(&b.v_full[sj], (uint32_t)(j / C::kStages));
                 for (int t = 0; t < nt && go; ++t) {
-                    go = wait(&b.p_full[t], (uint32_t)j);
+                    go = wait_warp(&b.p_full[t], (uint32_t)j);
                     if (!go) break;
                     tc_fence_after();
-                    weigh(t, sj, j > 0);
-                    if (j + 1 < nb) {
-                        if (t == 0) {
-                            go = wait(&b.k_full[sn], (uint32_t)((j + 1) / C::kStages));
-                            if (!go) break;
-                            tc_fence_after();
-                        }
-                        scores(t, sn);
-                        umma_commit(&b.s_full[t]);
-                    } else {
-                        umma_commit(&b.o_full[t]);
+                    if (mine) weigh(t, sj, j > 0);
+                    __syncwarp();
+                    if (t == 0 && j + 1 < nb) {
+                        go = wait_warp(&b.k_full[sn], (uint32_t)((j + 1) / C::kStages));
+                        if (!go) break;
+                        tc_fence_after();
                     }
-                }
-                if (go) {
-                    umma_commit(&b.v_empty[sj]);
-                    if (j + 1 < nb) umma_commit(&b.k_empty[sn]);
+                    if (mine) {
+                        if (j + 1 < nb) {
+                            scores(t, sn);
+                            umma_commit(&b.s_full[t]);
+                        } else {
+                            umma_commit(&b.o_full[t]);
+                        }
+                        if (t == nt - 1) {
+                            umma_commit(&b.v_empty[sj]);
+                            if (j + 1 < nb) umma_commit(&b.k_empty[sn]);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
-            umma_commit(&b.done);  // arrives once every MMA issued above has completed
-            if (!tc_wait(&b.done, 0)) fail();
+            if (mine) umma_commit(&b.done);  // arrives once every MMA issued above has completed
+            __syncwarp();
+            if (!tc_wait(&b.done, 0, nullptr)) fail();
         }
         if (warp == 25) {
             // ================= copies =================
             int issued = 0;
             feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride, head, nb, seen, 0, b.codes, units, issued, wait_warp);
             if (*abort)  // those in flight land before the shared memory goes away
-                for (int u = max(0, issued - kUnits); u < issued; ++u) tc_wait(&b.codes.full[u % kUnits], (uint32_t)(u / kUnits) & 1u);
+                for (int u = max(0, issued - kUnits); u < issued; ++u) tc_wait(&b.codes.full[u % kUnits], (uint32_t)(u / kUnits) & 1u, nullptr);
         }
         __syncwarp();
     }

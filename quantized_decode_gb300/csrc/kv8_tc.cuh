@@ -16,14 +16,15 @@ constexpr int kBlockPages = kTile / kKv8Page;
 constexpr int kPanel = kTile * 128;    // bytes of 128 rows of 64 fp16
 constexpr uint64_t kWaitNs = 1000000000ull;
 
-// Wait for the phase of `parity`, kWaitNs at most.  The timer is looked at once in a while only: reading
-// it takes longer than a hand-over between two warps.
-QD_DEV bool tc_wait(uint64_t *bar, uint32_t parity) {
+// Wait for the phase of `parity`, kWaitNs at most or until *abort.  Both are looked at once in a while only: reading the
+// timer takes longer than a hand-over between two warps.
+QD_DEV bool tc_wait(uint64_t *bar, uint32_t parity, const volatile int *abort) {
     if (ptx::mbar_test(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (ptx::mbar_test(bar, parity)) return true;
-        if ((i & 1023u) == 0) {
+        if ((i & 255u) == 0) {
+            if (abort && *abort) return false;
             const uint64_t t = ptx::gtimer();
             if (t0 == 0) t0 = t;
             else if (t - t0 > kWaitNs) return false;
@@ -81,8 +82,14 @@ QD_DEV void tmem_scale(uint32_t taddr, int n, float k) {
 constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
 QD_DEV uint32_t desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | 1u << 16; }
 QD_DEV uint32_t desc_mn(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (uint32_t)(kPanel >> 4) << 16; }
-// D (+)= A B with A from shared or tensor memory; the descriptors' low words.  The thread that issues shares its
-// scheduler with busy warps, so an MMA costs it few instructions.
+// One lane of the warp, by elect.sync: MMAs are issued in the branch of the lane that it names.  (In a branch on the lane's
+// number each MMA of 128 x 128 x 16 took 151 cycles beside busy warps; in this one 65, the tensor core's own time.)
+QD_DEV bool elect_lane() {
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x != 0;
+}
+// D (+)= A B with A from shared or tensor memory; the descriptors' low words.
 template <bool ADD>
 QD_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
     asm volatile(
@@ -135,7 +142,9 @@ QD_DEV void codes_f16(const uint4 &u, __half2 h2, bool scaled, uint4 &lo, uint4 
 // is divided by r again.
 constexpr int kRecs = 4;
 struct BlockRec {
-    float ks[kBlockPages], lr[kBlockPages], ir[kBlockPages], mul[kBlockPages];  // K scale, log2 r, 1 / r, 2^-k
+    struct __align__(16) Page {
+        float ks, lr, ir, mul;  // K scale, log2 r, 1 / r, 2^-k
+    } page[kBlockPages];
     float move, vref;  // factor of the output when vref changed with this block; vref
     uint32_t ok;       // pages that are there
     uint32_t scaled;   // some mul is not 1
@@ -237,10 +246,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
         const VSplit v = split_scale(vs, vref, vtop);
         BlockRec &rec = ring.rec[n % kRecs];
         if (lane < kBlockPages) {
-            rec.ks[lane] = ks;
-            rec.lr[lane] = log2f(v.r);
-            rec.ir[lane] = 1.f / v.r;
-            rec.mul[lane] = v.mul;
+            rec.page[lane] = BlockRec::Page{ks, log2f(v.r), 1.f / v.r, v.mul};
         }
         const bool scaled = __any_sync(kFullMask, v.mul != 1.f && ph >= 0);
         if (lane == 0) {
@@ -258,8 +264,9 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
     }
 }
 
-// NT threads turn a block's codes into fp16 rows.  Piece i of a thread is 16 dims of one token; a warp reads 512
-// consecutive bytes.
+// NT threads turn a block's codes into fp16 rows.  Piece i of a thread is 16 dims of one token.  Eight lanes that access
+// shared memory together take the first panel's dims of a token and the second's of its neighbour: 128 bytes of codes on
+// all banks, and (the swizzle) eight chunks on all banks.
 template <int D, int NT>
 struct Pieces {
     static constexpr int kCount = kTile * D / 16 / NT;   // pieces of a thread
@@ -267,20 +274,23 @@ struct Pieces {
     static_assert(kRun >= 1 && kRun * kCount == kBlockPages, "every piece of a block once");
     int tid;
     QD_DEV int page(int i) const { return kRun * i + tid / D; }
-    QD_DEV int in_page() const { return tid % D; }       // 16-byte piece of the page
-    QD_DEV int row() const { return in_page() / (D / 16); }
-    QD_DEV int dim() const { return 16 * (in_page() % (D / 16)); }
+    QD_DEV int panel() const { return D == 128 ? tid >> 2 & 1 : 0; }
+    QD_DEV int row() const {  // in its page
+        const int x = tid % D;
+        return D == 128 ? 2 * (x >> 4) + ((x >> 3 ^ x >> 2) & 1) : x >> 2;
+    }
+    QD_DEV int chunk() const { return 2 * (tid & 3); }   // of its row in the panel: 8 dims each
 
     // left: tokens of the block that are there; whatever lies in the slots behind them, and in pages that are not
     // there, becomes 0
     template <int FMT>
     QD_DEV void convert(const uint8_t *unit, uint8_t *dst, const BlockRec &rec, bool is_v, int left, uint64_t *empty) const {
-        const int lane = threadIdx.x & 31, c = (dim() >> 3) & 7;
-        // eight lanes write a row: those of the second panel the other chunk first, on other banks
-        const bool swap = dim() >= 64, scaled = is_v && rec.scaled != 0, whole = left >= kTile && rec.ok == 0xffu;
+        const int lane = threadIdx.x & 31;
+        const bool scaled = is_v && rec.scaled != 0, whole = left >= kTile && rec.ok == 0xffu;
+        const uint8_t *from = unit + (page(0) * kKv8Page + row()) * D + panel() * 64 + chunk() * 8;
         uint4 w[kCount];
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) w[i] = *reinterpret_cast<const uint4 *>(unit + (kRun * i * D + tid) * 16);
+        for (int i = 0; i < kCount; ++i) w[i] = *reinterpret_cast<const uint4 *>(from + i * (kRun * kKv8Page * D));
         // The next block's codes may come as soon as these have been read: the fence keeps the reads before the copies
         // that follow the arrival (without it they were overtaken).
         ptx::fence_proxy_async_smem();
@@ -291,14 +301,16 @@ struct Pieces {
             for (int i = 0; i < kCount; ++i)
                 if (!((rec.ok >> page(i)) & 1u) || page(i) * kKv8Page + row() >= left) w[i] = make_uint4(0, 0, 0, 0);
         }
+        const int r = page(0) * kKv8Page + row();  // whole pages further on, the swizzle is the same
+        const int x0 = (chunk() ^ (r & 7)) << 4, x1 = x0 ^ 16;
+        uint8_t *to = dst + panel() * kPanel + r * 128;
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
             uint4 c0, c1;
-            codes_f16<FMT>(w[i], __float2half2_rn(scaled ? rec.mul[page(i)] : 1.f), scaled, c0, c1);
-            const int r = page(i) * kKv8Page + row();
-            uint8_t *p = dst + (dim() >> 6) * kPanel + r * 128;
-            *reinterpret_cast<uint4 *>(p + (((c + (swap ? 1 : 0)) ^ (r & 7)) << 4)) = swap ? c1 : c0;
-            *reinterpret_cast<uint4 *>(p + (((c + (swap ? 0 : 1)) ^ (r & 7)) << 4)) = swap ? c0 : c1;
+            codes_f16<FMT>(w[i], __float2half2_rn(scaled ? rec.page[page(i)].mul : 1.f), scaled, c0, c1);
+            uint8_t *p = to + i * (kRun * kKv8Page * 128);
+            *reinterpret_cast<uint4 *>(p + x0) = c0;
+            *reinterpret_cast<uint4 *>(p + x1) = c1;
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
