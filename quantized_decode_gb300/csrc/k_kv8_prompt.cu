@@ -2,7 +2,8 @@
 // drafts): bound by arithmetic, so on the 5th-generation tensor cores.
 //
 // A CTA takes 256 (row, query head) pairs of one K/V head as two tiles of 128 and goes through the
-// keys in blocks of 128 tokens (8 pages):
+// keys in blocks of 128 tokens (8 pages); where that leaves SMs without work, a cluster of CTAs takes them, each an
+// equal share of the blocks, and joins its results through distributed shared memory:
 //   warps 0-15       softmax, eight for each tile: two threads own a row (a TMEM lane), each 64 of its scores;
 //                    they agree on the maximum, keep sums of their own and write the fp16 weights back over
 //                    their scores in TMEM, where they are the A operand of the second product
@@ -30,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 896, kSoftmax = 16, kConvert = 8;  // warps of each kind
 constexpr int kUnits = 2;              // of codes: the next block's K and V
+constexpr int kMaxLogSplit = 3, kLeastBlocks = 6;  // CTAs of a cluster (log2), and from how many blocks on
 constexpr int kQExp = 12;              // q is scaled so that a row's largest element is in [2^12, 2^13)
 
 template <int D, int HL>
@@ -39,6 +41,8 @@ struct Cfg {
     static constexpr int kQ = HL * kP * kPanel;          // bytes of a tile of q
     static constexpr int kKv = kP * kPanel;
     static constexpr int kTiles = 2 * kQ + 2 * kStages * kKv + kUnits * kTile * D;
+    static constexpr int kRes = D + 4;                   // floats of a row's result, which later take the tiles' place
+    static_assert(2 * kTile * (kRes + 1) * 4 <= kTiles, "and log2 of their sums behind them");
 };
 
 struct Bars {
@@ -46,9 +50,79 @@ struct Bars {
     CodeRing<kUnits> codes;
     uint32_t tmem;
     float half[2][2][kTile];  // by tile and half: what the two threads of a row tell each other
+    int64_t out_at;              // for the end, out of registers: row and head of the item's first (row, query head) pair,
+    int out_begin, out_pairs;    // its number among its row's, and how many there are
     int abort;
 };
 
+QD_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// from the shared memory of the cluster's CTA `rank`, what lies there where p does here
+QD_DEV uint32_t cluster_at(const float *p, int rank) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(p)), "r"(rank));
+    return at;
+}
+QD_DEV float cluster_load(const float *p, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_at(p, rank)) : "memory");
+    return v;
+}
+QD_DEV float4 cluster_load4(const float *p, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_at(p, rank)) : "memory");
+    return v;
+}
+// Four elements of a row's results in the cluster's CTAs, and log2 of their sums, together.
+QD_DEV void cluster_join(const float *from, const float *sums, int n, float4 &v, float &top) {
+    top = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) top = fmaxf(top, cluster_load(sums, i));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const float w = ex2(cluster_load(sums, i) - ref);
+        const float4 x = cluster_load4(from, i);
+        sum += w;
+        v = make_float4(fmaf(x.x, w, v.x), fmaf(x.y, w, v.y), fmaf(x.z, w, v.z), fmaf(x.w, w, v.w));
+    }
+    const float k = sum == 0.f ? 0.f : 1.f / sum;
+    v = make_float4(v.x * k, v.y * k, v.z * k, v.w * k);
+    top = ref + log2f(sum);  // of 0: -infinity
+}
+// dims d .. d + 3 of (row, head) number `at`, and its lse
+QD_DEV void store_row4(const Kv8AttnArgs &a, int64_t at, int D, int d, const float4 &v, float top) {
+    if (a.dtype == LLM_DTYPE_F32) {
+        *reinterpret_cast<float4 *>((float *)a.out + at * D + d) = v;
+    } else {
+        const uint2 w = a.dtype == LLM_DTYPE_F16
+                            ? make_uint2(h2_as_u32(__floats2half2_rn(v.x, v.y)), h2_as_u32(__floats2half2_rn(v.z, v.w)))
+                            : make_uint2(RowType<__nv_bfloat16>::two(v.x, v.y), RowType<__nv_bfloat16>::two(v.z, v.w));
+        *reinterpret_cast<uint2 *>((uint16_t *)a.out + at * D + d) = w;
+    }
+    if (d == 0 && a.lse) a.lse[at] = top * 0.69314718f;
+}
+// Dims d .. d + 31 of a row: to the output at `out` where the row is there, or with clusters to its place among the results.
+template <int D>
+QD_DEV void put_row32(const Kv8AttnArgs &a, float *res, int row, bool live, int64_t out, int d, const float (&v)[32]) {
+    if (a.log_split > 0) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(res + row * (D + 4) + d + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else if (live && a.dtype == LLM_DTYPE_F32) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>((float *)a.out + out + d + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else if (live) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+            const float f[8] = {v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
+            *reinterpret_cast<uint4 *>((uint16_t *)a.out + out + d + e) =
+                a.dtype == LLM_DTYPE_F16 ? RowType<__half>::pack(f) : RowType<__nv_bfloat16>::pack(f);
+        }
+    }
+}
 // Eight consecutive elements of a q row (0 where the row is not there).
 QD_DEV void load_q8(const Kv8AttnArgs &a, int64_t at, bool live, float (&v)[8]) {
 #pragma unroll
@@ -180,8 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
 
     // ---- the item: sequence b's pairs of tiles begin at row_start[b] G / 256 + b (as in kv8_item_base: a
     // sequence has at most rows G / 256 + 1 of them); the last ones, which see most, go first
-    const int head = (int)(blockIdx.x % Hkv);
-    const int64_t item = (int64_t)(gridDim.x / Hkv) - 1 - blockIdx.x / Hkv;
+    const unsigned rank = blockIdx.x & ((1u << a.log_split) - 1), id = blockIdx.x >> a.log_split;
+    const int head = (int)(id % Hkv);
+    const int64_t item = (int64_t)((gridDim.x >> a.log_split) / Hkv) - 1 - id / Hkv;
     int seq = 0;
     {
         auto begins = [&](int i) { return (int64_t)max(0, min(__ldg(a.row_start + i), a.n_rows)) * G / (2 * kTile) + i; };
@@ -202,8 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     const int64_t r0 = pair * (2 * kTile);
     const int nt = pairs_rows > kTile ? 2 : 1;
     const int last_tok = (int)min((r0 + 2 * kTile - 1) / G, (int64_t)s.rows - 1);
-    const int seen = max(0, s.kv - s.rows + last_tok + 1);  // tokens that any row of the item sees
-    const int nb = kv8_blocks(seen, kTile);
+    const int all = max(0, s.kv - s.rows + last_tok + 1);  // tokens that any row of the item sees
+    const int nb_all = kv8_blocks(all, kTile);
+    // this CTA's blocks; tokens are counted from the first one's from here on
+    const int b0 = (int)((int64_t)nb_all * rank >> a.log_split), nb = (int)((int64_t)nb_all * (rank + 1) >> a.log_split) - b0;
+    const int seen = all - b0 * kTile;
 
     if (threadIdx.x == 0) {
         mbar_init(&b.q_full, nt * 8);
@@ -229,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     const uint32_t tmem = b.tmem;
     auto s_at = [&](int t) { return tmem + (uint32_t)(t * kTile); };
     auto o_at = [&](int t) { return tmem + (uint32_t)((2 + t) * kTile); };
+    float *res = reinterpret_cast<float *>(smem), *sums = res + 2 * kTile * C::kRes;  // [row][kRes], [row]
     auto fail = [&]() {
         *abort = 1;
         if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
@@ -250,8 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         const int64_t rr = r0 + t * kTile + r;
         const int tok = (int)min(rr / G, (int64_t)INT32_MAX), h = head * G + (int)(rr % G);
         const bool live = t < nt && rr < (int64_t)s.rows * G;
-        const int limit = live ? max(0, s.kv - s.rows + tok + 1) : INT32_MAX;  // rows that are not there: q of 0
+        const int limit = live ? max(0, s.kv - s.rows + tok + 1) - b0 * kTile : INT32_MAX;  // rows that are not there: q of 0
         const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        if (threadIdx.x == 0) {
+            b.out_at = (int64_t)(s.row0 + tok) * a.Hq + head * G;
+            b.out_begin = h - head * G;
+            b.out_pairs = (int)min(pairs_rows, (int64_t)(2 * kTile));
+        }
         if (t < nt && nb > 0) {
             // ---- q: the row's largest element to [2^12, 2^13), fp16 (and the remainder) into the swizzled rows
             float top = 0.f;
@@ -315,48 +399,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p_full[t]);
             }
-            // ---- output
-            fine = fine && wait_warp(&b.o_full[t], 0);
+            // where the results take the tiles' place, both tiles' products have to be done
+            fine = fine && wait_warp(a.log_split > 0 ? &b.done : &b.o_full[t], 0);
             tc_fence_after();
             if (fine) l += other(l, nb);
-            if (fine) {
-                const float k = l == 0.f ? 0.f : vref / l;
-                const int64_t out = ((int64_t)(s.row0 + tok) * a.Hq + h) * D;
+            // ---- these keys' result, to where it belongs or to be joined
+            const float k = !fine || l == 0.f ? 0.f : vref / l;
+            const int row = t * kTile + r;
+            const int64_t out = (int64_t)(s.row0 + tok) * a.Hq + h;
+            const float log_sum = !fine || l == 0.f ? -INFINITY : m + (log2f(l) - kLift);
 #pragma unroll 1
-                for (int i = half * (D / 64); i < (half + 1) * (D / 64); ++i) {
-                    float v[32];
-                    tmem_ld32(o_at(t) + lanes + 32 * i, v);
-                    if (live) {
+            for (int i = half * (D / 64); i < (half + 1) * (D / 64); ++i) {
+                float v[32];
+                tmem_ld32(o_at(t) + lanes + 32 * i, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = l == 0.f ? 0.f : v[e] * k;
-                        if (a.dtype == LLM_DTYPE_F32) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4 *>((float *)a.out + out + 32 * i + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                const float f[8] = {v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5], v[e + 6], v[e + 7]};
-                                *reinterpret_cast<uint4 *>((uint16_t *)a.out + out + 32 * i + e) =
-                                    a.dtype == LLM_DTYPE_F16 ? RowType<__half>::pack(f) : RowType<__nv_bfloat16>::pack(f);
-                            }
-                        }
-                    }
-                }
-                if (live && half == 0 && a.lse) a.lse[(int64_t)(s.row0 + tok) * a.Hq + h] = l == 0.f ? -INFINITY : (m + (log2f(l) - kLift)) * 0.69314718f;
+                for (int e = 0; e < 32; ++e) v[e] = k == 0.f ? 0.f : v[e] * k;
+                put_row32<D>(a, res, row, live, out * D, 32 * i, v);
             }
-        } else if (live && half == 0) {  // no key at all
-            const int64_t out = ((int64_t)(s.row0 + tok) * a.Hq + h) * D;
-            for (int i = 0; i < D; i += 8) {
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                if (a.dtype == LLM_DTYPE_F32) {
-                    *reinterpret_cast<uint4 *>((float *)a.out + out + i) = z;
-                    *reinterpret_cast<uint4 *>((float *)a.out + out + i + 4) = z;
-                } else {
-                    *reinterpret_cast<uint4 *>((uint16_t *)a.out + out + i) = z;
-                }
+            if (half == 0) {
+                if (a.log_split > 0) sums[row] = log_sum;
+                else if (live && a.lse) a.lse[out] = log_sum * 0.69314718f;
             }
-            if (a.lse) a.lse[(int64_t)(s.row0 + tok) * a.Hq + h] = -INFINITY;
+        } else if (t < nt && half == 0) {  // no key
+            float v[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+            const int row = t * kTile + r;
+            const int64_t out = (int64_t)(s.row0 + tok) * a.Hq + h;
+            for (int i = 0; i < D; i += 32) put_row32<D>(a, res, row, live, out * D, i, v);
+            if (a.log_split > 0) sums[row] = -INFINITY;
+            else if (live && a.lse) a.lse[out] = -INFINITY;
         }
     } else if (warp < kSoftmax + kConvert) {
         // ================= codes -> fp16 =================
@@ -449,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         if (warp == 25) {
             // ================= copies =================
             int issued = 0;
-            feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride, head, nb, seen, 0, b.codes, units, issued, wait_warp);
+            feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride + (int64_t)b0 * kBlockPages, head, nb, seen, 0, b.codes, units, issued, wait_warp);
             if (*abort)  // those in flight land before the shared memory goes away
                 for (int u = max(0, issued - kUnits); u < issued; ++u) tc_wait(&b.codes.full[u % kUnits], (uint32_t)(u / kUnits) & 1u, nullptr);
         }
@@ -461,32 +533,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         tc_fence_after();
         tmem_free(tmem, 512);
     }
+    // ---- the cluster's results together, an equal share of the rows by each CTA, always in the order of the keys
+    if (a.log_split == 0) return;
+    cluster_sync();
+    if (warp < kSoftmax) {
+        constexpr int kRowsAtOnce = kSoftmax * 32 / (D / 4);
+        const volatile Bars &end = b;
+        const int inv = (65535 + G) / G;  // x inv / 2^16 is x / G rounded down for x < 2^13: G is 8 at most
+        const int d = threadIdx.x % (D / 4) * 4, share = 2 * kTile >> a.log_split, last = min((int)(rank + 1) * share, end.out_pairs);
+#pragma unroll 1
+        for (int row = (int)rank * share + threadIdx.x / (D / 4); row < last; row += kRowsAtOnce) {
+            float4 v;
+            float top;
+            cluster_join(res + row * C::kRes + d, sums + row, 1 << a.log_split, v, top);
+            const int x = end.out_begin + row, i = x * inv >> 16;
+            store_row4(a, end.out_at + (int64_t)i * a.Hq + (x - i * G), D, d, v, top);
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // a CTA's shared memory stays until all have read it
 }
 
 template <int D, int FMT, int HL>
-cudaError_t prompt(cudaStream_t s, const Kv8AttnArgs &a) {
+cudaError_t prompt(cudaStream_t s, int n_sm, Kv8AttnArgs a) {
     auto kernel = k_kv8_prompt<D, FMT, HL>;
     constexpr int kBytes = Cfg<D, HL>::kTiles + (int)sizeof(Bars);
     static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     const int G = a.Hq / a.c.n_kv_heads;
-    const int64_t items = (int64_t)a.n_rows * G / (2 * kTile) + a.c.n_seqs, grid = items * a.c.n_kv_heads;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    kernel<<<(unsigned)grid, kThreads, kBytes, s>>>(a);
-    return cudaGetLastError();
+    const int64_t items = (int64_t)a.n_rows * G / (2 * kTile) + a.c.n_seqs, ctas = items * a.c.n_kv_heads;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    // Clusters as long as all CTAs find an SM and the longest sequence that the table can hold has a block for each.  8 K/V
+    // heads, with and without: 200 rows at 20000 tokens 101 and 318 us, 60 at 2000 28 and 48 us; at 512 rows and tokens
+    // (4 blocks) 26.8 and 25.5 us, so not there.
+    const int64_t blocks = (int64_t)a.c.table_stride / kBlockPages;
+    a.log_split = 0;
+    while (a.log_split < kMaxLogSplit && (ctas << (a.log_split + 1)) <= n_sm && blocks >= kLeastBlocks && (2 << a.log_split) <= blocks) ++a.log_split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas << a.log_split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << a.log_split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.log_split > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 template <int D, int FMT>
-cudaError_t prompt(cudaStream_t s, const Kv8AttnArgs &a) {
-    return a.dtype == LLM_DTYPE_F32 ? prompt<D, FMT, 2>(s, a) : prompt<D, FMT, 1>(s, a);
+cudaError_t prompt(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
+    return a.dtype == LLM_DTYPE_F32 ? prompt<D, FMT, 2>(s, n_sm, a) : prompt<D, FMT, 1>(s, n_sm, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_prompt(cudaStream_t s, const Kv8AttnArgs &a) {
+cudaError_t launch_kv8_prompt(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
     if (a.c.format == LLM_KV8_INT8)
-        return a.c.head_dim == 128 ? prompt<128, LLM_KV8_INT8>(s, a) : prompt<64, LLM_KV8_INT8>(s, a);
-    return a.c.head_dim == 128 ? prompt<128, LLM_KV8_E4M3>(s, a) : prompt<64, LLM_KV8_E4M3>(s, a);
+        return a.c.head_dim == 128 ? prompt<128, LLM_KV8_INT8>(s, n_sm, a) : prompt<64, LLM_KV8_INT8>(s, n_sm, a);
+    return a.c.head_dim == 128 ? prompt<128, LLM_KV8_E4M3>(s, n_sm, a) : prompt<64, LLM_KV8_E4M3>(s, n_sm, a);
 }
 
 }  // namespace qd

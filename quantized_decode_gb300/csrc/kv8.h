@@ -41,6 +41,7 @@ struct Kv8AttnArgs {
     int32_t *counters;  // kKv8Counters, zero between calls
     float *parts;       // partial results behind them
     int places;         // of parts; as many for groups of them follow
+    int log_split;      // prompts: log2 of the CTAs of a cluster, which share the keys
     int32_t *err;
 };
 
@@ -53,6 +54,6 @@ cudaError_t launch_kv8_read(cudaStream_t s, int dtype, const Kv8RowsArgs &a);
 int64_t kv8_attention_workspace(int n_sm, int d);
 bool kv8_few_rows(const Kv8AttnArgs &a);  // launch_kv8_attention, or launch_kv8_prompt
 cudaError_t launch_kv8_attention(cudaStream_t s, int n_sm, const Kv8AttnArgs &a);
-cudaError_t launch_kv8_prompt(cudaStream_t s, const Kv8AttnArgs &a);
+cudaError_t launch_kv8_prompt(cudaStream_t s, int n_sm, const Kv8AttnArgs &a);
 
 }  // namespace qd

@@ -115,7 +115,7 @@ int llm_op_kv8_attention(const llm_kv8_cache *c, int32_t dtype, const void *q, i
     a.counters = (int32_t *)workspace;
     a.parts = (float *)((char *)workspace + kKv8Counters * sizeof(int32_t));
     a.places = 2 * n_sm;
-    if (!kv8_few_rows(a)) return status(launch_kv8_prompt((cudaStream_t)stream, a));
+    if (!kv8_few_rows(a)) return status(launch_kv8_prompt((cudaStream_t)stream, n_sm, a));
     return status(launch_kv8_attention((cudaStream_t)stream, n_sm, a));
 }
 

@@ -310,6 +310,24 @@ def test_attention_scales_at_the_ends_of_fp32(rows):
         _attend(DeviceCache(host, table), host, table, "f32", q, (rows,), (kv,))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("kv", [1, 40, 129, 1000, 5000])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (7, 1, 128)])
+def test_few_rows_in_a_long_table(dtype, kv, Hq, Hkv, d):
+    """Prompts too small for all SMs share their keys among CTAs by the table's length: those without keys, rows before
+    the first token and pairs of tiles that are not full change nothing."""
+    rng = np.random.default_rng(38 + kv)
+    rows = 90
+    table, pages = page_table(rng, [kv], capacity=[5008])
+    host = host_cache(rng, "e4m3", pages, Hkv, d)
+    q = _rand(rng, (rows + 1, Hq, d), dtype, 2.0)
+    dev = DeviceCache(host, table)
+    first = _attend(dev, host, table, dtype, q, (rows,), (kv,), extra=1)
+    for _ in range(3):
+        again = _attend(dev, host, table, dtype, q, (rows,), (kv,), extra=1)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_prompt_with_a_page_that_is_none():
     rng = np.random.default_rng(30)
     Hq, Hkv, d, rows, kv = 4, 2, 64, 200, 300
