@@ -29,11 +29,13 @@ namespace qd {
 
 namespace {
 
-// NT tiles of 8 rows: one with 16 warps of 128 registers (12 of 168 for fp32 rows), up to four with 8 of 255.
+// NT tiles of 8 rows: one with 16 warps of 128 registers (12 of 168 for fp32 rows), or two with 8 of 255.
 template <int D, int NT, bool HL>
 struct Cfg {
     static constexpr int kWarps = NT > 1 ? 8 : (HL ? 12 : 16), kThreads = kWarps * 32, kRows = 8 * NT;
-    static constexpr int kLeast = 2 * kWarps;   // pages of a part at least (for 4096 tokens of 4 heads: once 13.4 us, twice 12.8, four times 14.8)
+    // pages of a part at least.  One tile, 4096 tokens of 4 heads: a page for each warp 13.4 us, two 12.8, four 14.8; two tiles,
+    // 16 rows at 500 tokens: one 10.9 us, two 12.5
+    static constexpr int kLeast = (NT > 1 ? 1 : 2) * kWarps;
     static constexpr int kRow = D + 4;          // floats of a row in the merge buffer
     static constexpr int kMerge = kWarps * kRows * kRow * 4;
     static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * (HL ? 16 : 8);  // B fragments of q
@@ -672,23 +674,30 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
 }
 template <int D, int FMT>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
-    const bool one = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) <= (int64_t)8 * a.c.n_seqs;
-    if (a.dtype == LLM_DTYPE_F32) return one ? attend<D, FMT, 1, true>(s, n_sm, a) : attend<D, FMT, 4, true>(s, n_sm, a);
-    return one ? attend<D, FMT, 1, false>(s, n_sm, a) : attend<D, FMT, 4, false>(s, n_sm, a);
+    // Two tiles share a page's loads and conversions, one leaves registers for twice the warps and smaller parts.  Fp32 rows,
+    // one and two: 24 rows of 8 sequences to 8000 tokens of 2 heads 15.4 and 18.4 us, 24 rows at 60000 tokens 27 and 31
+    // us; but 16 rows of 8 sequences of 8 heads 35 and 24 us, 32 bf16 rows at 60000 tokens of 8 heads 103 and 73 us.  So one
+    // while the segments find a CTA each and their pages are few.  (Four tiles measured slower than two everywhere.)
+    const int64_t rows = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads), segs = (rows + 7 * (int64_t)a.c.n_seqs) / 8 * a.c.n_kv_heads;
+    const bool one = rows <= (int64_t)8 * a.c.n_seqs || (segs <= n_sm && segs * a.c.table_stride <= (int64_t)256 * n_sm);
+    if (a.dtype == LLM_DTYPE_F32) return one ? attend<D, FMT, 1, true>(s, n_sm, a) : attend<D, FMT, 2, true>(s, n_sm, a);
+    return one ? attend<D, FMT, 1, false>(s, n_sm, a) : attend<D, FMT, 2, false>(s, n_sm, a);
 }
 
 }  // namespace
 
 int64_t kv8_attention_workspace(int n_sm, int d) {
     // a segment cut into c >= 2 parts has more than (c - 1) share pages, so there are at most two parts for each
-    // CTA's share, each with a place of up to 32 rows, and another for its group
-    return kKv8Counters * 4 + 2 * 2 * (int64_t)n_sm * 32 * (d + 2) * 4;
+    // CTA's share, each with a place of up to 16 rows, and another for its group
+    return kKv8Counters * 4 + 2 * 2 * (int64_t)n_sm * 16 * (d + 2) * 4;
 }
 
 bool kv8_few_rows(const Kv8AttnArgs &a) {
-    // items are counted in 32 bits, whatever row_start holds; beyond this the prompt kernel, which counts none
+    // Rows of a sequence, times heads, where the prompt kernel's tiles of 128 begin to pay.  This one and that: 32 rows of 8
+    // sequences to 1000 tokens of 8 heads 23 and 26 us, 48 of 16 to 8000 of 2 heads 35 and 44 us, 64 of 8 to 1000 of 8 heads 28
+    // and 26 us.  Items are counted in 32 bits, whatever row_start holds; beyond this the prompt kernel, which counts none.
     const int64_t rows = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads);
-    return rows <= (int64_t)32 * a.c.n_seqs && (rows / 8 + 1) * a.c.n_seqs * a.c.n_kv_heads < 1 << 30;
+    return rows <= (int64_t)48 * a.c.n_seqs && (rows / 8 + 1) * a.c.n_seqs * a.c.n_kv_heads < 1 << 30;
 }
 
 cudaError_t launch_kv8_attention(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
