@@ -148,8 +148,8 @@ int llm_op_gemm_quant(int32_t fmt, const void *A, const void *w, const void *s, 
  * (nondecreasing, row_start[0] >= 0; sequence b has rows row_start[b] ..
  * row_start[b + 1] - 1); kv_len, int32 [n_seqs] on the device, each sequence's
  * length with those rows in it, so that its rows are its last tokens, at
- * positions kv_len[b] - rows .. kv_len[b] - 1; and n_rows on the host, the rows
- * that the arrays hold.  Rows behind row_start[n_seqs] are left as they are.  The
+ * positions kv_len[b] - rows .. kv_len[b] - 1; and n_rows >= 1 on the host, the
+ * rows that the arrays hold.  Rows behind row_start[n_seqs] are left as they are.  The
  * same three serve a step's append and then its attention.
  *
  * The calls are asynchronous on `stream`, allocate nothing and can be captured
@@ -211,7 +211,7 @@ int llm_op_qk_norm_rope(int32_t dtype, const void *q, int64_t q_stride, const vo
  * each operation in fp32, round half to even to the code's type, saturating.  A
  * block that is given a NaN or an infinity has a NaN scale from then on, and all
  * that is read from it is NaN.  Slots behind a sequence's last token keep their
- * codes.  Sequences of one call must not share a page that it writes.             */
+ * codes.  A page that a call writes must be in the tables of its sequences once.   */
 int llm_op_kv8_append(const llm_kv8_cache *cache, int32_t dtype, const void *k, int64_t k_stride,
                       const void *v, int64_t v_stride, const int32_t *row_start, const int32_t *kv_len,
                       int32_t n_rows, int32_t *err, void *stream);
@@ -235,7 +235,7 @@ int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32
  * row at a negative position (more rows than kv_len) sees nothing: out 0, lse
  * -infinity.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
  * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
- * 16-byte aligned.  Sums and softmax statistics are held in fp32; with fp32 rows
+ * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32; with fp32 rows
  * the products carry 22 bits of q and of the weights, with 16-bit rows q exactly
  * and 11 bits of the weights at least.  Results do not depend on the run.
  * Hq % Hkv == 0, Hq/Hkv <= 8.  workspace: device, 256-byte aligned, zero-filled

@@ -482,6 +482,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                         n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, x));
                         n1 = fmaxf(n1, __shfl_xor_sync(kFullMask, n1, x));
                     }
+                    // only rows that need it, so that a row's result has nothing to do with its neighbours
+                    if (n0 <= m[t][0] + kLag && m[t][0] != -INFINITY) n0 = m[t][0];
+                    if (n1 <= m[t][1] + kLag && m[t][1] != -INFINITY) n1 = m[t][1];
                     const float a0 = n0 == m[t][0] ? 1.f : ex2(m[t][0] - n0), a1 = n1 == m[t][1] ? 1.f : ex2(m[t][1] - n1);
                     m[t][0] = n0;
                     m[t][1] = n1;

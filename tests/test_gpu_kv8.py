@@ -679,3 +679,98 @@ def test_prompt_then_steps_against_the_bf16_attention():
             assert float((outs[i, h] - ref[h]).abs().max()) <= tol
     # typical error: far below
     assert float((outs[total - 1] - ref).square().mean().sqrt() / ref.square().mean().sqrt()) < 0.05
+
+
+# ---------------------------------------------------------------- calls at the edges of what is allowed
+
+
+@pytest.mark.parametrize("rows", [(1, 2), (150, 40)])
+def test_rows_before_the_first_sequence_and_strided_rows(rows):
+    """row_start[0] > 0, all rows inside wider ones, no err word: rows that are nobody's stay as they are."""
+    rng = np.random.default_rng(41)
+    Hq, Hkv, d, first, kv = 12, 2, 64, 301, (170, 45)
+    n = first + sum(rows) + 2
+    rs = first + starts(rows)
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    dev = DeviceCache(host, table)
+    wide = _rand(rng, (n, Hq + 2 * Hkv + 2, d), "f16", 2.0)
+    q, k, v = wide[:, 1:1 + Hq], wide[:, Hq + 1:Hq + Hkv + 1], wide[:, Hq + Hkv + 1:Hq + 2 * Hkv + 1]
+    lib, tid, r, lens = L.load(), DTYPES["f16"][1], ints(rs), ints(kv)
+    assert lib.llm_op_kv8_append(dev.struct(), tid, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), r.data_ptr(), lens.data_ptr(), n,
+                                 None, None) == 0
+    kv8.append(host, table, rs, kv, as_f32(k), as_f32(v))
+    got = dev.host()
+    for x in ("k", "v", "ks", "vs"):
+        np.testing.assert_array_equal(got[x], host[x])
+    back = torch.full((n, 2, Hkv + 1, d), 77.0, dtype=torch.float16, device="cuda")
+    assert lib.llm_op_kv8_read(dev.struct(), tid, r.data_ptr(), lens.data_ptr(), n, back[:, 0].data_ptr(), back.stride(0), back[:, 1].data_ptr(),
+                               back.stride(0), None, None) == 0
+    for i, ref in enumerate(kv8.read(host, table, rs, kv, n)):
+        assert torch.equal(back[first:first + sum(rows), i, :Hkv].cpu(), torch.from_numpy(ref[first:first + sum(rows)]).half())
+    assert torch.all(back[:first] == 77) and torch.all(back[-2:] == 77) and torch.all(back[:, :, Hkv] == 77)
+    out = torch.full((n, Hq, d), 55.0, dtype=torch.float16, device="cuda")
+    space = new_workspace(dev, Hq, n)
+    assert lib.llm_op_kv8_attention(dev.struct(), tid, q.data_ptr(), q.stride(0), r.data_ptr(), lens.data_ptr(), n, Hq, out.data_ptr(), None,
+                                    space.data_ptr(), space.numel(), None, None) == 0
+    ref = kv8.attention(host, table, rs, kv, as_f32(q))
+    tol, _ = attention_bounds("f16", *ref, max(kv))
+    mine = slice(first, first + sum(rows))
+    assert np.all(np.abs(as_f32(out) - ref[0])[mine] <= tol[mine])
+    assert torch.all(out[:first] == 55) and torch.all(out[-2:] == 55)
+
+
+def test_the_most_sequences():
+    rng = np.random.default_rng(42)
+    n, Hq, Hkv, d = 4096, 2, 1, 64
+    kv = rng.integers(0, 40, n)
+    rows = np.minimum(kv, rng.integers(0, 3, n))
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    q = _rand(rng, (int(rows.sum()), Hq, d), "f32", 2.0)
+    _attend(DeviceCache(host, table), host, table, "f32", q, tuple(int(x) for x in rows), tuple(int(x) for x in kv))
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+def test_many_heads_and_uneven_lengths(rows):
+    """More heads than SMs would share evenly, one long sequence among short ones."""
+    rng = np.random.default_rng(43)
+    Hq, Hkv, d, kv = 40, 40, 64, (5000, 80, 300)
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, "e4m3", pages, Hkv, d)
+    q = _rand(rng, (3 * rows, Hq, d), "bf16", 2.0)
+    _attend(DeviceCache(host, table), host, table, "bf16", q, (rows,) * 3, kv)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+def test_a_row_that_is_not_finite_is_its_own_affair(rows, bad):
+    rng = np.random.default_rng(44)
+    Hq, Hkv, d, kv = 8, 2, 128, (700, 260)
+    table, pages = page_table(rng, kv)
+    dev = DeviceCache(host_cache(rng, "int8", pages, Hkv, d), table)
+    q = _rand(rng, (2 * rows, Hq, d), "f32")
+    outs = []
+    for spoil in (False, True):
+        x = q.clone()
+        if spoil:
+            x[rows // 2, 3, 17] = bad
+        out, lse = torch.zeros_like(x), torch.zeros(2 * rows, Hq, device="cuda")
+        assert dev.attention("f32", x, ints([0, rows, 2 * rows]), ints(kv), out, lse) == 0
+        outs.append((out, lse))
+    keep = torch.ones(2 * rows, Hq, dtype=torch.bool, device="cuda")
+    keep[rows // 2, 3] = False
+    assert torch.equal(outs[0][0][keep], outs[1][0][keep]) and torch.equal(outs[0][1][keep], outs[1][1][keep])
+    if bad != 3e38:
+        assert torch.all(torch.isnan(outs[1][0][~keep]))
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    rng = np.random.default_rng(45)
+    table, pages = page_table(rng, [20])
+    dev = DeviceCache(host_cache(rng, "int8", pages, 2, 64), table)
+    q = _rand(rng, (1, 4, 64), "f32")
+    out = torch.full_like(q, 9.0)
+    space = new_workspace(dev, 4, 1)
+    assert dev.attention("f32", q, ints([0, 1]), ints([20]), out, workspace=space[:-1]) == L.LLM_ERR_ARG
+    assert torch.all(out == 9.0)
