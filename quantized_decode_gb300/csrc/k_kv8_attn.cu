@@ -24,23 +24,25 @@
 // segment of one part is written at once; else its parts leave partial results in the workspace, and the last
 // to arrive (a counter) joins them in the order of the parts: the result does not depend on who is last.
 //
-// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 107 us, 5.0 TB/s, 97 us for e4m3;
-// 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 38 us; one of 4096 tokens (28/4, fp32 rows)
-// 11 us.  The long ones are bound by the latency of loads over 16 warps of 128 registers an SM (issue slots 53% used), the
-// short ones by the chain from the lengths over the table and the pages to two joins.
+// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 91 us, 5.9 TB/s, 90 us for e4m3;
+// 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 34 us; one of 4096 tokens (28/4, fp32 rows)
+// 11 us.  The long ones are bound by memory and the latency of loads over 12 warps an SM (without the prefetch of the next pages
+// into L2 107 us), the short ones by the chain from the lengths over the table and the pages to two joins.
 #include "kv8.cuh"
 
 namespace qd {
 
 namespace {
 
-// NT tiles of 8 rows: one with 16 warps of 128 registers (12 of 168 for fp32 rows), or two with 8 of 255.
+// NT tiles of 8 rows: one with 12 warps of 168 registers, or two with 8 of 255.  (4 sequences of 131072 tokens, 16-bit rows:
+// 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141: the four schedulers want
+// equal shares.)
 template <int D, int NT, bool HL>
 struct Cfg {
-    static constexpr int kWarps = NT > 1 ? 8 : (HL ? 12 : 16), kThreads = kWarps * 32, kRows = 8 * NT;
-    // pages of a part at least.  One tile, 4096 tokens of 4 heads: a page for each warp 13.4 us, two 12.8, four 14.8; two tiles,
-    // 16 rows at 500 tokens: one 10.9 us, two 12.5
-    static constexpr int kLeast = (NT > 1 ? 1 : 2) * kWarps;
+    static constexpr int kWarps = NT > 1 ? 8 : 12, kThreads = kWarps * 32, kRows = 8 * NT;
+    // pages of a part at least: one for each warp.  One tile, 4096 tokens of 4 heads: one 11.4 us, two the same, three 11.9;
+    // two tiles, 24 rows at 500 tokens: one 10.9 us, two 12.5
+    static constexpr int kLeast = kWarps;
     static constexpr int kRow = D + 4;          // floats of a row in the merge buffer
     static constexpr int kMerge = kWarps * kRows * kRow * 4;
     static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * (HL ? 16 : 8);  // B fragments of q
@@ -682,7 +684,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
 }
 template <int D, int FMT>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
-    // Two tiles share a page's loads and conversions, one leaves registers for twice the warps and smaller parts.  Fp32 rows,
+    // Two tiles share a page's loads and conversions, one leaves registers for more warps and smaller parts.  Fp32 rows,
     // one and two: 24 rows of 8 sequences to 8000 tokens of 2 heads 15.4 and 18.4 us, 24 rows at 60000 tokens 27 and 31
     // us; but 16 rows of 8 sequences of 8 heads 35 and 24 us, 32 bf16 rows at 60000 tokens of 8 heads 103 and 73 us.  So one
     // while the segments find a CTA each and their pages are few.  (Four tiles measured slower than two everywhere.)
