@@ -7,11 +7,11 @@
 //   warps 0-15       softmax, eight for each tile: two threads own a row (a TMEM lane), each 64 of its scores;
 //                    they agree on the maximum, keep sums of their own and write the fp16 weights back over
 //                    their scores in TMEM, where they are the A operand of the second product
-//   warps 16-23      codes -> fp16 in shared memory, once for both tiles: K and V both as [token][dim] rows with
+//   warps 16-19      codes -> fp16 in shared memory, once for both tiles: K and V both as [token][dim] rows with
 //                    the 128-byte swizzle, K the K-major and V the MN-major B operand
-//   warp 24          issues the MMAs (one thread) and owns the 512 TMEM columns: two score
+//   warp 20          issues the MMAs (one thread) and owns the 512 TMEM columns: two score
 //                    tiles and two outputs of 128 columns each
-//   warp 25          copies the next block's codes (TMA) and prepares its scales
+//   warp 21          copies the next block's codes (TMA) and prepares its scales
 // While one tile's softmax runs, the tensor cores work for the other: for each block they do
 // O += P V (t, j) and S = Q K (t, j + 1), tile after tile, in order, so the next scores may take the
 // place of weights that are still read by the product issued before.
@@ -24,9 +24,9 @@
 // Rows of fp32 keep 22 bits of q and of the weights: a second tile of remainders each, added by a second MMA
 // into the same accumulator.
 //
-// Measured: 8192 rows of 32/8 heads of 128, 0.55 TFLOP: 548 us, 1.0 PFLOP/s (e4m3; int8 570 us, fp32 rows, with twice the
-// MMAs, 910 us).  The MMAs of a block, 32 of 128 x 128 x 16 at 64 cycles, are 2054 of its 4500 cycles; a tile's
-// scores wait for its softmax, whose 64 scores a thread are read twice from TMEM (72 registers a thread leave no room to keep
+// Measured: 8192 rows of 32/8 heads of 128, 0.55 TFLOP: 525 us, 1.05 PFLOP/s (e4m3; int8 535 us, fp32 rows, with twice the
+// MMAs, 884 us).  The MMAs of a block, 32 of 128 x 128 x 16 at 64 cycles, are 2054 of its 4300 cycles; a tile's
+// scores wait for its softmax, whose 64 scores a thread are read twice from TMEM (88 registers a thread leave no room to keep
 // them), so what bounds it is the latency of that turn, with issue slots half used.  Blocks of 64 tokens in two score buffers a
 // tile, which take the turn off the tensor cores, cost more MMA and hand-over time than they hide: 657 us.
 #include "kv8_tc.cuh"
@@ -35,7 +35,16 @@ namespace qd {
 
 namespace {
 
-constexpr int kThreads = 896, kSoftmax = 16, kConvert = 8;  // warps of each kind
+// Warps of each kind, the last group with two that idle.  (Eight that convert, 72 registers a thread: 549 us at 8192 rows,
+// four, 80 registers: 525 us.)
+constexpr int kSoftmax = 16, kConvert = 4, kMmaWarp = kSoftmax + kConvert, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = (kSoftmax + kConvert + 4) * 32;
+// Registers of a thread of each kind: 80 at launch, so 4 softmax + convert + rest groups share 6 x 80.
+template <int HL>
+struct Regs {
+    static constexpr int kOfSoftmax = HL == 2 ? 96 : 88, kOfConvert = HL == 2 ? 56 : 72, kOfRest = HL == 2 ? 40 : 56;
+    static_assert(4 * kOfSoftmax + kOfConvert + kOfRest <= 6 * 80, "no more than the launch has");
+};
 constexpr int kUnits = 2;              // of codes: the next block's K and V
 constexpr int kMaxLogSplit = 3, kLeastBlocks = 6;  // CTAs of a cluster (log2), and from how many blocks on
 constexpr int kQExp = 12;              // q is scaled so that a row's largest element is in [2^12, 2^13)
@@ -306,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         b.abort = 0;
         mbar_fence_init();
     }
-    if (warp == 24) tmem_alloc(&b.tmem, 512);
+    if (warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
 
     if (warp < kSoftmax) {
         // ================= softmax =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<HL>::kOfSoftmax));
         const int t = warp >> 3, half = (warp >> 2) & 1, q = warp & 3, r = 32 * q + lane;
         const int64_t rr = r0 + t * kTile + r;
         const int tok = (int)min(rr / G, (int64_t)INT32_MAX), h = head * G + (int)(rr % G);
@@ -438,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         }
     } else if (warp < kSoftmax + kConvert) {
         // ================= codes -> fp16 =================
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<HL>::kOfConvert));
         const Pieces<D, kConvert * 32> pieces{(int)threadIdx.x - kSoftmax * 32};
         for (int j = 0; j < nb; ++j) {
             const int st = j % C::kStages, left = seen - j * kTile;
@@ -454,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             if (lane == 0) mbar_arrive(&b.v_full[st]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 24 && nb > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<HL>::kOfRest));
+        if (warp == kMmaWarp && nb > 0) {
             // ================= MMA =================
             const uint32_t id_s = umma_idesc_f16_f32(kTile, kTile);
             const uint32_t id_o = umma_idesc_f16_f32(kTile, D) | kIdescBMn;
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             __syncwarp();
             if (!tc_wait(&b.done, 0, nullptr)) fail();
         }
-        if (warp == 25) {
+        if (warp == kCopyWarp) {
             // ================= copies =================
             int issued = 0;
             feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride + (int64_t)b0 * kBlockPages, head, nb, seen, 0, b.codes, units, issued, wait_warp);
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 24) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }
@@ -571,7 +580,7 @@ cudaError_t prompt(cudaStream_t s, int n_sm, Kv8AttnArgs a) {
     const int64_t items = (int64_t)a.n_rows * G / (2 * kTile) + a.c.n_seqs, ctas = items * a.c.n_kv_heads;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
     // Clusters as long as all CTAs find an SM and the longest sequence that the table can hold has a block for each.  8 K/V
-    // heads, with and without: 200 rows at 20000 tokens 101 and 318 us, 60 at 2000 28 and 48 us; at 512 rows and tokens
+    // heads, with and without: 200 rows at 20000 tokens 98 and 318 us, 60 at 2000 28 and 48 us; at 512 rows and tokens
     // (4 blocks) 26.8 and 25.5 us, so not there.
     const int64_t blocks = (int64_t)a.c.table_stride / kBlockPages;
     a.log_split = 0;
