@@ -48,7 +48,9 @@ struct Cfg {
     static constexpr int kQ = NT == 1 ? 0 : NT * (D / 16) * 32 * (HL ? 16 : 8);  // B fragments of q
     static constexpr int kBytes = kMerge + kQ;
 };
-constexpr int kGroupJoin = 8, kMaxJoin = 20;  // partial results joined at once
+// Partial results joined at once: up to kMaxJoin in one step, else in groups.  (4096 tokens of 4 heads, 22 parts a head: in one
+// step 10.8 us, in groups of 8 11.2.)
+constexpr int kGroupJoin = 8, kMaxJoin = 24;
 // weights are exp2(s - m) rel 2^kLift, s <= m + kLag, rel <= kWindow: at most 2^15
 constexpr float kLag = 4.f, kLift = 7.f, kWindow = 16.f;
 
