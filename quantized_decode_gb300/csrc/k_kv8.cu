@@ -18,7 +18,7 @@ constexpr int kWarps = 4;  // a CTA: small, so that few rows still spread over m
 // so that the two elements of a pair are in one lane.  The angles depend on the row and the lane alone: each of the
 // D / 2 is computed once in a warp and handed round.  In turns it is pos * turns[i] modulo 1, in 64-bit
 // integers exact at any position; its top 32 bits go to sincospif.  8191 rows of 32 + 8 heads of 128 in bf16 (168 MB):
-// 31.5 us, 5.3 TB/s, bound by memory; one row 2.3 us, bound by its chain of loads.
+// 31.8 us, 5.3 TB/s, bound by memory; one row 2.5 us, bound by its chain of loads.
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32) k_qk_norm_rope(const __grid_constant__ RopeArgs a) {
@@ -222,8 +222,8 @@ struct Largest<float> {
 
 // Append: the block's rows stay in registers between the maximum and the codes.  What is rare (codes that were there
 // before, scales outside the plain range) is in loops that are not unrolled: a warp lives for about a
-// thousand instructions, and fetching them is part of its time.  10491 rows of 8 heads of 128 in bf16 (64 MB): 11.2 us,
-// 5.8 TB/s; one row 3.1 us.
+// thousand instructions, and fetching them is part of its time.  10491 rows of 8 heads of 128 in bf16 (64 MB): 14.9 us,
+// 4.3 TB/s from memory (11.2 us with the rows in L2): a warp's chain of loads, two and a half waves of warps; 8 rows 2.9 us.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const __grid_constant__ Kv8RowsArgs a) {
     using R = RowType<T>;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_kv8_append(const __grid_constan
     if (lane == 0 && (slot0 == 0 || grown)) *scale_at = scale;
 }
 
-// Read: a lane turns the codes of one 16-byte piece of a row.  228 MB to fp32 rows: 37.8 us, 6.0 TB/s, bound by memory.
+// Read: a lane turns the codes of one 16-byte piece of a row.  228 MB to fp32 rows: 38.5 us, 5.9 TB/s, bound by memory.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kWarps * 32) k_kv8_read(const __grid_constant__ Kv8RowsArgs a) {
     using R = RowType<T>;

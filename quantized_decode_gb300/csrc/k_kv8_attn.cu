@@ -25,7 +25,7 @@
 // to arrive (a counter) joins them in the order of the parts: the result does not depend on who is last.
 //
 // Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 91 us, 5.9 TB/s, 90 us for e4m3;
-// 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 34 us; one of 4096 tokens (28/4, fp32 rows)
+// 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 36 us; one of 4096 tokens (28/4, fp32 rows)
 // 11 us.  The long ones are bound by memory and the latency of loads over 12 warps an SM (without the prefetch of the next pages
 // into L2 107 us), the short ones by the chain from the lengths over the table and the pages to two joins.
 #include "kv8.cuh"
