@@ -102,8 +102,8 @@ def attention_bounds(dtype, out, lse, absv, sumv, absqk, kv):
     A = sum |q_i k_i| / sqrt(d).  exp2 adds 2^-22, the split weights 2^-22: a weight is off by e = A 36 2^-23 + 2^-21 of itself,
     the output by 2 e of sum w|v| (numerator and denominator), and by its own additions: at most kv / 16 pages and 400 joined
     parts, 2^-23 of sum w|v| each.  A weight is also a pair of fp16 numbers, which have no spacing below 2^-24: next to a
-    largest weight of 1 or more, the smallest are off by up to 2^-25 for 16-bit rows and by 2^-32 for fp32 ones (the second
-    half is 2^-11 finer, or both are lifted by 2^8 and lag by at most 2), whatever their own size.  16-bit rows: products with fp16 weights of 11 bits, 2^-11 of sum w|v|, and the rounding of
+    largest weight of 1 or more, the smallest are off by up to 2^-25 for 16-bit rows and by 2^-32 for fp32 ones (which are
+    lifted by 2^7 at least before they are rounded), whatever their own size.  16-bit rows: products with fp16 weights of 11 bits, 2^-11 of sum w|v|, and the rounding of
     the result, half a step (2^-25 at least in fp16).  lse: the scores' absolute error, plus 2^-22 of itself and 2^-21 for the logarithm of the sum."""
     e = absqk[..., None] * 36 * 2.0 ** -23 + 2.0 ** -21
     tol = absv * (2 * e + (kv / 16 + 400) * 2.0 ** -23) + sumv * 2.0 ** (-32 if dtype == "f32" else -25)
