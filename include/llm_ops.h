@@ -235,9 +235,10 @@ int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32
  * row at a negative position (more rows than kv_len) sees nothing: out 0, lse
  * -infinity.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
  * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
- * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32; with fp32 rows
- * the products carry 22 bits of q and of the weights, with 16-bit rows q exactly
- * and 11 bits of the weights at least.  Results do not depend on the run.
+ * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32.  The
+ * products carry q exactly with 16-bit rows and in 22 bits with fp32 rows, and the
+ * weights in 22 bits with fp32 rows and, where n_rows * Hq/Hkv <= 48 * n_seqs (steps
+ * and drafts), with fp16 rows, else in 11.  Results do not depend on the run.
  * Hq % Hkv == 0, Hq/Hkv <= 8.  workspace: device, 256-byte aligned, zero-filled
  * once before its first use; every call leaves it ready for the next.  Calls that
  * may run at the same time (two streams, two graphs) need workspaces of their own. */

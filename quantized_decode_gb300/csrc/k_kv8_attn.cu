@@ -7,8 +7,10 @@
 //   O^T[dim][row] += V^T w^T     A = the page's V codes, transposed, B = the weights
 // so a page's codes fill the 16 rows of A and no product is wasted.  The weights leave the first product in the layout
 // of a result; movmatrix turns them into B.  Codes are exact in fp16.  q is scaled by a power of two so that its
-// largest element is in [2^12, 2^13); for rows of fp32 what fp16 rounds off of q and of the weights
-// is a second B, so both keep 22 bits.  The K scale multiplies the scores of its page, the V scale, relative to a power
+// largest element is in [2^12, 2^13).  What fp16 rounds off is a second B: of q for rows of fp32, of the weights
+// for fp32 and fp16 rows, so that they keep 22 bits.  (With weights of 11 bits, results of fp16 rows were 1.3 to 1.5 times as
+// far off as their own rounding makes them, 4 x 131072 tokens in 91 us instead of 95; bf16's rounding is eight times as
+// coarse, and 11 bits add 1% to its error.)  The K scale multiplies the scores of its page, the V scale, relative to a power
 // of two `vref` that follows it, the weights.  The softmax is the usual single pass in base 2, but the
 // maximum that it refers to moves only where a score is more than 2^4 above it: one vote per page
 // instead of a reduction, and the output is rarely rescaled.
@@ -24,7 +26,7 @@
 // segment of one part is written at once; else its parts leave partial results in the workspace, and the last
 // to arrive (a counter) joins them in the order of the parts: the result does not depend on who is last.
 //
-// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 91 us, 5.9 TB/s, 90 us for e4m3;
+// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 95 us, 5.7 TB/s;
 // 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 36 us; one of 4096 tokens (28/4, fp32 rows)
 // 11 us.  The long ones are bound by memory and the latency of loads over 12 warps an SM (without the prefetch of the next pages
 // into L2 107 us), the short ones by the chain from the lengths over the table and the pages to two joins.
@@ -34,8 +36,8 @@ namespace qd {
 
 namespace {
 
-// NT tiles of 8 rows: one with 12 warps of 168 registers, or two with 8 of 255.  (4 sequences of 131072 tokens, 16-bit rows:
-// 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141: the four schedulers want
+// NT tiles of 8 rows: one with 12 warps of 168 registers, or two with 8 of 255.  (4 sequences of 131072 tokens, 16-bit rows
+// with weights of 11 bits: 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141: the four schedulers want
 // equal shares.)
 template <int D, int NT, bool HL>
 struct Cfg {
@@ -214,15 +216,15 @@ QD_DEV Cut cut_line(const Kv8AttnArgs &a, int G, int least, int32_t *err) {
     return r;
 }
 
-// HL: rows of fp32.
-template <int D, int FMT, int NT, bool HL>
+// HL: rows of fp32, whose q is a pair.  WL: weights are pairs, for fp32 and fp16 rows.
+template <int D, int FMT, int NT, bool HL, bool WL>
 __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(const __grid_constant__ Kv8AttnArgs a) {
     using C = Cfg<D, NT, HL>;
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads, R = C::kRows, Q4 = D / 4;
     constexpr int KP = D / 64;      // 16-byte pieces of a token's K that a lane holds
     constexpr int VB = D / 8;       // bytes of a token's V that a lane holds (16 or 8)
     constexpr int OT = D / 16;      // output tiles of 16 dims
-    constexpr int NB = HL ? 2 : 1;  // Bs of a product
+    constexpr int NB = HL ? 2 : 1, NW = WL ? 2 : 1;  // Bs of the two products
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_fac[R];
     __shared__ float2 s_ml[kWarps][R];
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             }
             if (vs == 0.f) rel = 0.f;
             const bool edge = t0 + kKv8Page > shortest || !there;  // some row does not see all of the page
-            uint32_t pb[NT][NB][2];
+            uint32_t pb[NT][NW][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if (t >= nt) continue;
@@ -520,11 +522,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (HL) {
+                    if (WL) {
                         uint32_t hi, lo;
                         split2(p[2 * h], p[2 * h + 1], hi, lo);
                         pb[t][0][h] = transpose8(hi);
-                        pb[t][NB - 1][h] = transpose8(lo);
+                        pb[t][NW - 1][h] = transpose8(lo);
                     } else {
                         pb[t][0][h] = transpose8(h2_as_u32(__floats2half2_rn(p[2 * h], p[2 * h + 1])));
                     }
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                     for (int t = 0; t < NT; ++t)
                         if (t < nt) {
 #pragma unroll
-                            for (int x = 0; x < NB; ++x) mma16816(o[t][2 * w + y], af, pb[t][x][0], pb[t][x][1]);
+                            for (int x = 0; x < NW; ++x) mma16816(o[t][2 * w + y], af, pb[t][x][0], pb[t][x][1]);
                         }
                 }
             }
@@ -672,10 +674,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
     }
 }
 
-template <int D, int FMT, int NT, bool HL>
+template <int D, int FMT, int NT, bool HL, bool WL>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
     using C = Cfg<D, NT, HL>;
-    auto kernel = k_kv8_attend<D, FMT, NT, HL>;
+    auto kernel = k_kv8_attend<D, FMT, NT, HL, WL>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
     if (e != cudaSuccess) return e;
     // no more CTAs than there can be parts of the longest sequences
@@ -692,8 +694,9 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv8AttnArgs &a) {
     // while the segments find a CTA each and their pages are few.  (Four tiles measured slower than two everywhere.)
     const int64_t rows = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads), segs = (rows + 7 * (int64_t)a.c.n_seqs) / 8 * a.c.n_kv_heads;
     const bool one = rows <= (int64_t)8 * a.c.n_seqs || (segs <= n_sm && segs * a.c.table_stride <= (int64_t)256 * n_sm);
-    if (a.dtype == LLM_DTYPE_F32) return one ? attend<D, FMT, 1, true>(s, n_sm, a) : attend<D, FMT, 2, true>(s, n_sm, a);
-    return one ? attend<D, FMT, 1, false>(s, n_sm, a) : attend<D, FMT, 2, false>(s, n_sm, a);
+    if (a.dtype == LLM_DTYPE_F32) return one ? attend<D, FMT, 1, true, true>(s, n_sm, a) : attend<D, FMT, 2, true, true>(s, n_sm, a);
+    if (a.dtype == LLM_DTYPE_F16) return one ? attend<D, FMT, 1, false, true>(s, n_sm, a) : attend<D, FMT, 2, false, true>(s, n_sm, a);
+    return one ? attend<D, FMT, 1, false, false>(s, n_sm, a) : attend<D, FMT, 2, false, false>(s, n_sm, a);
 }
 
 }  // namespace
