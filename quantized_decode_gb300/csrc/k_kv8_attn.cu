@@ -459,7 +459,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
             float rel = vs * vinv, move = 1.f;
             if (there && vs > 0.f && vs < INFINITY && !(rel <= kWindow && rel >= 1.f / kWindow)) {
                 const int e = min(max((int)(__float_as_uint(vs) >> 23) - 127, -126), 126);
-                const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vtop * 7.8886091e-31f);  // 2^-100: outputs stay finite
+                // Not below 2^-70 of vtop: a token adds 2^24 units at most (weight 2^15, code 2^9), so before 2^31 tokens
+                // |o| vref <= 2^55 vtop, and |o| stays below 2^125 when its unit moves.
+                const float to = fmaxf(__uint_as_float((uint32_t)(127 + e) << 23), vtop * 8.4703295e-22f);
                 vtop = fmaxf(vtop, to);
                 move = vref / to;
                 vref = to;

@@ -61,3 +61,54 @@ def test_fp16_steps_and_drafts_are_as_exact_as_their_rounding(fmt, Hq, Hkv, d, r
     off = np.abs(out - ref[0]) / (tol + np.abs(ref[0]) * 2.0 ** -11 + 2.0 ** -25)
     assert np.all(off <= 1), (float(off.max()), float(np.mean(off > 1)))
     assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
+# ---------------------------------------------------------------- V scales far apart
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 4, 12])
+def test_a_tiny_scale_after_many_large_ones(fmt, dtype, rows):
+    """Every warp goes through two pages of scale 1, eighty or more of scale 15 whose codes are the largest and of one sign
+    in each dim, and then pages of 2^-110: the sum so far must not leave fp32's range when its unit moves.  20
+    sequences of 8 heads, so that no segment is cut: its 1008 pages go round the 8 or 12 warps of one CTA."""
+    rng = np.random.default_rng(51)
+    n, Hkv, d, pages = 20, 8, 64, 1008
+    sign = np.where(rng.random((Hkv, 1, d)) < 0.5, -1, 1)
+    v = np.broadcast_to(sign * float(kv8.CODE_MAX[fmt]), (pages, Hkv, 16, d)).astype(np.float32)
+    host = host_cache(rng, fmt, pages, Hkv, d)
+    host["v"] = kv8.encode(v, fmt)
+    host["ks"][:] *= np.float32(2.0 ** -6)  # near even weights
+    host["vs"][:24], host["vs"][24:-24], host["vs"][-24:] = 1, 15, np.float32(2.0 ** -110)
+    table = np.broadcast_to(np.arange(pages, dtype=np.int32), (n, pages))
+    q = _rand(rng, (rows, Hkv, d), dtype)
+    out, lse = _call(DeviceCache(host, table), dtype, q.repeat(n, 1, 1), (rows,) * n, (16 * pages,) * n)
+    ref = kv8.attention(host, table, [0, rows], [16 * pages], as_f32(q))
+    tol, ltol = _bounds(dtype, ref, 16 * pages)
+    for i in range(n):
+        assert np.all(np.abs(out[i * rows:(i + 1) * rows] - ref[0]) <= tol)
+        assert np.all(np.abs(lse[i * rows:(i + 1) * rows] - ref[1]) <= ltol)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", "f32"), ("e4m3", "f16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("rows", [1, 12])
+@pytest.mark.parametrize("spread", [3, 10, 40])
+def test_scales_far_apart_in_long_sequences(fmt, dtype, rows, spread):
+    """Dozens of pages to a warp, whose V scales wander by up to 2^(2 spread), with zeros and missing K scales."""
+    rng = np.random.default_rng(52 + spread)
+    n, Hkv, d, pages = 8, 4, 64, 1200
+    host = host_cache(rng, fmt, pages, Hkv, d)
+    host["vs"] *= np.float32(2.0) ** rng.integers(-spread, spread + 1, host["vs"].shape).astype(np.float32)
+    host["vs"][rng.random(host["vs"].shape) < 0.05] = 0
+    host["ks"][rng.random(host["ks"].shape) < 0.05] = 0
+    table = np.stack([rng.permutation(pages).astype(np.int32) for _ in range(n)])
+    kv = tuple(int(x) for x in rng.integers(12000, 16 * pages + 1, n))
+    q = _rand(rng, (n * rows, Hkv, d), dtype, 0.5)
+    if dtype == "f16":  # outputs within fp16's range
+        host["vs"] *= np.float32(2.0 ** -(spread + 6))
+    out, lse = _call(DeviceCache(host, table), dtype, q, (rows,) * n, kv)
+    ref = kv8.attention(host, table, starts((rows,) * n), kv, as_f32(q))
+    tol, ltol = _bounds(dtype, ref, max(kv))
+    assert np.all(np.abs(out - ref[0]) <= tol), float((np.abs(out - ref[0]) / tol).max())
+    assert np.all(np.abs(lse - ref[1]) <= ltol)
