@@ -177,7 +177,7 @@ typedef struct llm_kv8_cache {
     int32_t head_dim;           /* d: 64 or 128                                   */
     int32_t n_pool_pages;       /* pages in the pools                             */
     void *k_codes, *v_codes;    /* 8-bit [n_pool_pages][Hkv][16][d]               */
-    float *k_scale, *v_scale;   /* [n_pool_pages][Hkv]                            */
+    float *k_scale, *v_scale;   /* [n_pool_pages][Hkv], finite and >= 0, or NaN   */
     const int32_t *page_table;  /* [n_seqs][table_stride], logical -> physical page */
     int32_t n_seqs;             /* 1..4096                                        */
     int32_t table_stride;       /* logical pages of a sequence at most, 1..2^27 - 1 */
@@ -233,7 +233,8 @@ int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32
  *   lse[h] = log sum_t exp(q_h . K[g][t] / sqrt(d)).
  * One row per sequence is a decode step; more are drafted tokens or a prompt.  A
  * row at a negative position (more rows than kv_len) sees nothing: out 0, lse
- * -infinity.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
+ * -infinity.  A NaN scale of a V block that a row sees makes NaN of out and not of
+ * lse, of a K block of both.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
  * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
  * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32.  The
  * products carry q exactly with 16-bit rows and in 22 bits with fp32 rows, and the

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             if (lane == 0) mbar_arrive(&b.q_full);
 
             float m = -INFINITY, l = 0.f, vref = 0.f;
-            bool fine = true;
+            bool fine = true, sees_nan = false;
             // a warp whose rows all see a block whole has nothing to mask
             const int shortest = __reduce_min_sync(kFullMask, limit);
             auto other = [&](float x, int j) {  // what the row's other thread brings to its j-th call
@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 if (!fine) break;
                 tc_fence_after();
                 const bool cut = shortest - j * kTile < kTile || rec.ok != 0xffu;
+                if (rec.ok >> kNanBit) sees_nan |= kKv8Page * (__ffs(rec.ok >> kNanBit) - 1) < limit - j * kTile;
                 const float vmove = rec.move;
                 vref = rec.vref;
                 auto agree = [&](float x) { return fmaxf(x, other(x, j)); };
@@ -419,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             tc_fence_after();
             if (fine) l += other(l, nb);
             // ---- these keys' result, to where it belongs or to be joined
-            const float k = !fine || l == 0.f ? 0.f : vref / l;
+            const bool none = !fine || l == 0.f;
+            const float k = sees_nan ? __uint_as_float(0x7fffffffu) : vref / l;
             const int row = t * kTile + r;
             const int64_t out = (int64_t)(s.row0 + tok) * a.Hq + h;
             const float log_sum = !fine || l == 0.f ? -INFINITY : m + (log2f(l) - kLift);
@@ -428,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 float v[32];
                 tmem_ld32(o_at(t) + lanes + 32 * i, v);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = k == 0.f ? 0.f : v[e] * k;
+                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
                 put_row32<D>(a, res, row, live, out * D, 32 * i, v);
             }
             if (half == 0) {

@@ -140,19 +140,20 @@ QD_DEV void codes_f16(const uint4 &u, __half2 h2, bool scaled, uint4 &lo, uint4 
 // What the softmax has to know of a block's pages.  V's scale is split: vs / vref = r 2^-k; 2^-k goes into
 // V's fp16 values (exact for k <= 15), log2 r into the exponent of the weights, and a page's share of their sum
 // is divided by r again.
-constexpr int kRecs = 4;
+constexpr int kRecs = 4, kNanBit = 8;
 struct BlockRec {
     struct __align__(16) Page {
         float ks, lr, ir, mul;  // K scale, log2 r, 1 / r, 2^-k
     } page[kBlockPages];
     float move, vref;  // factor of the output when vref changed with this block; vref
-    uint32_t ok;       // pages that are there
+    uint32_t ok;       // pages that are there; from bit kNanBit on those whose V scale is NaN
     uint32_t scaled;   // some mul is not 1
 };
 
 // The split of a block's V scales against vref, which all lanes keep alike; lane p % 8 holds page p.
 // vref is a power of two that follows the scales where they leave [2^-14, 2^4] of it, but not below 2^-60 of the largest
-// one so far (vtop): outputs in its units stay finite.  Scales below 2^-100 of it count as 0.
+// one so far (vtop): outputs in its units stay finite.  Scales below 2^-100 of it count as 0.  One that is NaN counts as
+// vref here, since lse has nothing to do with it: the rows that see its page become NaN at their end.
 struct VSplit {
     float r, mul, move;  // mul = 2^-k, 0 for a scale of 0
 };
@@ -169,6 +170,7 @@ QD_DEV VSplit split_scale(float vs, float &vref, float &vtop) {
         vref = to;
         vtop = fmaxf(vtop, to);
     }
+    if (!(vs < INFINITY)) return VSplit{1.f, 1.f, o.move};
     o.r = vs / vref;
     const bool none = vs == 0.f || o.r < 7.8886091e-31f;  // 2^-100
     if (none) o.r = 1.f;
@@ -249,10 +251,11 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
             rec.page[lane] = BlockRec::Page{ks, log2f(v.r), 1.f / v.r, v.mul};
         }
         const bool scaled = __any_sync(kFullMask, v.mul != 1.f && ph >= 0);
+        const uint32_t nans = __ballot_sync(kFullMask, !(vs < INFINITY)) & 0xffu;
         if (lane == 0) {
             rec.move = v.move;
             rec.vref = vref;
-            rec.ok = ok;
+            rec.ok = ok | nans << kNanBit;
             rec.scaled = scaled;
         }
         __syncwarp();

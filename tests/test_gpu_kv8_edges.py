@@ -112,3 +112,76 @@ def test_scales_far_apart_in_long_sequences(fmt, dtype, rows, spread):
     tol, ltol = _bounds(dtype, ref, max(kv))
     assert np.all(np.abs(out - ref[0]) <= tol), float((np.abs(out - ref[0]) / tol).max())
     assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
+# ---------------------------------------------------------------- blocks that are not finite
+
+NAN_CALLS = {  # rows, length, capacity of the table
+    "step": (1, 300, 300),
+    "draft": (4, 300, 300),
+    "long draft": (30, 300, 300),
+    "prompt": (200, 300, 300),
+    "prompt of few rows over many keys": (120, 3000, 5008),
+}
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "f32"), ("int8", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (2, 2, 128)])
+@pytest.mark.parametrize("call", list(NAN_CALLS))
+def test_a_nan_block_of_v_leaves_lse_alone(fmt, dtype, Hq, Hkv, d, call):
+    """V's scale has no part in lse: where it is NaN, out is NaN for the rows that see the block, and lse stays what q and
+    K make it."""
+    rng = np.random.default_rng(54)
+    rows, kv, most = NAN_CALLS[call]
+    table, pages = page_table(rng, [kv], capacity=[most])
+    host = host_cache(rng, fmt, pages, Hkv, d)
+    q = _rand(rng, (rows, Hq, d), dtype, 2.0)
+    ref = kv8.attention(host, table, [0, rows], [kv], as_f32(q))
+    tol, ltol = _bounds(dtype, ref, kv)
+    for page in (0, (kv - rows // 2 - 1) // 16, (kv - 1) // 16):
+        bad = {**host, "vs": host["vs"].copy()}
+        bad["vs"][table[0, page], 1] = np.nan
+        out, lse = _call(DeviceCache(bad, table), dtype, q, (rows,), (kv,))
+        hit = np.zeros((rows, Hq), bool)
+        hit[max(0, 16 * page - (kv - rows)):, Hq // Hkv:] = True
+        assert np.all(np.isnan(out[hit])) and np.all((np.abs(out - ref[0]) <= tol)[~hit])
+        assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
+@pytest.mark.parametrize("rows", [1, 12, 200])
+def test_nothing_but_nan_and_zero_blocks_of_v(rows):
+    """No V scale that could be a unit: all of them NaN or 0, in one order and the other."""
+    rng = np.random.default_rng(55)
+    Hq, Hkv, d, kv = 4, 2, 64, 260
+    table, pages = page_table(rng, [kv])
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    q = _rand(rng, (rows, Hq, d), "f32", 2.0)
+    for pattern in (lambda p: np.nan, lambda p: np.nan if p < 8 else 0.0, lambda p: 0.0 if p < 8 else np.nan,
+                    lambda p: np.nan if p == 0 else 1e-30):
+        host["vs"][table[0]] = np.array([pattern(p) for p in range(table.shape[1])], np.float32)[:, None]
+        out, lse = _call(DeviceCache(host, table), "f32", q, (rows,), (kv,))
+        with np.errstate(invalid="ignore"):
+            ref = kv8.attention(host, table, [0, rows], [kv], as_f32(q))
+        ltol = _bounds("f32", ref, kv)[1]
+        np.testing.assert_array_equal(np.isnan(out), np.isnan(ref[0]))
+        fine = ~np.isnan(ref[0])
+        assert np.all(out[fine] == 0) and np.all(ref[0][fine] == 0)
+        assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
+@pytest.mark.parametrize("rows", [1, 12, 200])
+def test_a_nan_block_of_k_makes_nan_of_out_and_lse(rows):
+    rng = np.random.default_rng(56)
+    Hq, Hkv, d, kv = 4, 2, 64, 300
+    table, pages = page_table(rng, [kv])
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    q = _rand(rng, (rows, Hq, d), "f32", 2.0)
+    ref = kv8.attention(host, table, [0, rows], [kv], as_f32(q))
+    tol, ltol = _bounds("f32", ref, kv)
+    page = (kv - rows // 2 - 1) // 16
+    host["ks"][table[0, page], 0] = np.nan
+    out, lse = _call(DeviceCache(host, table), "f32", q, (rows,), (kv,))
+    hit = np.zeros((rows, Hq), bool)
+    hit[max(0, 16 * page - (kv - rows)):, :Hq // Hkv] = True
+    assert np.all(np.isnan(out[hit])) and np.all(np.isnan(lse[hit]))
+    assert np.all((np.abs(out - ref[0]) <= tol)[~hit]) and np.all((np.abs(lse - ref[1]) <= ltol)[~hit])
