@@ -131,6 +131,7 @@ QD_DEV bool kv8_item(const Kv8RowsArgs &a, Kv8Item &it) {
     const int per = 2 * a.c.n_kv_heads, lane = threadIdx.x & 31, B = a.c.n_seqs;
     const int64_t item = id / per;
     if (item >= kv8_items(a.n_rows, B)) return false;
+    if (id < (B + 31) / 32) kv8_check_seqs(a.row_start, a.kv_len, a.n_rows, a.c, (int)id, true, a.err);
     const int in = (int)(id - item * per);
     it.is_v = in & 1;
     it.head = in >> 1;
@@ -153,7 +154,6 @@ QD_DEV bool kv8_item(const Kv8RowsArgs &a, Kv8Item &it) {
     }
     const Kv8Seq s = kv8_seq(start, next, kv, a.n_rows, a.c.table_stride);
     it.span = kv8_span(s, item - kv8_item_base(start, b));
-    if ((!s.ok || s.rows > s.kv) && lane == 0) kv8_report(a.err);
     it.entry = a.c.page_table + (int64_t)b * a.c.table_stride + it.span.page;
     return it.span.count != 0;
 }

@@ -285,9 +285,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         }
     }
     const Kv8Seq s = attn_seq(a, seq);
-    if (!s.ok && threadIdx.x == 0) kv8_report(a.err);
     const int64_t pair = item - ((int64_t)s.row0 * G / (2 * kTile) + seq);
     const int64_t pairs_rows = (int64_t)s.rows * G - pair * (2 * kTile);  // rows of this item, and behind it
+    if (warp == kCopyWarp + 1 && blockIdx.x < (a.c.n_seqs + 31u) / 32)  // one that idles; there are more CTAs than sequences
+        kv8_check_seqs(a.row_start, a.kv_len, a.n_rows, a.c, (int)blockIdx.x, false, a.err);
     if (pair < 0 || pairs_rows <= 0) return;
     const int64_t r0 = pair * (2 * kTile);
     const int nt = pairs_rows > kTile ? 2 : 1;

@@ -114,6 +114,16 @@ QD_DEV int kv8_find_seq(const int32_t *row_start, int n_seqs, int64_t item) {
     return lo;
 }
 
+// Sequences 32 i .. 32 i + 31 that are out of range (or, for `within`, have more rows than tokens) to err, by a warp.  Work
+// items alone would not tell: where row_start falls, the search above may pass a sequence over.
+QD_DEV void kv8_check_seqs(const int32_t *row_start, const int32_t *kv_len, int n_rows, const llm_kv8_cache &c, int i, bool within,
+                           int32_t *err) {
+    const int b = 32 * i + (threadIdx.x & 31);
+    if (b >= c.n_seqs) return;
+    const Kv8Seq s = kv8_seq(__ldg(row_start + b), __ldg(row_start + b + 1), __ldg(kv_len + b), n_rows, c.table_stride);
+    if (!s.ok || (within && s.rows > s.kv)) kv8_report(err);
+}
+
 // ---- attention
 constexpr float kLog2e = 1.4426950408889634f;
 QD_DEV float ex2(float x) {

@@ -185,3 +185,33 @@ def test_a_nan_block_of_k_makes_nan_of_out_and_lse(rows):
     hit[max(0, 16 * page - (kv - rows)):, :Hq // Hkv] = True
     assert np.all(np.isnan(out[hit])) and np.all(np.isnan(lse[hit]))
     assert np.all((np.abs(out - ref[0]) <= tol)[~hit]) and np.all((np.abs(lse - ref[1]) <= ltol)[~hit])
+
+
+# ---------------------------------------------------------------- numbers out of order, calls after a failure
+
+FALLING = {  # row_start with a sequence that ends before it begins, no work item of which there is
+    "3 sequences": [0, 64, 32, 64],
+    "40 sequences": [0, 64, 32] + list(range(64, 102)),
+    "a prompt among 3": [0, 512, 300, 600],
+    "a prompt among 40": [0, 2560, 2304] + list(range(2600, 2638)),
+}
+
+
+@pytest.mark.parametrize("call", list(FALLING))
+def test_row_starts_that_fall_are_reported(call):
+    rng = np.random.default_rng(57)
+    rs = FALLING[call]
+    n, B, Hkv, d = rs[-1], len(rs) - 1, 2, 64
+    most = -(-n // 16)
+    table, pages = page_table(rng, [n] * B)  # pages of their own, as append wants them
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    r, lens = ints(rs), ints([n] * B)
+    x = _rand(rng, (n, 2, Hkv, d), "f32")
+    out = torch.zeros(n, Hkv, d, device="cuda")
+    for op in ("read", "attention", "append"):
+        dev = DeviceCache(host, table)
+        if op == "attention":
+            assert dev.attention("f32", x[:, 0], r, lens, out) == 0
+        else:
+            assert getattr(dev, op)("f32", x[:, 0], x[:, 1], r, lens) == 0
+        assert dev.err.item() == L.LLM_ERR_DEVICE, op
