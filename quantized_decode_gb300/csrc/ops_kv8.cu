@@ -34,13 +34,17 @@ bool cache_ok(const llm_kv8_cache *c) {
 
 bool opt_aligned(const void *p, size_t a) { return !p || aligned(p, a); }
 
-int status(cudaError_t e) { return e == cudaSuccess ? LLM_OK : LLM_ERR_CUDA; }
+// The runtime keeps a failed call's error until it is asked for; the next call's launch, which asks, must not find it.
+int status(cudaError_t e) {
+    if (e == cudaSuccess) return LLM_OK;
+    cudaGetLastError();
+    return LLM_ERR_CUDA;
+}
 
 int sm_count(int *n) {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return LLM_ERR_CUDA;
-    return LLM_OK;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return status(e == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : e);
 }
 
 }  // namespace

@@ -215,3 +215,30 @@ def test_row_starts_that_fall_are_reported(call):
         else:
             assert getattr(dev, op)("f32", x[:, 0], x[:, 1], r, lens) == 0
         assert dev.err.item() == L.LLM_ERR_DEVICE, op
+
+
+def test_a_call_that_failed_does_not_spoil_the_next():
+    """A call into a capture that has been broken off fails; the next one, on a good stream, does not."""
+    rng = np.random.default_rng(58)
+    Hq, Hkv, d, rows = 4, 2, 64, 200
+    table, pages = page_table(rng, [rows])
+    dev = DeviceCache(host_cache(rng, "int8", pages, Hkv, d), table)
+    q, out = _rand(rng, (rows, Hq, d), "f32"), torch.zeros(rows, Hq, d, device="cuda")
+    rs, lens = ints([0, rows]), ints([rows])
+    assert dev.attention("f32", q, rs, lens, out) == 0  # with a workspace
+    torch.cuda.synchronize()
+    with open("/proc/self/maps") as f:
+        path = next(line.split()[-1] for line in f if "libcudart" in line)
+    rt, stream, graph = ctypes.CDLL(path), ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    assert rt.cudaStreamBeginCapture(stream, 2) == 0
+    assert rt.cudaStreamSynchronize(stream) != 0  # not allowed in a capture, which is void from here on
+    assert dev.attention("f32", q, rs, lens, out, stream=stream) == L.LLM_ERR_CUDA
+    rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+    rt.cudaGetLastError()
+    x = _rand(rng, (rows, 2, Hkv, d), "f32")
+    assert dev.append("f32", x[:, 0], x[:, 1], rs, lens) == 0
+    assert dev.attention("f32", q, rs, lens, out) == 0
+    torch.cuda.synchronize()
+    assert rt.cudaStreamDestroy(stream) == 0
+    assert dev.err.item() == 0
