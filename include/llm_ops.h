@@ -159,8 +159,11 @@ int llm_op_gemm_quant(int32_t fmt, const void *A, const void *w, const void *s, 
  * (a sequence with kv_len outside [0, 16 * table_stride], in append and read
  * also one with more rows than kv_len, is left out: nothing of it is read or
  * written, its attention rows are zero; a page outside [0, n_pool_pages) is left
- * out; where row_start falls, rows of other sequences may be left out too).  No
- * call clears it.  Errors returned: LLM_ERR_ARG before any launch, LLM_ERR_CUDA. */
+ * out; where row_start falls, rows of other sequences may be left out too), and
+ * LLM_ERR_TIMEOUT if a wait inside llm_op_kv8_attention ran out (1 s; only a stalled
+ * GPU): out and lse of its rows are then undefined, NaN where the kernel had not
+ * finished a row.  No call clears it.  Errors returned: LLM_ERR_ARG before any
+ * launch, LLM_ERR_CUDA.                                                       */
 #define LLM_KV8_INT8 1 /* codes: int8 in [-127, 127]                            */
 #define LLM_KV8_E4M3 2 /* codes: 8-bit floats (4 exponent, 3 mantissa bits), finite */
 

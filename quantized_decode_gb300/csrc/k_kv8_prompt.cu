@@ -416,16 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p_full[t]);
             }
-            // where the results take the tiles' place, both tiles' products have to be done
-            fine = fine && wait_warp(a.log_split > 0 ? &b.done : &b.o_full[t], 0);
+            // where the results take the tiles' place, both tiles' products have to be done; `done` comes after a wait that
+            // ran out too
+            fine = fine && wait_warp(a.log_split > 0 ? &b.done : &b.o_full[t], 0) && !*abort;
             tc_fence_after();
             if (fine) l += other(l, nb);
             // ---- these keys' result, to where it belongs or to be joined
-            const bool none = !fine || l == 0.f;
-            const float k = sees_nan ? __uint_as_float(0x7fffffffu) : vref / l;
+            const bool none = fine && l == 0.f;
+            const float k = kv8_row_factor(fine && !sees_nan, l, vref);
             const int row = t * kTile + r;
             const int64_t out = (int64_t)(s.row0 + tok) * a.Hq + h;
-            const float log_sum = !fine || l == 0.f ? -INFINITY : m + (log2f(l) - kLift);
+            const float log_sum = kv8_row_log2(fine, l, m - kLift);
 #pragma unroll 1
             for (int i = half * (D / 64); i < (half + 1) * (D / 64); ++i) {
                 float v[32];

@@ -5,6 +5,7 @@
 // trusts those numbers: they come from device memory.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #ifdef __CUDACC__
@@ -66,5 +67,11 @@ KV8_FN Kv8Span kv8_span(const Kv8Seq &s, int64_t j) {
 KV8_FN int kv8_pages(int kv) { return kv > 0 ? (kv - 1) / kKv8Page + 1 : 1; }
 KV8_FN int kv8_blocks(int left, int tokens) { return left > 0 ? (left - 1) / tokens + 1 : 0; }
 KV8_FN bool kv8_page_there(int p, int left) { return left > 0 && p <= (left - 1) / kKv8Page; }
+
+// How a row of the attention ends, from the sum of its weights: what its weighted values, in units of `unit`, are
+// multiplied by, and log2 of the sum above `top`.  0 and -infinity for a row that saw nothing.  whole: every wait
+// on the way has ended in time.  Where one has not, both are NaN, which no call without an error gives where V and K have none.
+KV8_FN float kv8_row_factor(bool whole, float sum, float unit) { return whole ? (sum == 0.f ? 0.f : unit / sum) : NAN; }
+KV8_FN float kv8_row_log2(bool whole, float sum, float top) { return whole ? (sum == 0.f ? -INFINITY : top + log2f(sum)) : NAN; }
 
 }  // namespace qd
