@@ -45,7 +45,6 @@ struct Regs {
     static constexpr int kOfSoftmax = HL == 2 ? 96 : 88, kOfConvert = HL == 2 ? 56 : 72, kOfRest = HL == 2 ? 40 : 56;
     static_assert(4 * kOfSoftmax + kOfConvert + kOfRest <= 6 * 80, "no more than the launch has");
 };
-constexpr int kUnits = 2;              // of codes: the next block's K and V
 constexpr int kMaxLogSplit = 3, kLeastBlocks = 6;  // CTAs of a cluster (log2), and from how many blocks on
 constexpr int kQExp = 12;              // q is scaled so that a row's largest element is in [2^12, 2^13)
 
@@ -55,14 +54,14 @@ struct Cfg {
     static constexpr int kStages = HL == 2 ? 1 : 2;      // of K and of V
     static constexpr int kQ = HL * kP * kPanel;          // bytes of a tile of q
     static constexpr int kKv = kP * kPanel;
-    static constexpr int kTiles = 2 * kQ + 2 * kStages * kKv + kUnits * kTile * D;
+    static constexpr int kTiles = 2 * kQ + 2 * kStages * kKv + 2 * kTile * D;  // and a block's codes
     static constexpr int kRes = D + 4;                   // floats of a row's result, which later take the tiles' place
     static_assert(2 * kTile * (kRes + 1) * 4 <= kTiles, "and log2 of their sums behind them");
 };
 
 struct Bars {
     uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], agree[2][4], done;
-    CodeRing<kUnits> codes;
+    CodeRing codes;
     uint32_t tmem;
     float half[2][2][kTile];  // by tile and half: what the two threads of a row tell each other
     int64_t out_at;              // for the end, out of registers: row and head of the item's first (row, query head) pair,
@@ -539,10 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
         }
         if (warp == kCopyWarp) {
             // ================= copies =================
-            int issued = 0;
-            feed_codes<D, kUnits>(a, a.c.page_table + (int64_t)seq * a.c.table_stride + (int64_t)b0 * kBlockPages, head, nb, seen, 0, b.codes, units, issued, wait_warp);
+            int started[2] = {0, 0};
+            feed_codes<D>(a, a.c.page_table + (int64_t)seq * a.c.table_stride + (int64_t)b0 * kBlockPages, head, nb, seen, b.codes, units, started, wait_warp);
             if (*abort)  // those in flight land before the shared memory goes away
-                for (int u = max(0, issued - kUnits); u < issued; ++u) tc_wait(&b.codes.full[u % kUnits], (uint32_t)(u / kUnits) & 1u, nullptr);
+                for (int x = 0; x < 2; ++x)
+                    if (started[x] > 0) tc_wait(&b.codes.full[x], (uint32_t)(started[x] - 1) & 1u, nullptr);
         }
         __syncwarp();
     }

@@ -183,14 +183,13 @@ QD_DEV VSplit split_scale(float vs, float &vref, float &vtop) {
     return o;
 }
 
-// ---- codes on their way: a ring of UNITS places in shared memory, each the K or the V codes of a block of one
-// head ([page][16][D] bytes).  Copies are the TMA engine's, so many are in flight without registers.
-template <int UNITS>
+// ---- codes on their way: two places in shared memory, the first for the K codes of a block of one head, the second
+// for its V codes ([page][16][D] bytes).  Copies are the TMA engine's, so many are in flight without registers.
 struct CodeRing {
-    uint64_t full[UNITS], empty[UNITS], rec_full[kRecs];
+    uint64_t full[2], empty[2], rec_full[kRecs];
     BlockRec rec[kRecs];
     QD_DEV void init(int converters) {
-        for (int i = 0; i < UNITS; ++i) {
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&full[i], 1);
             ptx::mbar_init(&empty[i], converters);
         }
@@ -203,12 +202,12 @@ QD_DEV void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *b
                  : "memory");
 }
 
-// One warp: the copies and records of the nb blocks from `table` on (the first block's entries), n_done blocks
-// after the ring's first.  `left`: tokens from there on that any row sees.  `wait(bar, phase)`: by the whole warp, false
-// once something timed out.  issued: units whose copies were started, since the ring's first.
-template <int D, int UNITS, typename Wait>
-QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int nb, int left, int n_done, CodeRing<UNITS> &ring,
-                       uint8_t *units, int &issued, Wait wait) {
+// One warp: the copies and records of the nb blocks from `table` on (the first block's entries).  `left`: tokens
+// from there on that any row sees.  `wait(bar, phase)`: by the whole warp, false once something timed out.
+// started: copies of K and of V that were started.
+template <int D, typename Wait>
+QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int nb, int left, CodeRing &ring, uint8_t *units,
+                       int (&started)[2], Wait wait) {
     constexpr uint32_t kPage = kKv8Page * D, kUnit = kBlockPages * kPage;
     const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads;
     // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
@@ -225,28 +224,26 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
     int ph = checked(entry(0)), ph_next = entry(1);
     float ks = scale_of(a.c.k_scale, ph), vs = scale_of(a.c.v_scale, ph), vref = 0.f, vtop = 0.f;
     for (int j = 0; j < nb; ++j) {
-        const int n = n_done + j;
         const uint32_t ok = __ballot_sync(kFullMask, ph >= 0) & 0xffu;
-        auto copy = [&](int x) {  // K or V of block n
-            const uint32_t u = 2 * (uint32_t)n + x, place = u % UNITS, use = u / UNITS;
-            if (use > 0 && !wait(&ring.empty[place], use - 1)) return false;
-            if (lane == 0) ptx::mbar_expect_tx(&ring.full[place], kPage * __popc(ok));
+        auto copy = [&](int x) {  // K or V of block j
+            if (j > 0 && !wait(&ring.empty[x], (uint32_t)j - 1)) return false;
+            if (lane == 0) ptx::mbar_expect_tx(&ring.full[x], kPage * __popc(ok));
             __syncwarp();
-            issued = (int)u + 1;
+            started[x] = j + 1;
             if (lane < kBlockPages && ph >= 0)
-                bulk_load(ptx::smem_u32(units) + place * kUnit + lane * kPage,
-                          (const uint8_t *)(x ? a.c.v_codes : a.c.k_codes) + ((int64_t)ph * Hkv + head) * kPage, kPage, &ring.full[place]);
+                bulk_load(ptx::smem_u32(units) + x * kUnit + lane * kPage,
+                          (const uint8_t *)(x ? a.c.v_codes : a.c.k_codes) + ((int64_t)ph * Hkv + head) * kPage, kPage, &ring.full[x]);
             return true;
         };
         if (!copy(0)) return;
         const int next = checked(ph_next);
         ph_next = entry(j + 2);
         const float ks_next = scale_of(a.c.k_scale, next), vs_next = scale_of(a.c.v_scale, next);
-        // The unit of K waited for above held block n - 1 (UNITS is 2): its converters had waited for the scores of block
-        // n - 3 at the latest, those for the weights of n - 4, so nobody reads the record of n - kRecs any more
-        static_assert(UNITS == 2 && kRecs == 4, "the argument above");
+        // The place of K waited for above held block j - 1: its converters had waited for the scores of block
+        // j - 3 at the latest, those for the weights of j - 4, so nobody reads the record of j - kRecs any more
+        static_assert(kRecs == 4, "the argument above");
         const VSplit v = split_scale(vs, vref, vtop);
-        BlockRec &rec = ring.rec[n % kRecs];
+        BlockRec &rec = ring.rec[j % kRecs];
         if (lane < kBlockPages) {
             rec.page[lane] = BlockRec::Page{ks, log2f(v.r), 1.f / v.r, v.mul};
         }
@@ -259,7 +256,7 @@ QD_DEV void feed_codes(const Kv8AttnArgs &a, const int32_t *table, int head, int
             rec.scaled = scaled;
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ring.rec_full[n % kRecs]);
+        if (lane == 0) ptx::mbar_arrive(&ring.rec_full[j % kRecs]);
         if (!copy(1)) return;
         ph = next;
         ks = ks_next;
