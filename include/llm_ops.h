@@ -239,10 +239,13 @@ int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32
  * -infinity.  A NaN scale of a V block that a row sees makes NaN of out and not of
  * lse, of a K block of both.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
  * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
- * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32.  The
- * products carry q exactly with 16-bit rows and in 22 bits with fp32 rows, and the
- * weights in 22 bits with fp32 rows and, where n_rows * Hq/Hkv <= 48 * n_seqs (steps
- * and drafts), with fp16 rows, else in 11.  Results do not depend on the run.
+ * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32.
+ * The products take q as it is with 16-bit rows and in 22 bits with fp32 rows, but
+ * nothing below 2^-37 of the row's largest element; and the weights in 22 bits with
+ * fp32 rows and, where n_rows * Hq/Hkv <= 48 * n_seqs (steps and drafts), with fp16
+ * rows, else in 11, but a product with V may be off by 2^-28 of the row's largest
+ * weight times the largest V that the scales of the blocks it sees allow (scale *
+ * 127 or 448).  Results do not depend on the run.
  * Hq % Hkv == 0, Hq/Hkv <= 8.  workspace: device, 256-byte aligned, zero-filled
  * once before its first use; every call leaves it ready for the next.  Calls that
  * may run at the same time (two streams, two graphs) need workspaces of their own. */

@@ -8,12 +8,14 @@
 // so a page's codes fill the 16 rows of A and no product is wasted.  The weights leave the first product in the layout
 // of a result; movmatrix turns them into B.  Codes are exact in fp16.  q is scaled by a power of two so that its
 // largest element is in [2^12, 2^13).  What fp16 rounds off is a second B: of q for rows of fp32, of the weights
-// for fp32 and fp16 rows, so that they keep 22 bits.  (With weights of 11 bits, results of fp16 rows were 1.3 to 1.5 times as
-// far off as their own rounding makes them, 4 x 131072 tokens in 91 us instead of 95; bf16's rounding is eight times as
-// coarse, and 11 bits add 1% to its error.)  The K scale multiplies the scores of its page, the V scale, relative to a power
-// of two `vref` that follows it, the weights.  The softmax is the usual single pass in base 2, but the
-// maximum that it refers to moves only where a score is more than 2^4 above it: one vote per page
-// instead of a reduction, and the output is rarely rescaled.
+// for fp32 and fp16 rows, so that they keep 22 bits.  (With weights of 11 bits, results of fp16 rows were 1.3 to 1.5
+// times as far off as their own rounding makes them, 4 x 131072 tokens in 91 us instead of 95; bf16's rounding is eight
+// times as coarse, and 11 bits add 1% to its error.)  Where it is more, a weight is off by half of fp16's smallest step, 2^-25:
+// next to a largest one of 2^7 or above, and with a factor of 2^-4 or above for V's scale, 2^-28 of the largest.
+// The K scale multiplies the scores of its page, the V scale, relative to a power of two `vref` that follows it,
+// the weights.  The softmax is the usual single pass in base 2, but the maximum that it refers to moves only
+// where a score is more than 2^4 above it: one vote per page instead of a reduction, and the output is rarely
+// rescaled.
 //
 // The layout.  The contraction index of an mma may be permuted freely if both operands agree.  Lane (g = lane / 4,
 // c = lane % 4) reads 16 consecutive code bytes of tokens g and g + 8 for K (dims 16 c + 64 i), which are four
@@ -37,8 +39,8 @@ namespace qd {
 namespace {
 
 // NT tiles of 8 rows: one with 12 warps of 168 registers, or two with 8 of 255.  (4 sequences of 131072 tokens, 16-bit rows
-// with weights of 11 bits: 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141: the four schedulers want
-// equal shares.)
+// with weights of 11 bits: 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141:
+// the four schedulers want equal shares.)
 template <int D, int NT, bool HL>
 struct Cfg {
     static constexpr int kWarps = NT > 1 ? 8 : 12, kThreads = kWarps * 32, kRows = 8 * NT;
@@ -51,7 +53,7 @@ struct Cfg {
     static constexpr int kBytes = kMerge + kQ;
 };
 // Partial results joined at once: up to kMaxJoin in one step, else in groups.  (4096 tokens of 4 heads, 22 parts a head: in one
-// step 10.8 us, in groups of 8 11.2.)
+// step 10.8 us, in groups of 8 11.2.  More parts than that were not measured.)
 constexpr int kGroupJoin = 8, kMaxJoin = 24;
 // weights are exp2(s - m) rel 2^kLift, s <= m + kLag, rel <= kWindow: at most 2^15
 constexpr float kLag = 4.f, kLift = 7.f, kWindow = 16.f;

@@ -159,8 +159,8 @@ QD_DEV void load_q8(const Kv8AttnArgs &a, int64_t at, bool live, float (&v)[8]) 
 }
 
 // Weights are exp2(s - m) 2^kLift, s the score with log2 r, s <= m + kLag: at most 2^15.  Rows of 16 bits lag far
-// and rarely rescale; those of fp32 lift the weights instead, so that the second fp16 half keeps its 11 bits
-// down to 2^-21 of the largest (fp16 has no normal numbers below 2^-14).
+// and rarely rescale; those of fp32 lift the weights instead, so that the pair keeps its 22 bits down to 2^-14 of the
+// largest and is off by 2^-36 of it below (fp16's smallest step is 2^-24).
 template <int HL>
 struct Weights {
     static constexpr float kLag = HL == 2 ? 4.f : 8.f, kLift = HL == 2 ? 11.f : 7.f;

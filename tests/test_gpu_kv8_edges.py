@@ -114,6 +114,25 @@ def test_scales_far_apart_in_long_sequences(fmt, dtype, rows, spread):
     assert np.all(np.abs(lse - ref[1]) <= ltol)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 12, 150])
+def test_small_weights_at_small_scales(fmt, dtype, rows):
+    """V scales just above 1/16 of the first page's, so that the unit stays, and weights down to 2^-24 of the largest."""
+    rng = np.random.default_rng(53)
+    Hkv, d, pages = 2, 64, 400
+    table, total = page_table(rng, [16 * pages])
+    host = host_cache(rng, fmt, total, Hkv, d)
+    host["vs"][:] = np.float32(1 / 15.9)
+    host["vs"][table[0, :64]] = 1
+    q = _rand(rng, (rows, Hkv, d), dtype, 2.0)
+    out, lse = _call(DeviceCache(host, table), dtype, q, (rows,), (16 * pages,))
+    ref = kv8.attention(host, table, [0, rows], [16 * pages], as_f32(q))
+    tol, ltol = _bounds(dtype, ref, 16 * pages)
+    assert np.all(np.abs(out - ref[0]) <= tol)
+    assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
 # ---------------------------------------------------------------- blocks that are not finite
 
 NAN_CALLS = {  # rows, length, capacity of the table
