@@ -193,11 +193,12 @@ typedef struct llm_kv8_cache {
  *   a = pos * rope_base^(-2i/d),  i < d/2.
  * q, k: rows of `dtype`, q_stride and k_stride elements apart, with the heads of a
  * row side by side (so both may lie in the rows of one fused projection); gains:
- * bf16 [d], both or neither NULL; pos: int32 [n]; q_out [n][Hq][d], k_out
- * [n][Hkv][d] of the same type, dense (q_out may be q where q_stride is Hq * d, and
- * k_out k likewise).  Computed in fp32 and rounded once; the angle is reduced in
- * 64-bit integers, so far positions lose nothing.  Rows 16-byte aligned (pointers
- * and strides), d in {64, 128}, eps >= 0, rope_base > 0 and finite, n >= 1.       */
+ * bf16 [d], 16-byte aligned, both or neither NULL; pos: int32 [n]; q_out [n][Hq][d],
+ * k_out [n][Hkv][d] of the same type, dense (q_out may be q where q_stride is Hq * d, and
+ * k_out k likewise).  Computed in fp32 and rounded once, so mean(x^2) has to lie in
+ * its range; the angle is reduced in 64-bit integers, so far positions lose nothing.
+ * Rows 16-byte aligned (pointers and strides), d in {64, 128}, Hq and Hkv in
+ * 1..65536, eps >= 0 and finite, rope_base > 0 and finite, n >= 1.                */
 int llm_op_qk_norm_rope(int32_t dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                         const void *q_gain, const void *k_gain, float eps, float rope_base,
                         const int32_t *pos, int32_t n, int32_t Hq, int32_t Hkv, int32_t d, void *q_out,
@@ -237,9 +238,10 @@ int llm_op_kv8_attention_workspace(const llm_kv8_cache *cache, int32_t Hq, int32
  * One row per sequence is a decode step; more are drafted tokens or a prompt.  A
  * row at a negative position (more rows than kv_len) sees nothing: out 0, lse
  * -infinity.  A NaN scale of a V block that a row sees makes NaN of out and not of
- * lse, of a K block of both.  q: rows of `dtype`, q_stride elements apart; out: [n_rows][Hq][d] of
- * the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and q_stride
- * 16-byte aligned, out apart from q.  Sums and softmax statistics are held in fp32.
+ * lse, of a K block of both.  q: rows of `dtype`, q_stride elements apart; out:
+ * [n_rows][Hq][d] of the same type, dense; lse: fp32 [n_rows][Hq] or NULL; q, out and
+ * q_stride 16-byte aligned, out apart from q.  Sums and softmax statistics are held
+ * in fp32.
  * The products take q as it is with 16-bit rows and in 22 bits with fp32 rows, but
  * nothing below 2^-37 of the row's largest element; and the weights in 22 bits with
  * fp32 rows and, where n_rows * Hq/Hkv <= 48 * n_seqs (steps and drafts), with fp16
