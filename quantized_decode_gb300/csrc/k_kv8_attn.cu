@@ -9,7 +9,7 @@
 // of a result; movmatrix turns them into B.  Codes are exact in fp16.  q is scaled by a power of two so that its
 // largest element is in [2^12, 2^13).  What fp16 rounds off is a second B: of q for rows of fp32, of the weights
 // for fp32 and fp16 rows, so that they keep 22 bits.  (With weights of 11 bits, results of fp16 rows were 1.3 to 1.5
-// times as far off as their own rounding makes them, 4 x 131072 tokens in 91 us instead of 95; bf16's rounding is eight
+// times as far off as their own rounding makes them, 4 x 131072 tokens in 91 us instead of 94; bf16's rounding is eight
 // times as coarse, and 11 bits add 1% to its error.)  Where it is more, a weight is off by half of fp16's smallest step, 2^-25:
 // next to a largest one of 2^7 or above, and with a factor of 2^-4 or above for V's scale, 2^-28 of the largest.
 // The K scale multiplies the scores of its page, the V scale, relative to a power of two `vref` that follows it,
@@ -28,7 +28,7 @@
 // segment of one part is written at once; else its parts leave partial results in the workspace, and the last
 // to arrive (a counter) joins them in the order of the parts: the result does not depend on who is last.
 //
-// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 95 us, 5.7 TB/s;
+// Measured, heads of 128: 4 sequences of 131072 tokens (28/4 heads, fp16 rows, int8, 538 MB) 94 us, 5.7 TB/s;
 // 8 ragged sequences to 32768 tokens (32/8 heads, bf16 rows, e4m3, 146 MB) 36 us; one of 4096 tokens (28/4, fp32 rows)
 // 11 us.  The long ones are bound by memory and the latency of loads over 12 warps an SM (without the prefetch of the next pages
 // into L2 107 us), the short ones by the chain from the lengths over the table and the pages to two joins.
@@ -550,15 +550,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
                 decode_across<FMT>(vw[0][w], vw[1][w], p01);
                 decode_across<FMT>(vw[2][w], vw[3][w], p89);
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t af[4] = {p01[2 * y], p01[2 * y + 1], p89[2 * y], p89[2 * y + 1]};
+                for (int x = 0; x < NW; ++x)  // remainders behind the weights: a product does not wait for the one before it
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        if (t < nt) {
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t af[4] = {p01[2 * y], p01[2 * y + 1], p89[2 * y], p89[2 * y + 1]};
 #pragma unroll
-                            for (int x = 0; x < NW; ++x) mma16816(o[t][2 * w + y], af, pb[t][x][0], pb[t][x][1]);
-                        }
-                }
+                        for (int t = 0; t < NT; ++t)
+                            if (t < nt) mma16816(o[t][2 * w + y], af, pb[t][x][0], pb[t][x][1]);
+                    }
             }
             if (more) load_v(ph);
         }
