@@ -39,7 +39,7 @@ namespace qd {
 namespace {
 
 // NT tiles of 8 rows: one with 12 warps of 168 registers, or two with 8 of 255.  (4 sequences of 131072 tokens, 16-bit rows
-// with weights of 11 bits: 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115, 10 and 14 warps 141:
+// with weights of 11 bits: 12 warps 91 us, 16 of 128 registers 103, 14 118, 8 115; fp32 rows 115 then, 112 now, 10 and 14 warps 141:
 // the four schedulers want equal shares.)
 template <int D, int NT, bool HL>
 struct Cfg {

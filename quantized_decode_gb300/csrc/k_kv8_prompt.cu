@@ -24,8 +24,8 @@
 // Rows of fp32 keep 22 bits of q and of the weights: a second tile of remainders each, added by a second MMA
 // into the same accumulator.
 //
-// Measured: 8192 rows of 32/8 heads of 128, 0.55 TFLOP: 525 us, 1.05 PFLOP/s (e4m3; int8 535 us, fp32 rows, with twice the
-// MMAs, 884 us).  The MMAs of a block, 32 of 128 x 128 x 16 at 64 cycles, are 2054 of its 4300 cycles; a tile's
+// Measured: 8192 rows of 32/8 heads of 128, 0.55 TFLOP: 523 us, 1.05 PFLOP/s (e4m3; int8 533 us, fp32 rows, with twice the
+// MMAs, 885 us).  The MMAs of a block, 32 of 128 x 128 x 16 at 64 cycles, are 2054 of its 4300 cycles; a tile's
 // scores wait for its softmax, whose 64 scores a thread are read twice from TMEM (88 registers a thread leave no room to keep
 // them), so what bounds it is the latency of that turn, with issue slots half used.  Blocks of 64 tokens in two score buffers a
 // tile, which take the turn off the tensor cores, cost more MMA and hand-over time than they hide: 657 us.
