@@ -571,14 +571,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::kThreads, 1) k_kv8_attend(cons
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[t][z] += __shfl_xor_sync(kFullMask, l[t][z], x);
                 const int row = 8 * t + 2 * c + z;
-                const float k = l[t][z] == 0.f ? 0.f : vref / l[t][z];
+                const float k = kv8_row_factor(true, l[t][z]);
                 if (g == 0) s_ml[warp][row] = make_float2(m[t][z] - kLift, l[t][z]);
                 // dims VB g + 2 w' + {0, 1} lie in o[w'][z], o[w'][2 + z]
                 float *to = merge_o + (warp * R + row) * C::kRow + VB * g;
 #pragma unroll
                 for (int w = 0; w < OT; w += 2)
                     *reinterpret_cast<float4 *>(to + 2 * w) =
-                        make_float4(o[t][w][z] * k, o[t][w][2 + z] * k, o[t][w + 1][z] * k, o[t][w + 1][2 + z] * k);
+                        make_float4(o[t][w][z] * k * vref, o[t][w][2 + z] * k * vref, o[t][w + 1][z] * k * vref, o[t][w + 1][2 + z] * k * vref);
             }
         }
         __syncthreads();

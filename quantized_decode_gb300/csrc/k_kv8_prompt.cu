@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
             if (fine) l += other(l, nb);
             // ---- these keys' result, to where it belongs or to be joined
             const bool none = fine && l == 0.f;
-            const float k = kv8_row_factor(fine && !sees_nan, l, vref);
+            const float k = kv8_row_factor(fine && !sees_nan, l);
             const int row = t * kTile + r;
             const int64_t out = (int64_t)(s.row0 + tok) * a.Hq + h;
             const float log_sum = kv8_row_log2(fine, l, m - kLift);
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_prompt(const __grid_constan
                 float v[32];
                 tmem_ld32(o_at(t) + lanes + 32 * i, v);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
+                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k * vref;
                 put_row32<D>(a, res, row, live, out * D, 32 * i, v);
             }
             if (half == 0) {

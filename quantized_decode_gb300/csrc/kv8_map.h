@@ -68,10 +68,10 @@ KV8_FN int kv8_pages(int kv) { return kv > 0 ? (kv - 1) / kKv8Page + 1 : 1; }
 KV8_FN int kv8_blocks(int left, int tokens) { return left > 0 ? (left - 1) / tokens + 1 : 0; }
 KV8_FN bool kv8_page_there(int p, int left) { return left > 0 && p <= (left - 1) / kKv8Page; }
 
-// How a row of the attention ends, from the sum of its weights: what its weighted values, in units of `unit`, are
-// multiplied by, and log2 of the sum above `top`.  0 and -infinity for a row that saw nothing.  whole: every wait
+// How a row of the attention ends, from the sum of its weights: what its weighted values are multiplied by (before their
+// unit: of V near the smallest fp32 numbers the two together would be below them), and log2 of the sum above `top`.  0 and -infinity for a row that saw nothing.  whole: every wait
 // on the way has ended in time.  Where one has not, both are NaN, which no call without an error gives where V and K have none.
-KV8_FN float kv8_row_factor(bool whole, float sum, float unit) { return whole ? (sum == 0.f ? 0.f : unit / sum) : NAN; }
+KV8_FN float kv8_row_factor(bool whole, float sum) { return whole ? (sum == 0.f ? 0.f : 1.f / sum) : NAN; }
 KV8_FN float kv8_row_log2(bool whole, float sum, float top) { return whole ? (sum == 0.f ? -INFINITY : top + log2f(sum)) : NAN; }
 
 }  // namespace qd

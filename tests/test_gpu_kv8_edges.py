@@ -133,6 +133,23 @@ def test_small_weights_at_small_scales(fmt, dtype, rows):
     assert np.all(np.abs(lse - ref[1]) <= ltol)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (2, 1, 128)])
+@pytest.mark.parametrize("rows,kv", [((1,), (300,)), ((1, 1), (9000, 40)), ((12,), (700,)), ((200,), (300,)), ((120,), (4000,))])
+def test_v_near_the_smallest_numbers(Hq, Hkv, d, rows, kv):
+    """V of about 2^-118 keeps its bits: results scale with V as they do in 64 bits, but for the steps of 2^-149 that fp32
+    has near 0 (one rounding in each warp, part and row)."""
+    rng = np.random.default_rng(59)
+    table, pages = page_table(rng, kv)
+    host = host_cache(rng, "int8", pages, Hkv, d)
+    q = _rand(rng, (sum(rows), Hq, d), "f32", 2.0)
+    ref = kv8.attention(host, table, starts(rows), kv, as_f32(q))
+    tol, ltol = _bounds("f32", ref, max(kv))
+    host["vs"] *= np.float32(2.0 ** -118)
+    out, lse = _call(DeviceCache(host, table), "f32", q, rows, kv)
+    assert np.all(np.abs(out.astype(np.float64) * 2.0 ** 118 - ref[0]) <= tol + 4 * 2.0 ** (118 - 149))
+    assert np.all(np.abs(lse - ref[1]) <= ltol)
+
+
 # ---------------------------------------------------------------- blocks that are not finite
 
 NAN_CALLS = {  # rows, length, capacity of the table
