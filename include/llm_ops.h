@@ -256,6 +256,117 @@ int llm_op_kv8_attention(const llm_kv8_cache *cache, int32_t dtype, const void *
                          void *out, float *lse, void *workspace, int64_t workspace_bytes, int32_t *err,
                          void *stream);
 
+/* ---- The 16-bit K/V cache ---------------------------------------------------
+ * Operators over pages of fp16 or bf16 numbers laid out as the engine's pools, for
+ * any number of sequences in one call: a rotation over several axes that writes the
+ * pages, attention of sequences that share prefixes, the attention weight that each
+ * cached token received, and eviction by it.  A step of a layer is
+ * llm_op_kv16_rope_append, llm_op_kv16_attention and, where a cache is held to a
+ * budget, llm_op_kv16_weigh and now and then llm_op_kv16_evict.
+ *
+ * Sequences are given by row_start, kv_len and n_rows as for the 8-bit cache above,
+ * and the calls keep its rules: asynchronous on `stream`, no allocation, fit for
+ * capture, every index checked on the device before it is used, err set to
+ * LLM_ERR_DEVICE (or LLM_ERR_TIMEOUT) if it was 0 and something is out of range and
+ * left out, rows behind row_start[n_seqs] left as they are.  A token's slot (its place
+ * in its sequence's pages, 0 .. kv_len - 1) decides what comes before what; positions
+ * are a matter of the rotation alone, so the two part ways once tokens were evicted.
+ * Rows that the attention calls take and give have the pages' type.                 */
+typedef struct llm_kv16_cache {
+    int32_t dtype;              /* of the pages: LLM_DTYPE_F16 or LLM_DTYPE_BF16  */
+    int32_t n_kv_heads;         /* Hkv, 1..1024                                   */
+    int32_t head_dim;           /* d: 64 or 128                                   */
+    int32_t n_pool_pages;       /* pages in the pools; times Hkv * 16: 2^31 - 1 at most */
+    void *k_pool, *v_pool;      /* [n_pool_pages][Hkv][16][d], 16-byte aligned    */
+    const int32_t *page_table;  /* [n_seqs][table_stride], logical -> physical page */
+    int32_t n_seqs;             /* 1..4096                                        */
+    int32_t table_stride;       /* logical pages of a sequence at most, 1..2^27 - 1 */
+} llm_kv16_cache;
+
+/* Prefixes that sequences share: group g, the sequences seq_start[g] ..
+ * seq_start[g + 1] - 1, has len[g] tokens in front of each of its sequences' own, in
+ * pages of the same pools.  Sequences of no group have none.  A group whose numbers are
+ * out of range is left out (its rows see their own tokens alone) and reported.       */
+typedef struct llm_kv16_prefix {
+    const int32_t *page_table;  /* [n_groups][table_stride], as above              */
+    const int32_t *len;         /* [n_groups], 0 .. 16 * table_stride              */
+    const int32_t *seq_start;   /* [n_groups + 1], nondecreasing, 0 .. n_seqs      */
+    int32_t n_groups;           /* 1..4096                                        */
+    int32_t table_stride;       /* 1..2^27 - 1                                    */
+} llm_kv16_prefix;
+
+/* RMS norm of every query and key head, the rotation to its position, and K and V into
+ * the pages, in one pass.  As llm_op_qk_norm_rope, but a position has n_axes numbers
+ * (time, height and width of a picture's patch, say) and each frequency belongs to
+ * one of them:
+ *   a = pos[axis[i]][row] * rope_base^(-2i/d),  i < d/2.
+ * axis: uint8 [d/2] on the HOST, each below n_axes; n_axes 1..8; pos: int32
+ * [n_axes][n_rows] on the device.  All axes alike is the rotation of text.  q, k, v: rows
+ * of `dtype` (any), strides in elements, heads side by side, 16-byte aligned (pointers
+ * and strides); q_out: [n_rows][Hq][d] of the pages' type, dense.  Computed in fp32 and
+ * rounded once; V is rounded as it is.  A sequence with more rows than kv_len is left
+ * out.  A page that a call writes must be in the tables of its sequences once.  q_out
+ * apart from q, k and v.                                                           */
+int llm_op_kv16_rope_append(const llm_kv16_cache *cache, int32_t dtype, const void *q, int64_t q_stride,
+                            const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const void *q_gain, const void *k_gain, float eps, float rope_base,
+                            const uint8_t *axis, int32_t n_axes, const int32_t *pos,
+                            const int32_t *row_start, const int32_t *kv_len, int32_t n_rows, int32_t Hq,
+                            void *q_out, int32_t *err, void *stream);
+
+/* Bytes of workspace that llm_op_kv16_attention needs for calls of up to n_rows rows
+ * with these heads, n_seqs and n_groups (prefix may be NULL) on the current device.   */
+int llm_op_kv16_attention_workspace(const llm_kv16_cache *cache, const llm_kv16_prefix *prefix, int32_t Hq,
+                                    int32_t n_rows, int64_t *bytes);
+
+/* Grouped-query attention of each sequence's last rows over the prefix of its group,
+ * read once for all its rows, and causally over its own tokens: the row at slot p,
+ * query head h with K/V head g = h / (Hq/Hkv):
+ *   out[h] = sum_t softmax_t(q_h . K[g][t] / sqrt(d)) V[g][t]  over the prefix's t and own t <= p,
+ *   lse[h] = log sum_t exp(q_h . K[g][t] / sqrt(d)).
+ * prefix: NULL for none.  A row that sees nothing has out 0 and lse -infinity.  What
+ * lies in slots that no row of a sequence sees has no influence; of tokens that some
+ * rows of a sequence in the call see and others do not, V has to be finite.
+ * q, out: as for llm_op_kv8_attention, of the pages' type; lse: fp32 [n_rows][Hq] or
+ * NULL; Hq % Hkv == 0, Hq/Hkv <= 8.  Sums and softmax statistics are fp32.  Results do
+ * not depend on the run.  workspace: device, 256-byte aligned, zero-filled once before
+ * its first use; every call leaves it ready for the next.  Calls that may run at the
+ * same time need workspaces of their own.                                          */
+int llm_op_kv16_attention(const llm_kv16_cache *cache, const llm_kv16_prefix *prefix, const void *q,
+                          int64_t q_stride, const int32_t *row_start, const int32_t *kv_len, int32_t n_rows,
+                          int32_t Hq, void *out, float *lse, void *workspace, int64_t workspace_bytes,
+                          int32_t *err, void *stream);
+
+/* The attention weight that each of a sequence's own tokens received from its rows,
+ * summed over them and over the query heads of each K/V head:
+ *   scores[b][g][t] = keep * scores[b][g][t] (0 for t >= kv_len - rows: tokens of this call)
+ *                     + sum of exp(q_h . K[g][t] / sqrt(d) - lse[row][h]) over rows that see t, h of g,
+ * for t < kv_len; entries behind are left as they are, and so is a sequence without
+ * rows.  lse: what the attention returned (with a prefix, its tokens are in it).  q as
+ * for llm_op_kv16_attention; scores: fp32 [n_seqs][Hkv][score_stride] on the device;
+ * keep: finite, >= 0 (1 adds up, less forgets, 0 does not look at what was there).  A
+ * sequence longer than score_stride is left out.  Sums are fp32.  Results do not depend on
+ * the run.                                                                         */
+int llm_op_kv16_weigh(const llm_kv16_cache *cache, const void *q, int64_t q_stride, const int32_t *row_start,
+                      const int32_t *kv_len, int32_t n_rows, int32_t Hq, const float *lse, float keep,
+                      float *scores, int64_t score_stride, int32_t *err, void *stream);
+
+/* Sequences held to `budget` tokens: where kv_len is above it, each K/V head keeps the
+ * first n_first tokens, the last n_last and of those between the ones of the largest
+ * scores (the lower slot where two are equal; a NaN counts as less than any number), and
+ * moves them together, in their order, into slots 0 .. budget - 1 of the same pages.
+ *   kept[b][g][j] = the slot that the token now in slot j came from, int32 [n_seqs][Hkv][budget],
+ *   scores_out[b][g][j] = scores[b][g][kept[b][g][j]]  (both [n_seqs][Hkv][score_stride]),
+ *   new_len[b] = min(kv_len[b], budget),
+ * for j < new_len[b]; what lies behind in kept, scores_out and the pages is left as it
+ * is.  scores_out may be scores; new_len apart from kv_len.  0 <= n_first, n_last and
+ * n_first + n_last <= budget, 1 <= budget <= score_stride.  A sequence with kv_len
+ * outside the table or above score_stride is left out (new_len is its kv_len).  A page of
+ * a sequence must be in the tables once.                                            */
+int llm_op_kv16_evict(const llm_kv16_cache *cache, const int32_t *kv_len, int32_t budget, int32_t n_first,
+                      int32_t n_last, const float *scores, float *scores_out, int64_t score_stride,
+                      int32_t *kept, int32_t *new_len, int32_t *err, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -64,7 +64,18 @@ class llm_kv8_cache(ctypes.Structure):
                [("n_seqs", i32), ("table_stride", i32)]
 
 
+class llm_kv16_cache(ctypes.Structure):
+    _fields_ = [(n, i32) for n in ("dtype", "n_kv_heads", "head_dim", "n_pool_pages")] + \
+               [(n, vp) for n in ("k_pool", "v_pool", "page_table")] + [("n_seqs", i32), ("table_stride", i32)]
+
+
+class llm_kv16_prefix(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("page_table", "len", "seq_start")] + [("n_groups", i32), ("table_stride", i32)]
+
+
 _kv8 = ctypes.POINTER(llm_kv8_cache)
+_kv16 = ctypes.POINTER(llm_kv16_cache)
+_kv16_prefix = ctypes.POINTER(llm_kv16_prefix)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -134,6 +145,12 @@ SIGNATURES = {
     "llm_op_kv8_read": (i32, [_kv8, i32, vp, vp, i32, vp, i64, vp, i64, vp, vp]),
     "llm_op_kv8_attention_workspace": (i32, [_kv8, i32, i32, ctypes.POINTER(i64)]),
     "llm_op_kv8_attention": (i32, [_kv8, i32, vp, i64, vp, vp, i32, i32, vp, vp, vp, i64, vp, vp]),
+    "llm_op_kv16_rope_append": (i32, [_kv16, i32, vp, i64, vp, i64, vp, i64, vp, vp, f32, f32, vp, i32, vp, vp, vp, i32, i32,
+                                      vp, vp, vp]),
+    "llm_op_kv16_attention_workspace": (i32, [_kv16, _kv16_prefix, i32, i32, ctypes.POINTER(i64)]),
+    "llm_op_kv16_attention": (i32, [_kv16, _kv16_prefix, vp, i64, vp, vp, i32, i32, vp, vp, vp, i64, vp, vp]),
+    "llm_op_kv16_weigh": (i32, [_kv16, vp, i64, vp, vp, i32, i32, vp, f32, vp, i64, vp, vp]),
+    "llm_op_kv16_evict": (i32, [_kv16, vp, i32, i32, i32, vp, vp, i64, vp, vp, vp, vp]),
 }
 
 _lib = None
