@@ -1,80 +1,565 @@
-// k_kv16_attn.cu - attention over the 16-bit paged cache behind shared prefixes: one warp for each row and query
-// head goes through the prefix and the row's own tokens with a running maximum and sum.
-#include "kv16.cuh"
+// k_kv16_attn.cu - attention over the 16-bit paged cache behind shared prefixes, for few rows per sequence (decode
+// steps, drafted tokens): the sequences' own tokens, and the join with what the wide kernel made of the prefixes.
+//
+// The mathematics, for 8 (row, query head) pairs of one K/V head and a page of 16 tokens, with mma.sync m16n8k16:
+//   S^T[token][row] = K q^T      A = the page's K, B = q of the 8 rows
+//   O^T[dim][row] += V^T w^T     A = the page's V, transposed, B = the weights
+// so a page fills the 16 rows of A.  The weights leave the first product in the layout of a result; movmatrix turns them
+// into B.  They go in as two numbers of the pages' type, what rounding to the first leaves being the second (16 bits for
+// bf16, 22 for fp16): the products are few, and the result is off by little more than its own rounding.  The softmax is
+// the usual single pass in base 2, but the maximum that it refers to moves only where a score is more than 2^kLag above it.
+//
+// The layout.  The contraction index of an mma may be permuted freely if both operands agree.  Lane (g = lane / 4, c = lane
+// % 4) reads 16 bytes, 8 dims, of tokens g and g + 8 for each 32 dims of K: two steps of the contraction; q is read the
+// same way.  Of V it reads dims 8 g .. 8 g + 7 of each 64 of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9 and pairs
+// tokens up with byte permutations.  No shuffles, no shared memory; the next page is loaded as soon as a page's registers are free.
+//
+// The split.  A segment (sequence, head, 8 pairs) of p pages is cut into ceil(p / share) even parts, one work item
+// each; the warps of a CTA take its pages in turn.  A segment of one part is written at once; else its parts leave partial results
+// in the workspace, and the last to arrive (a counter) joins them in the order of the parts: the result does not
+// depend on who is last.
+#include "kv16_attn.cuh"
 
 namespace qd {
 
 namespace {
 
+constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
+constexpr int kLeast = kWarps;  // pages of a part at least: one for each warp
+// Partial results joined at once: up to kMaxJoin in one step, else in groups.
+constexpr int kGroupJoin = 8, kMaxJoin = 24;
+constexpr float kLag = 4.f;
+
+template <int D>
+constexpr int kPartFloats = kRows * (D + 1);  // [row][D], [row] log2 of the sum
+
 template <typename P>
-QD_DEV float one(const P *p) {
-    return (float)*p;
+QD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+QD_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 8 x 8 of 16 bits: rows and columns exchanged over the warp
+QD_DEV uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+QD_DEV int parts_of(int pages, int share) { return (int)((unsigned)(pages + share - 1) / (unsigned)share); }
+
+QD_DEV int block_sum(int x, int *scratch) {
+    x = (int)__reduce_add_sync(kFullMask, (unsigned)x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return scratch[0] + scratch[1] + scratch[2] + scratch[3];
+}
+QD_DEV float block_sum(float x, int *scratch) {  // the same in every thread
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = __float_as_int(x);
+    __syncthreads();
+    return __int_as_float(scratch[0]) + __int_as_float(scratch[1]) + (__int_as_float(scratch[2]) + __int_as_float(scratch[3]));
 }
 
 template <typename P, int D>
-__global__ void __launch_bounds__(128) k_attend(const __grid_constant__ Kv16AttnArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id < (a.c.n_seqs + 31) / 32) kv16_check_seqs(a.row_start, a.kv_len, a.n_rows, a.c, (int)id, false, a.err);
-    const int64_t row = id / a.Hq;
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_constant__ Kv16AttnArgs a, int32_t *counters, float *parts_at,
+                                                                 const int4 *plan, const float *wide) {
+    using T = Bits16<P>;
+    constexpr int KP = D / 32;   // 16-byte pieces of a token's K that a lane holds
+    constexpr int VP = D / 64;   // of its V
+    constexpr int OT = D / 16;   // output tiles of 16 dims
+    constexpr int kRow = D + 4;  // floats of a row in the merge buffer
+    __shared__ __align__(16) float merge_o[kWarps][kRows][kRow];
+    __shared__ float s_top[kWarps][kRows];
+    __shared__ int s_sum[kWarps], s_run[kWarps][2], s_last;
+    extern __shared__ int upto[];  // items that end with sequence b: [n_seqs], and of those the cut ones
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs, ctas = (int)gridDim.x;
+
+    // ---- the cut: each thread counts for B / 128 sequences, one after another
+    const int per_thread = (B + kThreads - 1) / kThreads, b0 = threadIdx.x * per_thread, b1 = min(b0 + per_thread, B);
+    int share;
+    {
+        int segs = 0, tiles0 = 0, pages0 = 1, longest = 1;  // tiles0, pages0: of b0, read once in calls of few sequences
+        float total = 0.f;
+        for (int b = b0; b < b1; ++b) {
+            const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+            if (!s.ok && blockIdx.x == 0) kv8_report(a.err);
+            const int tiles = (s.rows * G + kRows - 1) / kRows, pages = kv8_pages(s.kv);
+            if (b == b0) {
+                tiles0 = tiles;
+                pages0 = pages;
+            }
+            segs += tiles * Hkv;
+            total += (float)(tiles * Hkv) * (float)pages;
+            if (tiles) longest = max(longest, pages);
+        }
+        const float all = block_sum(total, s_sum);
+        const int all_segs = block_sum(segs, s_sum);
+        longest = (int)__reduce_max_sync(kFullMask, (unsigned)longest);
+        __syncthreads();
+        if (lane == 0) s_sum[warp] = longest;
+        __syncthreads();
+        longest = max(max(s_sum[0], s_sum[1]), max(s_sum[2], s_sum[3]));
+        // total / n, a little more rather than less (floats carry 24 bits)
+        auto over = [&](int n) { return (int)fminf(__fdividef(all, (float)n) * 1.00001f + 1.f, (float)longest); };
+        auto items_at = [&](int sh) {
+            int n = tiles0 * Hkv * parts_of(pages0, sh);
+            for (int b = b0 + 1; b < b1; ++b) {
+                const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+                n += (s.rows * G + kRows - 1) / kRows * Hkv * parts_of(kv8_pages(s.kv), sh);
+            }
+            return block_sum(n, s_sum);
+        };
+        share = min(max(kLeast, over(ctas)), longest);
+        if (2 * all_segs <= ctas && items_at(share) > ctas) {
+            // at total / (ctas - segs) they fit: the sum of ceil(p / s) is at most total / s + segs
+            int bad = share, good = max(over(ctas - all_segs), bad);
+#pragma unroll 1
+            for (int i = 0; i < 5 && good - bad > 1; ++i) {
+                const int half = bad + (good - bad) / 2;
+                if (items_at(half) <= ctas) good = half;
+                else bad = half;
+            }
+            share = good;
+        }
+        // ---- running sums of the items, and of those of cut segments
+        int mine = 0, mine_cut = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+            const int n = parts_of(kv8_pages(s.kv), share), items = (s.rows * G + kRows - 1) / kRows * Hkv * n;
+            mine += items;
+            mine_cut += n > 1 ? items : 0;
+            upto[b] = mine;
+            upto[B + b] = mine_cut;
+        }
+        int run = mine, run_cut = mine_cut;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, run, m), w = __shfl_up_sync(kFullMask, run_cut, m);
+            if (lane >= m) {
+                run += v;
+                run_cut += w;
+            }
+        }
+        if (lane == 31) {
+            s_run[warp][0] = run;
+            s_run[warp][1] = run_cut;
+        }
+        __syncthreads();
+        int before = run - mine, before_cut = run_cut - mine_cut;
+        for (int w = 0; w < warp; ++w) {
+            before += s_run[w][0];
+            before_cut += s_run[w][1];
+        }
+        for (int b = b0; b < b1; ++b) {
+            upto[b] += before;
+            upto[B + b] += before_cut;
+        }
+        __syncthreads();
+    }
+    const int items = upto[B - 1];
+    bool waited = false;
+
+    for (int item = (int)blockIdx.x; item < items; item += ctas) {
+        // ---- the item's sequence: the first whose items end behind it
+        int b = 0;
+        for (int n = B; n > 1;) {
+            const int step = (n + 31) / 32, i = lane * step + step - 1;
+            const int passed = __popc(__ballot_sync(kFullMask, i < n && upto[min(b + i, B - 1)] <= item));
+            b += passed * step;
+            n = min(n - passed * step, step);
+        }
+        const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+        const int in = item - (b > 0 ? upto[b - 1] : 0), place = b > 0 ? upto[B + b - 1] : 0;
+        // tiles fastest: those that read the same pages run side by side
+        const int pages = kv8_pages(s.kv), tiles = (s.rows * G + kRows - 1) / kRows, parts = parts_of(pages, share);
+        const int hp = (int)((unsigned)in / (unsigned)tiles), tile = in - hp * tiles;
+        const int head = (int)((unsigned)hp / (unsigned)parts), part = hp - head * parts;
+        const int p0 = (int)((int64_t)pages * part / parts), p1 = (int)((int64_t)pages * (part + 1) / parts);
+        const int n_live = min(kRows, s.rows * G - tile * kRows);
+        // what the tile's last row sees bounds the pages and the tokens that count
+        const int seen = max(0, s.kv - s.rows + (tile * kRows + n_live - 1) / G + 1);
+        const int pe = min(p1, (seen + kKv8Page - 1) / kKv8Page);
+
+        // ---- this warp's pages: p0 + warp, then every kWarps-th.  Lane i knows page number i of a
+        // batch of 32; the next batch's entries are on their way while a batch is worked on.
+        const int first = p0 + warp, n_mine = pe > first ? (pe - first + kWarps - 1) / kWarps : 0;
+        const int32_t *table = a.c.page_table + (int64_t)b * a.c.table_stride;
+        auto entry = [&](int j) { return j < n_mine ? __ldg(table + first + j * kWarps) : -2; };
+        auto checked = [&](int ph) {  // -1 for a page that is not there
+            if (ph != -2 && (ph < 0 || ph >= a.c.n_pool_pages)) kv8_report(a.err);
+            return ph < a.c.n_pool_pages ? max(ph, -1) : -1;
+        };
+        int phys = entry(lane), phys_next = entry(32 + lane);
+
+        // ---- q as B fragments: lane (g, c) has row g's dims 32 i + 8 c .. + 7, two steps
+        uint4 qf[KP];
+        {
+            const int r = tile * kRows + g, i = r / G;
+            const P *at = (const P *)a.q + (int64_t)(s.row0 + i) * a.q_stride + (int64_t)(head * G + r % G) * D + 8 * c;
+#pragma unroll
+            for (int p = 0; p < KP; ++p) {
+                qf[p] = make_uint4(0, 0, 0, 0);
+                if (g < n_live) qf[p] = __ldg(reinterpret_cast<const uint4 *>(at + 32 * p));
+            }
+        }
+        phys = checked(phys);
+        uint4 kw[2][KP], vw[4][VP];
+        const int64_t page_step = (int64_t)Hkv * (kKv8Page * D), head_at = (int64_t)head * (kKv8Page * D);
+        const P *k_at = (const P *)a.c.k_pool + head_at + g * D + 8 * c, *v_at = (const P *)a.c.v_pool + head_at + 2 * c * D + 8 * g;
+        auto load_k = [&](int ph) {
+            if (ph < 0) return;
+            const P *p = k_at + ph * page_step;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < KP; ++i) kw[t][i] = ld_stream(reinterpret_cast<const uint4 *>(p + 8 * t * D + 32 * i));
+        };
+        auto load_v = [&](int ph) {
+            if (ph < 0) return;
+            const P *p = v_at + ph * page_step;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < VP; ++i) vw[r][i] = ld_stream(reinterpret_cast<const uint4 *>(p + ((r & 1) + 8 * (r >> 1)) * D + 64 * i));
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < KP; ++i) kw[t][i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < VP; ++i) vw[r][i] = make_uint4(0, 0, 0, 0);
+        int ph = __shfl_sync(kFullMask, phys, 0);
+        load_k(ph);
+        load_v(ph);
+
+        const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[OT][4];
+        int limit[2], shortest = INT32_MAX;  // tokens that rows 2 c, 2 c + 1 see; those not there have q = 0
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int r = 2 * c + z;
+            limit[z] = r < n_live ? s.kv - s.rows + (tile * kRows + r) / G + 1 : INT32_MAX;
+            shortest = min(shortest, limit[z]);
+        }
+        shortest = __reduce_min_sync(kFullMask, shortest);
+#pragma unroll
+        for (int w = 0; w < OT; ++w) o[w][0] = o[w][1] = o[w][2] = o[w][3] = 0.f;
+
+        // ---- the pages
+#pragma unroll 1
+        for (int j = 0; j < n_mine; ++j) {
+            const int at = j & 31;
+            const bool there = ph >= 0, more = j + 1 < n_mine;
+            const int t0 = (first + j * kWarps) * kKv8Page;
+            // the next page, and at the ends of a batch the next batch
+            if (at == 16) phys_next = checked(phys_next);
+            if (at == 31) {
+                phys = phys_next;
+                phys_next = entry(j + 33 + lane);
+            }
+            ph = __shfl_sync(kFullMask, phys, (at + 1) & 31);
+            // ---- scores of tokens g, g + 8 and rows 2 c, 2 c + 1
+            float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < KP; ++i) {
+                const uint32_t a0[4] = {kw[0][i].x, kw[1][i].x, kw[0][i].y, kw[1][i].y}, a1[4] = {kw[0][i].z, kw[1][i].z, kw[0][i].w, kw[1][i].w};
+                mma16816<P>(acc, a0, qf[i].x, qf[i].y);
+                mma16816<P>(acc2, a1, qf[i].z, qf[i].w);
+            }
+            if (more) load_k(ph);
+            const bool edge = t0 + kKv8Page > shortest || !there;  // some row does not see all of the page
+            float sc[4];  // (g, 2c), (g, 2c + 1), (g + 8, 2c), (g + 8, 2c + 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sc[e] = (acc[e] + acc2[e]) * fac;
+                if (edge && (!there || t0 + g + 8 * (e >> 1) >= limit[e & 1])) sc[e] = -INFINITY;
+            }
+            const float top0 = fmaxf(sc[0], sc[2]), top1 = fmaxf(sc[1], sc[3]);
+            if (__any_sync(kFullMask, top0 > m[0] + kLag || top1 > m[1] + kLag || (m[0] == -INFINITY && top0 > m[0]) ||
+                                          (m[1] == -INFINITY && top1 > m[1]))) {
+                float n0 = fmaxf(top0, m[0]), n1 = fmaxf(top1, m[1]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, x));
+                    n1 = fmaxf(n1, __shfl_xor_sync(kFullMask, n1, x));
+                }
+                // only rows that need it, so that a row's result has nothing to do with its neighbours
+                if (n0 <= m[0] + kLag && m[0] != -INFINITY) n0 = m[0];
+                if (n1 <= m[1] + kLag && m[1] != -INFINITY) n1 = m[1];
+                const float k0 = n0 == m[0] ? 1.f : ex2(m[0] - n0), k1 = n1 == m[1] ? 1.f : ex2(m[1] - n1);
+                m[0] = n0;
+                m[1] = n1;
+                l[0] *= k0;
+                l[1] *= k1;
+#pragma unroll
+                for (int w = 0; w < OT; ++w) {
+                    o[w][0] *= k0;
+                    o[w][1] *= k1;
+                    o[w][2] *= k0;
+                    o[w][3] *= k1;
+                }
+            }
+            const float ref0 = T::kLift - (m[0] == -INFINITY ? 0.f : m[0]), ref1 = T::kLift - (m[1] == -INFINITY ? 0.f : m[1]);
+            uint32_t pb[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float w0 = ex2(sc[2 * h] + ref0), w1 = ex2(sc[2 * h + 1] + ref1);
+                l[0] += w0;
+                l[1] += w1;
+                const uint32_t hi = T::pack(w0, w1);
+                const float2 f = T::unpack(hi);
+                pb[0][h] = transpose8(hi);
+                pb[1][h] = transpose8(T::pack(w0 - f.x, w1 - f.y));
+            }
+            if (edge) {  // slots that no row sees
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!there || t0 + 2 * c + (r & 1) + 8 * (r >> 1) >= seen) {
+#pragma unroll
+                        for (int i = 0; i < VP; ++i) vw[r][i] = make_uint4(0, 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)  // remainders behind the weights: a product does not wait for the one before it
+#pragma unroll
+                for (int i = 0; i < VP; ++i) {
+                    const uint32_t w[4][4] = {{vw[0][i].x, vw[0][i].y, vw[0][i].z, vw[0][i].w}, {vw[1][i].x, vw[1][i].y, vw[1][i].z, vw[1][i].w},
+                                              {vw[2][i].x, vw[2][i].y, vw[2][i].z, vw[2][i].w}, {vw[3][i].x, vw[3][i].y, vw[3][i].z, vw[3][i].w}};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const uint32_t af[4] = {prmt(w[0][y], w[1][y], 0x5410u), prmt(w[0][y], w[1][y], 0x7632u), prmt(w[2][y], w[3][y], 0x5410u),
+                                                prmt(w[2][y], w[3][y], 0x7632u)};
+                        mma16816<P>(o[4 * i + y], af, pb[x][0], pb[x][1]);
+                    }
+                }
+            if (more) load_v(ph);
+        }
+
+        // ---- the warps' results together, each divided by its own sum so that none leaves fp32's range
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[z] += __shfl_xor_sync(kFullMask, l[z], x);
+            const int row = 2 * c + z;
+            const float k = kv8_row_factor(true, l[z]);
+            if (g == 0) s_top[warp][row] = kv8_row_log2(true, l[z], m[z] - T::kLift);
+            // dims 64 i + 8 g + 2 y + {0, 1} lie in o[4 i + y][z], o[4 i + y][2 + z]
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+#pragma unroll
+                for (int y = 0; y < 4; y += 2)
+                    *reinterpret_cast<float4 *>(&merge_o[warp][row][64 * i + 8 * g + 2 * y]) =
+                        make_float4(o[4 * i + y][z] * k, o[4 * i + y][2 + z] * k, o[4 * i + y + 1][z] * k, o[4 * i + y + 1][2 + z] * k);
+        }
+        __syncthreads();
+        // the group's plan, for the results of its prefix
+        int4 front = make_int4(0, 0, 0, 0);
+        int front_row = 0;
+        auto look_ahead = [&]() {  // by the whole warp, before results are written
+            const int group = kv16_group_of(a, b);
+            if (group < 0) return;
+            const Kv16Group gr = kv16_group(a, group);
+            if (!gr.ok || gr.len == 0 || s.row0 < gr.row0 || s.row0 + s.rows > gr.row0 + gr.rows) return;
+            if (!waited) pdl_wait();
+            waited = true;
+            front = __ldcg(plan + group);
+            front_row = s.row0 - gr.row0;
+        };
+        auto write_out = [&](Kv16Join &join, int row, int d4) {
+            const int rr = tile * kRows + row, i = rr / G, hq = rr % G;
+            if (front.z > 0) join.add_parts(kv16_parts(front, wide, D, G, head, hq, front_row + i), d4);
+            const int64_t at = (int64_t)(s.row0 + i) * a.Hq + head * G + hq;
+            store_out4((P *)a.out + at * D + 4 * d4, join.value());
+            if (d4 == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
+        };
+        // of this segment's part k: places of one tile's parts are `tiles` apart, as its items are
+        auto place_of = [&](int k) { return place + (head * parts + k) * tiles + tile; };
+        auto part_at = [&](int k) { return parts_at + (int64_t)place_of(k) * kPartFloats<D>; };
+        auto group_at = [&](int k) { return parts_at + (int64_t)(kKv16Counters / 2 + place_of(k)) * kPartFloats<D>; };  // from part k on
+        auto write_part = [&](float *to, const Kv16Join &join, int row, int d4) {
+            __stcg(reinterpret_cast<float4 *>(to + row * D + 4 * d4), join.value());
+            if (d4 == 0) __stcg(to + kRows * D + row, join.log_sum());
+        };
+        if (parts == 1) look_ahead();
+        for (int e = threadIdx.x; e < n_live * (D / 4); e += kThreads) {
+            const int row = e / (D / 4), d4 = e % (D / 4);
+            Kv16Join join;
+            const float t[kWarps] = {s_top[0][row], s_top[1][row], s_top[2][row], s_top[3][row]};
+            float4 v[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v[w] = *reinterpret_cast<const float4 *>(&merge_o[w][row][4 * d4]);
+            join.add(t, v);
+            if (parts == 1) write_out(join, row, d4);
+            else write_part(part_at(part), join, row, d4);
+        }
+        if (parts > 1) {
+            // groups of `per` parts are joined by their last to arrive, the groups by the last of those: two short
+            // chains instead of one long.  per <= kMaxJoin, and as many groups.
+            const int per = parts <= kMaxJoin ? parts : max(kGroupJoin, (parts + kMaxJoin - 1) / kMaxJoin);
+            const int group = part / per, groups = (parts + per - 1) / per, n = min(per, parts - group * per);
+            auto arrive = [&](int32_t *at, int of) {  // whether this CTA is the last of `of`
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    s_last = atomicAdd(at, 1) == of - 1;
+                    if (s_last) *at = 0;
+                    __threadfence();
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            // results k0, k0 + step, ... (n of them) to the output or to the group's place
+            auto join_all = [&](const float *from, int k0, int step, int count, bool final) {
+                if (final) look_ahead();
+                const int64_t stride = (int64_t)step * tiles * kPartFloats<D>;
+                for (int e = threadIdx.x; e < n_live * (D / 4); e += kThreads) {
+                    const int row = e / (D / 4), d4 = e % (D / 4);
+                    Kv16Join join;
+                    for (int i0 = 0; i0 < count; i0 += 8) {
+                        float t[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float *p = from + (i0 + i) * stride;
+                            t[i] = i0 + i < count ? __ldcg(p + kRows * D + row) : -INFINITY;
+                            v[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4 *>(p + row * D + 4 * d4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        join.add(t, v);
+                    }
+                    if (final) write_out(join, row, d4);
+                    else write_part(group_at(k0), join, row, d4);
+                }
+            };
+            if (arrive(counters + place_of(group * per), n)) {
+                join_all(part_at(group * per), group * per, 1, n, groups == 1);
+                if (groups > 1 && arrive(counters + kKv16Counters / 2 + place_of(0), groups)) join_all(group_at(0), 0, per, groups, true);
+            }
+        }
+        __syncthreads();  // the merge buffer is free again
+    }
+    if (!waited) pdl_wait();  // so that this kernel's end is that of both
+}
+
+// ---- the rows of wide calls: their partial results joined, one warp for each row and head
+template <typename P, int D>
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnArgs a, const int4 *plan, const float *wide) {
+    const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads, G = a.Hq / Hkv;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), row = id / a.Hq;
+    pdl_wait();
     if (row >= a.n_rows) return;
-    const int h = (int)(id - row * a.Hq), Hkv = a.c.n_kv_heads, g = h / (a.Hq / Hkv);
-    const int b = kv16_seq_of_row(a.row_start, a.c.n_seqs, (int)row);
+    const int h = (int)(id - row * a.Hq), b = kv16_seq_of_row(a.row_start, a.c.n_seqs, (int)row);
     const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
     if (row < s.row0 || row >= s.row0 + s.rows) return;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = one((const P *)a.q + row * a.q_stride + (int64_t)h * D + lane * E + e);
-        o[e] = 0.f;
+    const int group = kv16_group_of(a, b), d4 = lane % (D / 4);
+    const int4 own = __ldcg(plan + a.p.n_groups + b);
+    if (a.p.n_groups == 0 && own.z == 1) return;  // written already
+    Kv16Join join;
+    if (group >= 0) {
+        const Kv16Group gr = kv16_group(a, group);
+        const int4 front = __ldcg(plan + group);
+        if (gr.ok && gr.len > 0 && row >= gr.row0 && row < gr.row0 + gr.rows)
+            join.add_parts(kv16_parts(front, wide, D, G, h / G, h % G, (int)row - gr.row0), d4);
     }
-    auto through = [&](const int32_t *table, int n) {
-        for (int t = 0; t < n; ++t) {
-            const int page = __ldg(table + t / kKv8Page);
-            if (page < 0 || page >= a.c.n_pool_pages) {
-                if (lane == 0) kv8_report(a.err);
-                continue;
-            }
-            const int64_t at = (((int64_t)page * Hkv + g) * kKv8Page + t % kKv8Page) * D + lane * E;
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x = fmaf(q[e], one((const P *)a.c.k_pool + at + e), x);
-            x = warp_sum(x) * (D == 128 ? 0.08838834764831845f : 0.125f);
-            if (x == -INFINITY) continue;
-            const float to = fmaxf(m, x), k = m == to ? 1.f : expf(m - to), w = expf(x - to);
-            m = to;
-            l = l * k + w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(w, one((const P *)a.c.v_pool + at + e), o[e] * k);
-        }
-    };
-    for (int i = 0; i < a.p.n_groups; ++i) {
-        const Kv16Group r = kv16_group(a, i);
-        if (!r.ok && lane == 0) kv8_report(a.err);
-        if (r.ok && row >= r.row0 && row < r.row0 + r.rows) through(a.p.page_table + (int64_t)i * a.p.table_stride, r.len);
-    }
-    through(a.c.page_table + (int64_t)b * a.c.table_stride, max(0, s.kv - s.rows + (int)row - s.row0 + 1));
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) ((P *)a.out)[(row * a.Hq + h) * D + lane * E + e] = (P)(o[e] * inv);
-    if (lane == 0 && a.lse) a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+    join.add_parts(kv16_parts(own, wide, D, G, h / G, h % G, (int)row - s.row0), d4);
+    const int64_t at = row * a.Hq + h;
+    if (lane < D / 4) store_out4((P *)a.out + at * D + 4 * d4, join.value());
+    if (lane == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
+}
+
+// A launch that may begin while the one before it ends; what it reads of that one waits for its end.
+template <typename... Args, typename... Given>
+cudaError_t launch_behind(bool behind, void (*kernel)(Args...), unsigned blocks, unsigned threads, size_t bytes, cudaStream_t s, Given... given) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
+}
+
+// Fields of the workspace behind the counters: the partial results of the kernel for few rows, the plan (one int4 for each
+// group and sequence), the wide kernel's partial results.
+struct Space {
+    int64_t parts, plan, wide, bytes;
+};
+Space space_of(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_rows) {
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    const bool own = !kv16_few_rows(c, Hq, n_rows);
+    Space s;
+    s.parts = kKv16Counters * 4;
+    s.plan = up(s.parts + (int64_t)kKv16Counters * (c.head_dim == 128 ? kPartFloats<128> : kPartFloats<64>) * 4);
+    s.wide = up(s.plan + 16 * ((int64_t)n_groups + c.n_seqs));
+    const int G = Hq / c.n_kv_heads;
+    int64_t units = n_groups ? kv16_units(n_rows, G, n_groups) : 0;
+    if (own) units += kv16_units(n_rows, G, c.n_seqs);
+    s.bytes = up(s.wide + (units ? (units * c.n_kv_heads + n_sm) * kv16_place(c.head_dim) * 4 : 0));
+    return s;
 }
 
 template <typename P, int D>
-cudaError_t attend(cudaStream_t s, const Kv16AttnArgs &a) {
-    const int64_t warps = (int64_t)a.n_rows * a.Hq + (a.c.n_seqs + 31) / 32;
-    k_attend<P, D><<<(unsigned)((warps + 3) / 4), 128, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
+    const Space at = space_of(n_sm, a.c, a.p.n_groups, a.Hq, a.n_rows);
+    uint8_t *space = (uint8_t *)a.workspace;
+    int4 *plan = (int4 *)(space + at.plan);
+    float *wide = (float *)(space + at.wide);
+    const bool own = !kv16_few_rows(a.c, a.Hq, a.n_rows);
+    if (own || a.p.n_groups) {
+        const cudaError_t e = launch_kv16_wide(s, n_sm, a, own, (int32_t *)plan, wide);
+        if (e != cudaSuccess) return e;
+    }
+    if (own) {
+        const int64_t blocks = ((int64_t)a.n_rows * a.Hq + 3) / 4;
+        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+        return launch_behind(true, k_join<P, D>, (unsigned)blocks, 128, 0, s, a, plan, wide);
+    }
+    auto kernel = k_attend<P, D>;
+    const size_t bytes = 8 * (size_t)a.c.n_seqs;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kKv8MaxSeqs);
+    if (e != cudaSuccess) return e;
+    // no more CTAs than there can be parts of the longest sequences
+    const int64_t segs = ((int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) / kRows + a.c.n_seqs) * a.c.n_kv_heads, ctas = kCtasPerSm * n_sm;
+    const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
+    return launch_behind(a.p.n_groups > 0, kernel, (unsigned)(most < ctas ? most : ctas), kThreads, bytes, s, a, (int32_t *)space,
+                         (float *)(space + at.parts), plan, wide);
 }
 
 }  // namespace
 
-int64_t kv16_attention_workspace(int, const llm_kv16_cache &, int, int, int) { return 256; }
+bool kv16_few_rows(const llm_kv16_cache &c, int Hq, int n_rows) {
+    // Rows of a sequence, times heads, where the wide kernel's tiles of 128 begin to pay.  Items are counted in 32 bits, whatever
+    // row_start holds; beyond this the wide kernel.
+    const int64_t rows = (int64_t)n_rows * (Hq / c.n_kv_heads);
+    return rows <= (int64_t)48 * c.n_seqs && (rows / 8 + 1) * c.n_seqs * c.n_kv_heads < 1 << 30;
+}
 
-cudaError_t launch_kv16_attention(cudaStream_t s, int, const Kv16AttnArgs &a) {
-    if (a.c.dtype == LLM_DTYPE_F16) return a.c.head_dim == 128 ? attend<__half, 128>(s, a) : attend<__half, 64>(s, a);
-    return a.c.head_dim == 128 ? attend<__nv_bfloat16, 128>(s, a) : attend<__nv_bfloat16, 64>(s, a);
+int64_t kv16_attention_workspace(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_rows) {
+    return space_of(n_sm, c, n_groups, Hq, n_rows).bytes;
+}
+
+cudaError_t launch_kv16_attention(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
+    // a segment cut into c >= 2 parts has more than (c - 1) share pages, so there are at most two parts for each CTA's share
+    if (2 * kCtasPerSm * n_sm > kKv16Counters / 2 || kCtasPerSm * n_sm > kMaxJoin * kMaxJoin) return cudaErrorInvalidConfiguration;
+    if (a.c.dtype == LLM_DTYPE_F16) return a.c.head_dim == 128 ? attend<__half, 128>(s, n_sm, a) : attend<__half, 64>(s, n_sm, a);
+    return a.c.head_dim == 128 ? attend<__nv_bfloat16, 128>(s, n_sm, a) : attend<__nv_bfloat16, 64>(s, n_sm, a);
 }
 
 }  // namespace qd

@@ -1,0 +1,614 @@
+// k_kv16_wide.cu - attention over the 16-bit paged cache for many (row, query head) pairs of the same keys: a prefix with the
+// rows of all its sequences, and prompts; on the 5th-generation tensor cores.
+//
+// A CTA takes one item: up to 256 (row, query head) pairs of one K/V head as two tiles of 128, and a part of the keys of
+// their span (a prefix, or a sequence's own tokens) in blocks of 128 tokens (8 pages).  Where the pairs are one tile, both
+// tiles hold them and take the blocks in turn, so that one works while the other waits.
+//   warps 0-7     softmax, four for each tile: a thread owns a row (a TMEM lane) and holds its 128 scores in registers;
+//                 the 16-bit weights go back over the scores in TMEM, where they are the A operand of the second product
+//   warp 8        issues the MMAs (one lane) and owns the 512 TMEM columns: two score tiles and two outputs
+//   warp 9        copies q, K and V by TMA: the pages as they lie, each 64 dims a panel of 128-byte swizzled rows, K the
+//                 K-major and V the MN-major B operand
+// For each block of a tile the tensor cores do O += P V and then S = Q K of the tile's next block, tile after tile, in order, so
+// the next scores may take the place of weights that the product issued before still reads.
+//
+// The maximum that the exponent refers to follows the row's only when that has grown by 2^kLag, so O is rarely rescaled.
+// Weights are rounded to the pages' type once; their sum is taken before.
+#include "kv16_attn.cuh"
+#include "kv8_tc.cuh"
+
+namespace qd {
+
+namespace {
+
+constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 12 * 32;
+constexpr int kRegsSoftmax = 208, kRegsRest = 88;  // 168 at launch
+static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "no more than the launch has");
+constexpr int kStages = 2, kRecs = 4;
+constexpr int kLeastBlocks = 2;  // of a part: one for each tile
+constexpr float kLag = 8.f;
+
+struct WideArgs {
+    Kv16AttnArgs a;
+    CUtensorMap q, k, v;
+    int4 *plan;
+    float *wide;
+    int spans, ctas;   // ctas: what the keys are cut for
+    int64_t capacity;  // places
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kP = D / 64;           // panels of a row
+    static constexpr int kTileBytes = kP * kPanel;
+    static constexpr int kTiles = (2 + 2 * kStages) * kTileBytes;  // q, K and V
+    static_assert(kTileLanes * D * 4 <= 2 * kTileBytes, "a tile's output takes the place of q");
+};
+
+struct Bars {
+    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_part, s_full[2], p_full[2], o_full[2], done,
+        rec_full[kRecs];
+    uint32_t rec[kRecs];  // pages of a block that are there
+    uint32_t tmem;
+    float top[kTileLanes];
+    int abort;
+};
+
+// How many blocks a part has, and the segments; every warp for itself.
+struct Cut {
+    int share;
+    int64_t segs;
+};
+QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
+    const int lane = threadIdx.x & 31;
+    float total = 0.f;
+    int64_t segs = 0;
+    int longest = 1;
+    for (int i = lane; i < w.spans; i += 32) {
+        const Kv16Span s = kv16_span(w.a, i, err);
+        const int u = s.units(G), n = s.blocks();
+        segs += (int64_t)u * Hkv;
+        total += (float)u * (float)Hkv * (float)n;
+        if (u) longest = max(longest, n);
+    }
+    total = warp_sum(total);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) segs += __shfl_xor_sync(kFullMask, segs, m);
+    longest = __reduce_max_sync(kFullMask, longest);
+    auto items_at = [&](int share) {
+        int n = 0;
+        for (int i = lane; i < w.spans; i += 32) {
+            const Kv16Span s = kv16_span(w.a, i, nullptr);
+            n += s.units(G) * Hkv * ((s.blocks() + share - 1) / share);
+        }
+        return (int)__reduce_add_sync(kFullMask, (unsigned)n);
+    };
+    // total / n, a little more rather than less (floats carry 24 bits)
+    auto over = [&](int n) { return (int)fminf(__fdividef(total, (float)n) * 1.00001f + 1.f, (float)longest); };
+    Cut r;
+    r.segs = segs;
+    r.share = min(max(kLeastBlocks, over(w.ctas)), longest);
+    // The smallest share that leaves no more items than SMs, so that all end together; with more segments than half the SMs, or too many
+    // spans to count again, the average load.
+    if (2 * segs <= w.ctas && w.spans <= 256 && items_at(r.share) > w.ctas) {
+        // at total / (ctas - segs) they fit: the sum of ceil(p / s) is at most total / s + segs
+        int bad = r.share, good = max(over(w.ctas - (int)segs), bad);
+#pragma unroll 1
+        for (int i = 0; i < 6 && good - bad > 1; ++i) {
+            const int mid = bad + (good - bad) / 2;
+            if (items_at(mid) <= w.ctas) good = mid;
+            else bad = mid;
+        }
+        r.share = good;
+    }
+    return r;
+}
+
+// 128 scores of a lane's row: loads under way together, then one wait that names what it waits for.
+QD_DEV void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+template <bool WAIT>
+QD_DEV void tmem_ld32_end(uint32_t (&r)[32]) {
+#define QD_ALL32 \
+    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), \
+        "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), \
+        "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), \
+        "+r"(r[31])
+    if (WAIT) asm volatile("tcgen05.wait::ld.sync.aligned;" : QD_ALL32 : : "memory");
+    else asm volatile("" : QD_ALL32 : : "memory");
+#undef QD_ALL32
+}
+
+// A row's softmax of a block, by each lane of a warp: 128 scores at s_at in TMEM, weights in their place, m and l
+// brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on, and of pages that are not
+// there, have no weight.
+template <typename P, int D, bool CUT>
+QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, uint32_t ok, bool have_o, float &m, float &l) {
+    uint32_t raw[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) tmem_ld32_start(s_at + 32 * c, raw[c]);
+    tmem_ld32_end<true>(raw[0]);
+#pragma unroll
+    for (int c = 1; c < 4; ++c) tmem_ld32_end<false>(raw[c]);
+    if (CUT) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+            if (e >= limit || !((ok >> (e / kKv8Page)) & 1u)) raw[e / 32][e % 32] = 0xff800000u;
+    }
+    auto x = [&](int e) { return __uint_as_float(raw[e / 32][e % 32]); };
+    float tops[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float u = fmaxf(x(32 * c), x(32 * c + 1)), v = fmaxf(x(32 * c + 2), x(32 * c + 3));
+#pragma unroll
+        for (int e = 4; e < 32; e += 4) {  // three operands to an instruction
+            u = fmaxf(fmaxf(u, x(32 * c + e)), x(32 * c + e + 1));
+            v = fmaxf(fmaxf(v, x(32 * c + e + 2)), x(32 * c + e + 3));
+        }
+        tops[c] = fmaxf(u, v);
+    }
+    const float most = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * fac;
+    const bool grow = most > m + kLag || (m == -INFINITY && most > m);
+    if (__any_sync(kFullMask, grow)) {
+        const float to = grow ? most : m, k = m == to ? 1.f : ex2(m - to);
+        m = to;
+        l *= k;
+        if (have_o) tmem_scale(o_at, D, k);
+    }
+    const float off = Bits16<P>::kLift - (m == -INFINITY ? 0.f : m);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t w16[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float2 w = fma2(make_float2(x(32 * c + e), x(32 * c + e + 1)), make_float2(fac, fac), make_float2(off, off));
+            w.x = ex2(w.x);
+            w.y = ex2(w.y);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
+            w16[e / 2] = Bits16<P>::pack(w.x, w.y);
+        }
+        tmem_st16(s_at + 16 * c, w16);
+    }
+    sum[0] = add2(sum[0], sum[1]);
+    l += sum[0].x + sum[0].y;
+}
+
+QD_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map),
+        "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+QD_DEV void tma_load_rows(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x),
+        "r"(y), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+QD_DEV void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename P, int D>
+__global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ WideArgs w) {
+    using namespace ptx;
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Bars &b = *reinterpret_cast<Bars *>(smem + C::kTiles);
+    uint8_t *sq = smem, *sk = smem + 2 * C::kTileBytes, *sv = sk + kStages * C::kTileBytes;
+    volatile int *abort = &b.abort;
+    const Kv16AttnArgs &a = w.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, R = kv16_tile_rows(G);
+    pdl_launch();
+
+    // ---- the item: a scan over the spans, 32 at a time; the first CTA writes the plan down as it goes
+    const Cut cut = cut_spans(w, G, Hkv, blockIdx.x == 0 && warp == 0 ? a.err : nullptr);
+    Kv16Span s = {0, 0, 0, -1};
+    int span = -1, units = 0, parts = 0;
+    int64_t base = 0, in = 0;
+    for (int i0 = 0; i0 < w.spans; i0 += 32) {
+        Kv16Span mine = {0, 0, 0, -1};
+        if (i0 + lane < w.spans) mine = kv16_span(a, i0 + lane, nullptr);
+        const int u = mine.units(G), n = (mine.blocks() + cut.share - 1) / cut.share;
+        const int64_t items = (int64_t)u * Hkv * n;
+        int64_t upto = items;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t v = __shfl_up_sync(kFullMask, upto, m);
+            if (lane >= m) upto += v;
+        }
+        if (blockIdx.x == 0 && warp == 0 && i0 + lane < w.spans) {
+            const bool fits = base + upto <= w.capacity;  // else row_start falls somewhere
+            if (!fits) kv8_report(a.err);
+            w.plan[i0 + lane] = make_int4((int)(base + upto - items), u, fits && u > 0 ? n : 0, 0);
+        }
+        const unsigned hit = __ballot_sync(kFullMask, (int64_t)blockIdx.x < base + upto);
+        if (hit && span < 0) {
+            const int l = __ffs(hit) - 1;
+            span = i0 + l;
+            in = (int64_t)blockIdx.x - base - __shfl_sync(kFullMask, upto - items, l);
+            units = __shfl_sync(kFullMask, u, l);
+            parts = __shfl_sync(kFullMask, n, l);
+            s.row0 = __shfl_sync(kFullMask, mine.row0, l);
+            s.rows = __shfl_sync(kFullMask, mine.rows, l);
+            s.len = __shfl_sync(kFullMask, mine.len, l);
+            s.seq = __shfl_sync(kFullMask, mine.seq, l);
+            if (base + __shfl_sync(kFullMask, upto, l) > w.capacity) units = 0;
+            if (blockIdx.x != 0) break;
+        }
+        base += __shfl_sync(kFullMask, upto, 31);
+    }
+    if (span < 0 || units == 0) return;
+    // units fastest: those that read the same pages run side by side
+    const int hp = (int)(in / units), unit = (int)(in - (int64_t)hp * units), head = hp / parts, part = hp - head * parts;
+    const int row0 = unit * 2 * R, rows = min(2 * R, s.rows - row0);  // of the span
+    const bool pair = rows > R;                                        // two tiles of rows, else one for every other block
+    const bool prefix = s.seq < 0;
+    // tokens that any row of the item sees, and this part's blocks of them; tokens are counted from the first one's on
+    const int all = prefix ? s.len : max(0, s.len - s.rows + row0 + rows);
+    const int nb_span = s.blocks(), blk0 = (int)((int64_t)nb_span * part / parts), blk1 = (int)((int64_t)nb_span * (part + 1) / parts);
+    const int nb = max(0, min(blk1, kv8_blocks(all, kKeyBlock)) - blk0), seen = all - blk0 * kKeyBlock;
+    auto tile_blocks = [&](int t) { return pair ? nb : (nb - t + 1) / 2; };
+    auto block_of = [&](int t, int i) { return pair ? i : 2 * i + t; };
+
+    if (threadIdx.x == 0) {
+        mbar_init(&b.q_full, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&b.k_full[i], 1);
+            mbar_init(&b.k_empty[i], 1);
+            mbar_init(&b.v_full[i], 1);
+            mbar_init(&b.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.p_full[i], 4);
+            mbar_init(&b.o_full[i], 1);
+        }
+        for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
+        mbar_init(&b.v_part, 1);
+        mbar_init(&b.done, 1);
+        b.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    auto s_at = [&](int t) { return tmem + (uint32_t)(t * 128); };
+    auto o_at = [&](int t) { return tmem + (uint32_t)((2 + t) * 128); };
+    auto fail = [&]() {
+        *abort = 1;
+        if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
+    };
+    auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
+        if (!tc_wait(bar, phase & 1u, abort)) {
+            fail();
+            return false;
+        }
+        return true;
+    };
+    auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
+    if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
+
+    if (warp < kSoftmax) {
+        // ================= softmax =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int t = warp >> 2, lane_of = (warp & 3) * 32 + lane;
+        const int i = lane_of / G, row = (pair ? t * R : 0) + i;  // of the unit
+        const bool live = i < R && row < rows;
+        // tokens of this part that the row sees; rows that are not there hide nothing
+        const int limit = prefix ? seen : (live ? max(0, s.len - s.rows + row0 + row + 1) - blk0 * kKeyBlock : INT32_MAX);
+        const int shortest = __reduce_min_sync(kFullMask, limit);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
+        const int n = tile_blocks(t);
+        float m = -INFINITY, l = 0.f;
+        bool fine = true;
+        for (int k = 0; k < n && fine; ++k) {
+            const int j = block_of(t, k);
+            fine = wait_warp(&b.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)k);
+            if (!fine) break;
+            tc_fence_after();
+            const uint32_t ok = b.rec[j % kRecs];
+            const int left = limit - j * kKeyBlock;
+            if (shortest - j * kKeyBlock < kKeyBlock || ok != 0xffu) block_weights<P, D, true>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
+            else block_weights<P, D, false>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.p_full[t]);
+        }
+        // both tiles' products have to be done where one's result takes the place of q; `done` comes after a wait that ran out too
+        const bool some = n > 0;
+        if (nb > 0) fine = wait_warp(pair ? &b.o_full[t] : &b.done, 0) && fine && !*abort;
+        tc_fence_after();
+        float k = some ? kv8_row_factor(fine, l) : 0.f;
+        float top = some ? kv8_row_log2(fine, l, m - Bits16<P>::kLift) : -INFINITY;
+        const bool none = top == -INFINITY;
+        float *mine = w.wide + ((int64_t)blockIdx.x) * kv16_place(D);
+        float4 *other = reinterpret_cast<float4 *>(sq);  // [d / 4][lane]
+        const bool direct = !prefix && parts == 1 && a.p.n_groups == 0;
+        if (!pair) {
+            if (t == 1) {
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    float v[32];
+                    tmem_ld32(o_at(1) + lanes + d, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        other[(d + e) / 4 * kTileLanes + lane_of] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
+                }
+                b.top[lane_of] = top;
+            }
+            softmax_sync();
+        }
+        if (pair || t == 0) {
+            float k1 = 0.f;
+            if (!pair) {
+                // the other half's result: weights of the two, which add up to 1
+                const float top1 = b.top[lane_of], most = fmaxf(top, top1), ref = most == -INFINITY ? 0.f : most;
+                const float w0 = none ? 0.f : ex2(top - ref), w1 = top1 == -INFINITY ? 0.f : ex2(top1 - ref), sum = w0 + w1;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                k *= w0 * inv;
+                k1 = w1 * inv;
+                top = sum == 0.f ? -INFINITY : ref + log2f(sum);
+            }
+            const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
+            float *to = mine + (int64_t)t * D * kTileLanes;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                float v[32];
+                tmem_ld32(o_at(t) + lanes + d, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
+                if (!pair && k1 != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 x = other[(d + e) / 4 * kTileLanes + lane_of];
+                        v[e] = fmaf(x.x, k1, v[e]);
+                        v[e + 1] = fmaf(x.y, k1, v[e + 1]);
+                        v[e + 2] = fmaf(x.z, k1, v[e + 2]);
+                        v[e + 3] = fmaf(x.w, k1, v[e + 3]);
+                    }
+                }
+                __syncwarp();
+                if (live && direct) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>((P *)a.out + at * D + d + e) =
+                            make_uint4(Bits16<P>::pack(v[e], v[e + 1]), Bits16<P>::pack(v[e + 2], v[e + 3]), Bits16<P>::pack(v[e + 4], v[e + 5]),
+                                       Bits16<P>::pack(v[e + 6], v[e + 7]));
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        __stcg(reinterpret_cast<float4 *>(to + ((int64_t)(d + e) / 4 * kTileLanes + lane_of) * 4), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                }
+                __syncwarp();
+            }
+            if (live && !direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + t * kTileLanes + lane_of, top);
+            else if (live && a.lse) a.lse[at] = top * 0.69314718f;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+        if (warp == kMmaWarp && nb > 0) {
+            // ================= MMA =================
+            const uint32_t type = Bits16<P>::kFormat << 7 | Bits16<P>::kFormat << 10;
+            const uint32_t id_s = umma_idesc_f16_f32(kTileLanes, kKeyBlock) | type, id_o = umma_idesc_f16_f32(kTileLanes, D) | kIdescBMn | type;
+            const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
+            auto scores = [&](int t, int st) {
+                const uint32_t d = s_at(t), qd = q_at + (pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                    if (kk == 0) mma_ss<false>(d, qd, kd, id_s);
+                    else mma_ss<true>(d, qd + at, kd + at, id_s);
+                }
+            };
+            auto weigh = [&](int t, int st, bool more) {
+                const uint32_t d = o_at(t), p = s_at(t), vd = v_at + st * (C::kTileBytes >> 4);
+                if (more) mma_ts<true>(d, p, vd, id_o);
+                else mma_ts<false>(d, p, vd, id_o);
+#pragma unroll
+                for (int kk = 1; kk < kKeyBlock / 16; ++kk) mma_ts<true>(d, p + kk * 8, vd + kk * (2048 >> 4), id_o);
+            };
+            const bool mine = elect_lane();
+            bool go = wait_warp(&b.q_full, 0);
+            for (int t = 0; t < 2 && go; ++t) {
+                if (tile_blocks(t) == 0) break;
+                const int j = block_of(t, 0);
+                go = wait_warp(&b.k_full[j % kStages], 0);
+                if (!go) break;
+                tc_fence_after();
+                if (mine) {
+                    scores(t, j % kStages);
+                    umma_commit(&b.s_full[t]);
+                    if (!pair || t == 1) umma_commit(&b.k_empty[j % kStages]);
+                }
+                __syncwarp();
+            }
+            for (int k = 0; k < tile_blocks(0) && go; ++k)
+                for (int t = 0; t < 2 && go; ++t) {
+                    const int n = tile_blocks(t);
+                    if (k >= n) break;
+                    const int j = block_of(t, k), jn = block_of(t, k + 1), st = j % kStages, sn = jn % kStages;
+                    const bool last = !pair || t == 1;  // of the tiles that use the block
+                    go = wait_warp(&b.v_full[st], (uint32_t)(j / kStages)) && wait_warp(&b.p_full[t], (uint32_t)k);
+                    if (!go) break;
+                    tc_fence_after();
+                    if (mine) weigh(t, st, k > 0);
+                    __syncwarp();
+                    if (k + 1 < n) {
+                        go = wait_warp(&b.k_full[sn], (uint32_t)(jn / kStages));
+                        if (!go) break;
+                        tc_fence_after();
+                    }
+                    if (mine) {
+                        if (k + 1 < n) {
+                            scores(t, sn);
+                            umma_commit(&b.s_full[t]);
+                            if (last) umma_commit(&b.k_empty[sn]);
+                        } else {
+                            umma_commit(&b.o_full[t]);
+                        }
+                        if (last) umma_commit(&b.v_empty[st]);
+                    }
+                    __syncwarp();
+                }
+            if (mine) umma_commit(&b.done);  // arrives once every MMA issued above has completed
+            __syncwarp();
+            if (!tc_wait(&b.done, 0, nullptr)) fail();
+        }
+        if (warp == kCopyWarp && nb > 0) {
+            // ================= copies =================
+            constexpr uint32_t kPageBytes = kKv8Page * 128;  // of a panel
+            const int page = lane & 7, panel = lane >> 3;
+            const int32_t *table = (prefix ? a.p.page_table + (int64_t)span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
+                                   (int64_t)blk0 * (kKeyBlock / kKv8Page);
+            if (lane == 0) {
+                mbar_expect_tx(&b.q_full, (pair ? 2 : 1) * C::kP * R * G * 128);
+                for (int t = 0; t < (pair ? 2 : 1); ++t)
+                    for (int p = 0; p < C::kP; ++p)
+                        tma_load_3d(smem_u32(sq) + t * C::kTileBytes + p * kPanel, &w.q, p * 64, head * G, s.row0 + row0 + t * R, &b.q_full);
+            }
+            __syncwarp();
+            // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
+            auto entry = [&](int j) {
+                const int p = j * (kKeyBlock / kKv8Page) + page;
+                return j < nb && kv8_page_there(p, seen) ? max(-1, __ldg(table + p)) : -2;
+            };
+            auto checked = [&](int ph) {
+                if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
+                if (panel == 0) kv8_report(a.err);
+                return -1;
+            };
+            const int beyond = a.c.n_pool_pages * Hkv * kKv8Page;  // the row behind the pools: reads as zeros
+            int ph = checked(entry(0)), ph_next = entry(1), started = 0;
+            bool part_started = false, go = true;
+            for (int j = 0; j < nb && go; ++j) {
+                const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + head) * kKv8Page : beyond;
+                const uint32_t use = (uint32_t)(j / kStages), ok = __ballot_sync(kFullMask, ph != -1) & 0xffu;
+                if (use > 0 && !(go = wait_warp(&b.k_empty[st], use - 1))) break;
+                // Record j - kRecs: the scores of block j - kStages, done, were issued behind the weights of a block after it.
+                if (lane == 0) {
+                    b.rec[j % kRecs] = ok;
+                    mbar_arrive(&b.rec_full[j % kRecs]);
+                    mbar_expect_tx(&b.k_full[st], C::kTileBytes);
+                }
+                __syncwarp();
+                if (panel < C::kP) tma_load_rows(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st]);
+                started = 2 * j + 1;
+                const int next = checked(ph_next);
+                ph_next = entry(j + 2);
+                if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
+                // a page of which the last slots hold nothing: they become 0 before V is used
+                const int left = seen - j * kKeyBlock;
+                const bool cut_page = left < kKeyBlock && left % kKv8Page != 0;
+                uint64_t *bar = cut_page ? &b.v_part : &b.v_full[st];
+                if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
+                __syncwarp();
+                if (panel < C::kP) tma_load_rows(smem_u32(sv) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.v, panel * 64, y, bar);
+                if (cut_page) {  // the last block
+                    part_started = true;
+                    if (!(go = wait_warp(bar, 0))) break;
+                    const int end = (left / kKv8Page + 1) * kKv8Page, chunks = (end - left) * 8;
+                    for (int e = lane; e < chunks * C::kP; e += 32)
+                        *reinterpret_cast<uint4 *>(sv + st * C::kTileBytes + e / chunks * kPanel + left * 128 + e % chunks * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.v_full[st]);
+                }
+                started = 2 * j + 2;
+                ph = next;
+            }
+            if (*abort) {  // copies in flight land before the shared memory goes away
+                tc_wait(&b.q_full, 0, nullptr);
+                const int ks = (started + 1) / 2, vs = started / 2;
+                for (int j = max(0, ks - kStages); j < ks; ++j) tc_wait(&b.k_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
+                for (int j = max(0, vs - kStages); j < vs; ++j) tc_wait(&b.v_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
+                if (part_started) tc_wait(&b.v_part, 0, nullptr);
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled through the runtime's driver entry point (null if unavailable)
+EncodeFn encoder() {
+    static EncodeFn enc = []() -> EncodeFn {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeFn>(p);
+        return nullptr;
+    }();
+    return enc;
+}
+bool encode(CUtensorMap *map, int dims, const void *p, const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box) {
+    const cuuint32_t step[3] = {1, 1, 1};
+    return encoder() && encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, dims, const_cast<void *>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename P, int D>
+cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
+    auto kernel = k_wide<P, D>;
+    constexpr int kBytes = Cfg<D>::kTiles + (int)sizeof(Bars);
+    static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
+    // the warps' split of the registers waits for ever if the launch has fewer
+    static const int regs = [&]() {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (3 * regs < 2 * kRegsSoftmax + kRegsRest) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kThreads, kBytes, s>>>(w);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int32_t *plan, float *space) {
+    WideArgs w{};
+    w.a = a;
+    w.plan = (int4 *)plan;
+    w.wide = space;
+    w.spans = a.p.n_groups + (own ? a.c.n_seqs : 0);
+    w.ctas = n_sm;
+    const int G = a.Hq / a.c.n_kv_heads, D = a.c.head_dim;
+    const int64_t units = (a.p.n_groups ? kv16_units(a.n_rows, G, a.p.n_groups) : 0) + (own ? kv16_units(a.n_rows, G, a.c.n_seqs) : 0);
+    w.capacity = units * a.c.n_kv_heads + n_sm;
+    if (w.capacity > INT32_MAX) return cudaErrorInvalidValue;
+    const cuuint64_t rows = (cuuint64_t)a.c.n_pool_pages * a.c.n_kv_heads * kKv8Page;
+    const cuuint64_t size[2] = {(cuuint64_t)D, rows}, stride[1] = {(cuuint64_t)D * 2};
+    const cuuint32_t box[2] = {64, kKv8Page};
+    const cuuint64_t q_size[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.n_rows}, q_stride[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)kv16_tile_rows(G)};
+    if (!encode(&w.k, 2, a.c.k_pool, size, stride, box) || !encode(&w.v, 2, a.c.v_pool, size, stride, box) ||
+        !encode(&w.q, 3, a.q, q_size, q_stride, q_box))
+        return cudaErrorInvalidValue;
+    const unsigned blocks = (unsigned)w.capacity;
+    if (a.c.dtype == LLM_DTYPE_F16) return D == 128 ? wide<__half, 128>(s, w, blocks) : wide<__half, 64>(s, w, blocks);
+    return D == 128 ? wide<__nv_bfloat16, 128>(s, w, blocks) : wide<__nv_bfloat16, 64>(s, w, blocks);
+}
+
+}  // namespace qd

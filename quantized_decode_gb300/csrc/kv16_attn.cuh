@@ -1,0 +1,128 @@
+// kv16_attn.cuh - what the two attention kernels over the 16-bit cache share: the workspace, the plan of the wide kernel's
+// items, and partial results.
+//
+// A row's result is joined from partial ones: of the prefix and of its own tokens, each maybe cut.  The wide
+// kernel (k_kv16_wide.cu) takes (row, query head) pairs of one K/V head as two tiles of 128 lanes; a span is a group with
+// its prefix, or a sequence with its own tokens.  Its partial results are those of an item: a unit (up to two tiles) of a span, a
+// head and a part of the keys.
+#pragma once
+
+#include "kv16.cuh"
+
+namespace qd {
+
+constexpr int kTileLanes = 128, kKeyBlock = 128;  // lanes of a tile, tokens of a block of keys
+constexpr int kKv16Counters = 4096;
+
+inline __host__ __device__ int kv16_tile_rows(int G) { return kTileLanes / G; }
+// floats of a wide item's result: [tile][d / 4][lane][4] and [tile][lane] log2 of the sums
+inline __host__ __device__ int64_t kv16_place(int d) { return 2 * (int64_t)kTileLanes * (d + 1); }
+// Units that there can be: a span has rows / (2 tile rows) + 1 at most.
+inline __host__ __device__ int64_t kv16_units(int n_rows, int G, int spans) { return (int64_t)n_rows / (2 * kv16_tile_rows(G)) + spans; }
+
+// A span as the wide kernel takes it: groups first, then sequences where they are its own too.
+struct Kv16Span {
+    int row0, rows, len, seq;  // seq -1: a prefix
+    QD_DEV int units(int G) const { return (rows + 2 * kv16_tile_rows(G) - 1) / (2 * kv16_tile_rows(G)); }
+    QD_DEV int blocks() const { return len > 0 ? (len - 1) / kKeyBlock + 1 : 1; }
+};
+QD_DEV Kv16Span kv16_span(const Kv16AttnArgs &a, int i, int32_t *err) {
+    if (i < a.p.n_groups) {
+        const Kv16Group g = kv16_group(a, i);
+        if (!g.ok) kv8_report(err);
+        return Kv16Span{g.row0, g.len > 0 ? g.rows : 0, g.len, -1};
+    }
+    const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, i - a.p.n_groups);
+    if (!s.ok) kv8_report(err);
+    return Kv16Span{s.row0, s.rows, s.kv, i - a.p.n_groups};
+}
+
+// Where a (row, head) pair's partial results of a span lie: `n` of them, `step` floats apart.
+struct Kv16Parts {
+    const float *o, *top;  // of dims 0 .. 3 (those of d4 lie d4 * kTileLanes * 4 further on), and log2 of the sum
+    int64_t step;
+    int n;
+};
+QD_DEV Kv16Parts kv16_parts(const int4 &plan, const float *wide, int d, int G, int head, int in, int row_in_span) {
+    const int R = kv16_tile_rows(G), u = row_in_span / (2 * R), r = row_in_span - u * 2 * R, tile = r / R, lane = (r - tile * R) * G + in;
+    const int64_t step = kv16_place(d);
+    const float *p = wide + (plan.x + (int64_t)head * plan.z * plan.y + u) * step;
+    return Kv16Parts{p + ((int64_t)tile * (d / 4) * kTileLanes + lane) * 4, p + 2 * (int64_t)kTileLanes * d + tile * kTileLanes + lane,
+                     step * plan.y, plan.z};
+}
+
+// The group of a sequence: its number, or -1; by the whole warp.
+QD_DEV int kv16_group_of(const Kv16AttnArgs &a, int b) {
+    if (a.p.n_groups == 0) return -1;
+    const int g = kv16_seq_of_row(a.p.seq_start, a.p.n_groups, b);
+    return b >= __ldg(a.p.seq_start + g) && b < __ldg(a.p.seq_start + g + 1) ? g : -1;
+}
+
+// Sixteen-bit types as the kernels need them.
+template <typename P>
+struct Bits16 {  // __nv_bfloat16
+    static constexpr float kLift = 0.f;
+    static constexpr uint32_t kFormat = 1;  // of an instruction descriptor's operand
+    QD_DEV static uint32_t pack(float a, float b) { return RowType<__nv_bfloat16>::two(a, b); }
+    QD_DEV static float2 unpack(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+};
+template <>
+struct Bits16<__half> {
+    // fp16 weights are lifted: below 2^-14 they lose bits, and the largest is 2^8 before
+    static constexpr float kLift = 7.f;
+    static constexpr uint32_t kFormat = 0;
+    QD_DEV static uint32_t pack(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+    QD_DEV static float2 unpack(uint32_t w) { return __half22float2(u32_as_h2(w)); }
+};
+
+template <typename P>
+QD_DEV void store_out4(P *p, const float4 &v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(Bits16<P>::pack(v.x, v.y), Bits16<P>::pack(v.z, v.w));
+}
+
+// Partial results joined one after another: their outputs are divided by their own sums, `top` is log2 of them.
+struct Kv16Join {
+    float top = -INFINITY, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    // kN at a time, so that their loads are under way together
+    template <int kN>
+    QD_DEV void add(const float (&t)[kN], const float4 (&o)[kN]) {
+        float to = top;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) to = fmaxf(to, t[i]);
+        const float ref = to == -INFINITY ? 0.f : to, k = ex2(top - ref);
+        top = to;
+        sum *= k;
+        v = make_float4(v.x * k, v.y * k, v.z * k, v.w * k);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            if (t[i] == -INFINITY) continue;
+            const float w = ex2(t[i] - ref);
+            sum += w;
+            v = make_float4(fmaf(o[i].x, w, v.x), fmaf(o[i].y, w, v.y), fmaf(o[i].z, w, v.z), fmaf(o[i].w, w, v.w));
+        }
+    }
+    QD_DEV void add_parts(const Kv16Parts &p, int d4) {
+        for (int i0 = 0; i0 < p.n; i0 += 8) {
+            float t[8];
+            float4 o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool in = i0 + i < p.n;
+                t[i] = in ? __ldcg(p.top + (i0 + i) * p.step) : -INFINITY;
+                o[i] = in ? __ldcg(reinterpret_cast<const float4 *>(p.o + (i0 + i) * p.step + (int64_t)d4 * kTileLanes * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            add(t, o);
+        }
+    }
+    QD_DEV float4 value() const {
+        const float k = sum == 0.f ? 0.f : 1.f / sum;
+        return make_float4(v.x * k, v.y * k, v.z * k, v.w * k);
+    }
+    QD_DEV float log_sum() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
+};
+
+bool kv16_few_rows(const llm_kv16_cache &c, int Hq, int n_rows);
+cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int32_t *plan, float *wide);
+
+}  // namespace qd

@@ -22,7 +22,7 @@ int dtype_size(int32_t t) {
 // A row array: 16-byte aligned rows of `width` elements that do not overlap.
 bool rows_ok(const void *p, int64_t stride, int64_t width, int32_t dtype) {
     const int size = dtype_size(dtype);
-    return size && aligned(p, 16) && stride >= width && stride <= (int64_t)1 << 40 && (stride * size) % 16 == 0;
+    return size && aligned(p, 16) && stride >= width && stride < (int64_t)1 << 38 && (stride * size) % 16 == 0;  // 2^40 bytes: a tensor map's limit
 }
 
 bool cache_ok(const llm_kv16_cache *c) {
