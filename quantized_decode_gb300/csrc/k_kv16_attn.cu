@@ -19,6 +19,7 @@
 // in the workspace, and the last to arrive (a counter) joins them in the order of the parts: the result does not
 // depend on who is last.
 #include "kv16_attn.cuh"
+#include "kv16_line.cuh"
 
 namespace qd {
 
@@ -33,44 +34,6 @@ constexpr float kLag = 4.f;
 template <int D>
 constexpr int kPartFloats = kRows * (D + 1);  // [row][D], [row] log2 of the sum
 
-template <typename P>
-QD_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-QD_DEV void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 8 x 8 of 16 bits: rows and columns exchanged over the warp
-QD_DEV uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-QD_DEV int parts_of(int pages, int share) { return (int)((unsigned)(pages + share - 1) / (unsigned)share); }
-
-QD_DEV int block_sum(int x, int *scratch) {
-    x = (int)__reduce_add_sync(kFullMask, (unsigned)x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-    __syncthreads();
-    return scratch[0] + scratch[1] + scratch[2] + scratch[3];
-}
-QD_DEV float block_sum(float x, int *scratch) {  // the same in every thread
-    x = warp_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = __float_as_int(x);
-    __syncthreads();
-    return __int_as_float(scratch[0]) + __int_as_float(scratch[1]) + (__int_as_float(scratch[2]) + __int_as_float(scratch[3]));
-}
-
 template <typename P, int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_constant__ Kv16AttnArgs a, int32_t *counters, float *parts_at,
                                                                  const int4 *plan, const float *wide) {
@@ -81,109 +44,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     constexpr int kRow = D + 4;  // floats of a row in the merge buffer
     __shared__ __align__(16) float merge_o[kWarps][kRows][kRow];
     __shared__ float s_top[kWarps][kRows];
-    __shared__ int s_sum[kWarps], s_run[kWarps][2], s_last;
+    __shared__ int s_last;
     extern __shared__ int upto[];  // items that end with sequence b: [n_seqs], and of those the cut ones
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs, ctas = (int)gridDim.x;
 
-    // ---- the cut: each thread counts for B / 128 sequences, one after another
-    const int per_thread = (B + kThreads - 1) / kThreads, b0 = threadIdx.x * per_thread, b1 = min(b0 + per_thread, B);
-    int share;
-    {
-        int segs = 0, tiles0 = 0, pages0 = 1, longest = 1;  // tiles0, pages0: of b0, read once in calls of few sequences
-        float total = 0.f;
-        for (int b = b0; b < b1; ++b) {
+    const int share = kv16_cut<kWarps>(
+        B, ctas, kLeast,
+        [&](int b) {
             const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
-            if (!s.ok && blockIdx.x == 0) kv8_report(a.err);
-            const int tiles = (s.rows * G + kRows - 1) / kRows, pages = kv8_pages(s.kv);
-            if (b == b0) {
-                tiles0 = tiles;
-                pages0 = pages;
-            }
-            segs += tiles * Hkv;
-            total += (float)(tiles * Hkv) * (float)pages;
-            if (tiles) longest = max(longest, pages);
-        }
-        const float all = block_sum(total, s_sum);
-        const int all_segs = block_sum(segs, s_sum);
-        longest = (int)__reduce_max_sync(kFullMask, (unsigned)longest);
-        __syncthreads();
-        if (lane == 0) s_sum[warp] = longest;
-        __syncthreads();
-        longest = max(max(s_sum[0], s_sum[1]), max(s_sum[2], s_sum[3]));
-        // total / n, a little more rather than less (floats carry 24 bits)
-        auto over = [&](int n) { return (int)fminf(__fdividef(all, (float)n) * 1.00001f + 1.f, (float)longest); };
-        auto items_at = [&](int sh) {
-            int n = tiles0 * Hkv * parts_of(pages0, sh);
-            for (int b = b0 + 1; b < b1; ++b) {
-                const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
-                n += (s.rows * G + kRows - 1) / kRows * Hkv * parts_of(kv8_pages(s.kv), sh);
-            }
-            return block_sum(n, s_sum);
-        };
-        share = min(max(kLeast, over(ctas)), longest);
-        if (2 * all_segs <= ctas && items_at(share) > ctas) {
-            // at total / (ctas - segs) they fit: the sum of ceil(p / s) is at most total / s + segs
-            int bad = share, good = max(over(ctas - all_segs), bad);
-#pragma unroll 1
-            for (int i = 0; i < 5 && good - bad > 1; ++i) {
-                const int half = bad + (good - bad) / 2;
-                if (items_at(half) <= ctas) good = half;
-                else bad = half;
-            }
-            share = good;
-        }
-        // ---- running sums of the items, and of those of cut segments
-        int mine = 0, mine_cut = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
-            const int n = parts_of(kv8_pages(s.kv), share), items = (s.rows * G + kRows - 1) / kRows * Hkv * n;
-            mine += items;
-            mine_cut += n > 1 ? items : 0;
-            upto[b] = mine;
-            upto[B + b] = mine_cut;
-        }
-        int run = mine, run_cut = mine_cut;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int v = __shfl_up_sync(kFullMask, run, m), w = __shfl_up_sync(kFullMask, run_cut, m);
-            if (lane >= m) {
-                run += v;
-                run_cut += w;
-            }
-        }
-        if (lane == 31) {
-            s_run[warp][0] = run;
-            s_run[warp][1] = run_cut;
-        }
-        __syncthreads();
-        int before = run - mine, before_cut = run_cut - mine_cut;
-        for (int w = 0; w < warp; ++w) {
-            before += s_run[w][0];
-            before_cut += s_run[w][1];
-        }
-        for (int b = b0; b < b1; ++b) {
-            upto[b] += before;
-            upto[B + b] += before_cut;
-        }
-        __syncthreads();
-    }
+            return Kv16Line{(s.rows * G + kRows - 1) / kRows * Hkv, kv8_pages(s.kv), s.ok};
+        },
+        upto, blockIdx.x == 0 ? a.err : nullptr);
     const int items = upto[B - 1];
     bool waited = false;
 
     for (int item = (int)blockIdx.x; item < items; item += ctas) {
         // ---- the item's sequence: the first whose items end behind it
-        int b = 0;
-        for (int n = B; n > 1;) {
-            const int step = (n + 31) / 32, i = lane * step + step - 1;
-            const int passed = __popc(__ballot_sync(kFullMask, i < n && upto[min(b + i, B - 1)] <= item));
-            b += passed * step;
-            n = min(n - passed * step, step);
-        }
+        const int b = kv16_find(upto, B, item);
         const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
         const int in = item - (b > 0 ? upto[b - 1] : 0), place = b > 0 ? upto[B + b - 1] : 0;
         // tiles fastest: those that read the same pages run side by side
-        const int pages = kv8_pages(s.kv), tiles = (s.rows * G + kRows - 1) / kRows, parts = parts_of(pages, share);
+        const int pages = kv8_pages(s.kv), tiles = (s.rows * G + kRows - 1) / kRows, parts = kv16_parts_of(pages, share);
         const int hp = (int)((unsigned)in / (unsigned)tiles), tile = in - hp * tiles;
         const int head = (int)((unsigned)hp / (unsigned)parts), part = hp - head * parts;
         const int p0 = (int)((int64_t)pages * part / parts), p1 = (int)((int64_t)pages * (part + 1) / parts);

@@ -15,7 +15,7 @@
 // The maximum that the exponent refers to follows the row's only when that has grown by 2^kLag, so O is rarely rescaled.
 // Weights are rounded to the pages' type once; their sum is taken before.
 #include "kv16_attn.cuh"
-#include "kv8_tc.cuh"
+#include "kv16_tc.cuh"
 
 namespace qd {
 
@@ -104,29 +104,6 @@ QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
     return r;
 }
 
-// 128 scores of a lane's row: loads under way together, then one wait that names what it waits for.
-QD_DEV void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
-          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(taddr));
-}
-template <bool WAIT>
-QD_DEV void tmem_ld32_end(uint32_t (&r)[32]) {
-#define QD_ALL32 \
-    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), \
-        "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), \
-        "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), \
-        "+r"(r[31])
-    if (WAIT) asm volatile("tcgen05.wait::ld.sync.aligned;" : QD_ALL32 : : "memory");
-    else asm volatile("" : QD_ALL32 : : "memory");
-#undef QD_ALL32
-}
-
 // A row's softmax of a block, by each lane of a warp: 128 scores at s_at in TMEM, weights in their place, m and l
 // brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on, and of pages that are not
 // there, have no weight.
@@ -182,18 +159,6 @@ QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, ui
     l += sum[0].x + sum[0].y;
 }
 
-QD_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map),
-        "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
-        : "memory");
-}
-QD_DEV void tma_load_rows(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x),
-        "r"(y), "r"(ptx::smem_u32(bar))
-        : "memory");
-}
 QD_DEV void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <typename P, int D>
@@ -547,27 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
     }
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-// cuTensorMapEncodeTiled through the runtime's driver entry point (null if unavailable)
-EncodeFn encoder() {
-    static EncodeFn enc = []() -> EncodeFn {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<EncodeFn>(p);
-        return nullptr;
-    }();
-    return enc;
-}
-bool encode(CUtensorMap *map, int dims, const void *p, const cuuint64_t *size, const cuuint64_t *stride, const cuuint32_t *box) {
-    const cuuint32_t step[3] = {1, 1, 1};
-    return encoder() && encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, dims, const_cast<void *>(p), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename P, int D>
 cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
     auto kernel = k_wide<P, D>;
@@ -598,13 +542,8 @@ cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bo
     const int64_t units = (a.p.n_groups ? kv16_units(a.n_rows, G, a.p.n_groups) : 0) + (own ? kv16_units(a.n_rows, G, a.c.n_seqs) : 0);
     w.capacity = units * a.c.n_kv_heads + n_sm;
     if (w.capacity > INT32_MAX) return cudaErrorInvalidValue;
-    const cuuint64_t rows = (cuuint64_t)a.c.n_pool_pages * a.c.n_kv_heads * kKv8Page;
-    const cuuint64_t size[2] = {(cuuint64_t)D, rows}, stride[1] = {(cuuint64_t)D * 2};
-    const cuuint32_t box[2] = {64, kKv8Page};
-    const cuuint64_t q_size[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.n_rows}, q_stride[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
-    const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)kv16_tile_rows(G)};
-    if (!encode(&w.k, 2, a.c.k_pool, size, stride, box) || !encode(&w.v, 2, a.c.v_pool, size, stride, box) ||
-        !encode(&w.q, 3, a.q, q_size, q_stride, q_box))
+    if (!kv16_page_map(&w.k, a.c.k_pool, a.c) || !kv16_page_map(&w.v, a.c.v_pool, a.c) ||
+        !kv16_row_map(&w.q, a.q, a.q_stride, a.n_rows, a.Hq, G, kv16_tile_rows(G), D))
         return cudaErrorInvalidValue;
     const unsigned blocks = (unsigned)w.capacity;
     if (a.c.dtype == LLM_DTYPE_F16) return D == 128 ? wide<__half, 128>(s, w, blocks) : wide<__half, 64>(s, w, blocks);

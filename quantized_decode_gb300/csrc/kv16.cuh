@@ -54,4 +54,21 @@ QD_DEV Kv16Group kv16_group(const Kv16AttnArgs &a, int g) {
     return r;
 }
 
+// Sixteen-bit types as the kernels need them.
+template <typename P>
+struct Bits16 {  // __nv_bfloat16
+    static constexpr float kLift = 0.f;
+    static constexpr uint32_t kFormat = 1;  // of an instruction descriptor's operand
+    QD_DEV static uint32_t pack(float a, float b) { return RowType<__nv_bfloat16>::two(a, b); }
+    QD_DEV static float2 unpack(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+};
+template <>
+struct Bits16<__half> {
+    // fp16 weights are lifted: below 2^-14 they lose bits, and the largest is 2^8 before
+    static constexpr float kLift = 7.f;
+    static constexpr uint32_t kFormat = 0;
+    QD_DEV static uint32_t pack(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+    QD_DEV static float2 unpack(uint32_t w) { return __half22float2(u32_as_h2(w)); }
+};
+
 }  // namespace qd

@@ -58,23 +58,6 @@ QD_DEV int kv16_group_of(const Kv16AttnArgs &a, int b) {
     return b >= __ldg(a.p.seq_start + g) && b < __ldg(a.p.seq_start + g + 1) ? g : -1;
 }
 
-// Sixteen-bit types as the kernels need them.
-template <typename P>
-struct Bits16 {  // __nv_bfloat16
-    static constexpr float kLift = 0.f;
-    static constexpr uint32_t kFormat = 1;  // of an instruction descriptor's operand
-    QD_DEV static uint32_t pack(float a, float b) { return RowType<__nv_bfloat16>::two(a, b); }
-    QD_DEV static float2 unpack(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
-};
-template <>
-struct Bits16<__half> {
-    // fp16 weights are lifted: below 2^-14 they lose bits, and the largest is 2^8 before
-    static constexpr float kLift = 7.f;
-    static constexpr uint32_t kFormat = 0;
-    QD_DEV static uint32_t pack(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
-    QD_DEV static float2 unpack(uint32_t w) { return __half22float2(u32_as_h2(w)); }
-};
-
 template <typename P>
 QD_DEV void store_out4(P *p, const float4 &v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(Bits16<P>::pack(v.x, v.y), Bits16<P>::pack(v.z, v.w));
