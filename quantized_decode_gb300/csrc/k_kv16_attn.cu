@@ -26,7 +26,7 @@ namespace qd {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
-constexpr int kLeast = kWarps;  // pages of a part at least: one for each warp
+constexpr int kLeast = 2 * kWarps;  // pages of a part at least
 // Partial results joined at once: up to kMaxJoin in one step, else in groups.
 constexpr int kGroupJoin = 8, kMaxJoin = 24;
 constexpr float kLag = 4.f;
@@ -36,7 +36,7 @@ constexpr int kPartFloats = kRows * (D + 1);  // [row][D], [row] log2 of the sum
 
 template <typename P, int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_constant__ Kv16AttnArgs a, int32_t *counters, float *parts_at,
-                                                                 const int4 *plan, const float *wide) {
+                                                                 const Kv16Plan plan) {
     using T = Bits16<P>;
     constexpr int KP = D / 32;   // 16-byte pieces of a token's K that a lane holds
     constexpr int VP = D / 64;   // of its V
@@ -249,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
         }
         __syncthreads();
         // the group's plan, for the results of its prefix
-        int4 front = make_int4(0, 0, 0, 0);
-        int front_row = 0;
+        int front = -1, front_row = 0, front_blocks = 0;
         auto look_ahead = [&]() {  // by the whole warp, before results are written
             const int group = kv16_group_of(a, b);
             if (group < 0) return;
@@ -258,12 +257,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
             if (!gr.ok || gr.len == 0 || s.row0 < gr.row0 || s.row0 + s.rows > gr.row0 + gr.rows) return;
             if (!waited) pdl_wait();
             waited = true;
-            front = __ldcg(plan + group);
+            front = group;
             front_row = s.row0 - gr.row0;
+            front_blocks = (gr.len - 1) / kKeyBlock + 1;
         };
         auto write_out = [&](Kv16Join &join, int row, int d4) {
             const int rr = tile * kRows + row, i = rr / G, hq = rr % G;
-            if (front.z > 0) join.add_parts(kv16_parts(front, wide, D, G, head, hq, front_row + i), d4);
+            if (front >= 0) join.add_parts(kv16_parts(plan, front, true, front_blocks, D, G, head, hq, front_row + i), d4);
             const int64_t at = (int64_t)(s.row0 + i) * a.Hq + head * G + hq;
             store_out4((P *)a.out + at * D + 4 * d4, join.value());
             if (d4 == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
 
 // ---- the rows of wide calls: their partial results joined, one warp for each row and head
 template <typename P, int D>
-__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnArgs a, const int4 *plan, const float *wide) {
+__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan) {
     const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads, G = a.Hq / Hkv;
     const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), row = id / a.Hq;
     pdl_wait();
@@ -347,16 +347,16 @@ __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnAr
     const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
     if (row < s.row0 || row >= s.row0 + s.rows) return;
     const int group = kv16_group_of(a, b), d4 = lane % (D / 4);
-    const int4 own = __ldcg(plan + a.p.n_groups + b);
-    if (a.p.n_groups == 0 && own.z == 1) return;  // written already
+    const int own_blocks = s.kv > 0 ? (s.kv - 1) / kKeyBlock + 1 : 1;
+    const Kv16Parts own = kv16_parts(plan, a.p.n_groups + b, false, own_blocks, D, G, h / G, h % G, (int)row - s.row0);
+    if (a.p.n_groups == 0 && own.n == 1) return;  // written already
     Kv16Join join;
     if (group >= 0) {
         const Kv16Group gr = kv16_group(a, group);
-        const int4 front = __ldcg(plan + group);
         if (gr.ok && gr.len > 0 && row >= gr.row0 && row < gr.row0 + gr.rows)
-            join.add_parts(kv16_parts(front, wide, D, G, h / G, h % G, (int)row - gr.row0), d4);
+            join.add_parts(kv16_parts(plan, group, true, (gr.len - 1) / kKeyBlock + 1, D, G, h / G, h % G, (int)row - gr.row0), d4);
     }
-    join.add_parts(kv16_parts(own, wide, D, G, h / G, h % G, (int)row - s.row0), d4);
+    join.add_parts(own, d4);
     const int64_t at = row * a.Hq + h;
     if (lane < D / 4) store_out4((P *)a.out + at * D + 4 * d4, join.value());
     if (lane == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
@@ -378,8 +378,7 @@ cudaError_t launch_behind(bool behind, void (*kernel)(Args...), unsigned blocks,
     return cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
 }
 
-// Fields of the workspace behind the counters: the partial results of the kernel for few rows, the plan (one int4 for each
-// group and sequence), the wide kernel's partial results.
+// Fields of the workspace behind the counters: the partial results of the kernel for few rows, the plan, the wide kernel's partial results.
 struct Space {
     int64_t parts, plan, wide, bytes;
 };
@@ -389,7 +388,7 @@ Space space_of(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_ro
     Space s;
     s.parts = kKv16Counters * 4;
     s.plan = up(s.parts + (int64_t)kKv16Counters * (c.head_dim == 128 ? kPartFloats<128> : kPartFloats<64>) * 4);
-    s.wide = up(s.plan + 16 * ((int64_t)n_groups + c.n_seqs));
+    s.wide = up(s.plan + 16 * (1 + (int64_t)n_groups + c.n_seqs));
     const int G = Hq / c.n_kv_heads;
     int64_t units = n_groups ? kv16_units(n_rows, G, n_groups) : 0;
     if (own) units += kv16_units(n_rows, G, c.n_seqs);
@@ -401,17 +400,18 @@ template <typename P, int D>
 cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
     const Space at = space_of(n_sm, a.c, a.p.n_groups, a.Hq, a.n_rows);
     uint8_t *space = (uint8_t *)a.workspace;
-    int4 *plan = (int4 *)(space + at.plan);
+    int4 *plan_at = (int4 *)(space + at.plan);
     float *wide = (float *)(space + at.wide);
+    const Kv16Plan plan = {plan_at, wide};
     const bool own = !kv16_few_rows(a.c, a.Hq, a.n_rows);
     if (own || a.p.n_groups) {
-        const cudaError_t e = launch_kv16_wide(s, n_sm, a, own, (int32_t *)plan, wide);
+        const cudaError_t e = launch_kv16_wide(s, n_sm, a, own, plan_at, wide);
         if (e != cudaSuccess) return e;
     }
     if (own) {
         const int64_t blocks = ((int64_t)a.n_rows * a.Hq + 3) / 4;
         if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        return launch_behind(true, k_join<P, D>, (unsigned)blocks, 128, 0, s, a, plan, wide);
+        return launch_behind(true, k_join<P, D>, (unsigned)blocks, 128, 0, s, a, plan);
     }
     auto kernel = k_attend<P, D>;
     const size_t bytes = 8 * (size_t)a.c.n_seqs;
@@ -421,7 +421,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
     const int64_t segs = ((int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) / kRows + a.c.n_seqs) * a.c.n_kv_heads, ctas = kCtasPerSm * n_sm;
     const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
     return launch_behind(a.p.n_groups > 0, kernel, (unsigned)(most < ctas ? most : ctas), kThreads, bytes, s, a, (int32_t *)space,
-                         (float *)(space + at.parts), plan, wide);
+                         (float *)(space + at.parts), plan);
 }
 
 }  // namespace

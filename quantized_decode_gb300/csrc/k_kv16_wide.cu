@@ -21,9 +21,7 @@ namespace qd {
 
 namespace {
 
-constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 12 * 32;
-constexpr int kRegsSoftmax = 208, kRegsRest = 88;  // 168 at launch
-static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "no more than the launch has");
+constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 10 * 32;  // 200 registers a thread
 constexpr int kStages = 2, kRecs = 4;
 constexpr int kLeastBlocks = 2;  // of a part: one for each tile
 constexpr float kLag = 8.f;
@@ -33,7 +31,7 @@ struct WideArgs {
     CUtensorMap q, k, v;
     int4 *plan;
     float *wide;
-    int spans, ctas;   // ctas: what the keys are cut for
+    int spans;
     int64_t capacity;  // places
 };
 
@@ -45,36 +43,33 @@ struct Cfg {
     static_assert(kTileLanes * D * 4 <= 2 * kTileBytes, "a tile's output takes the place of q");
 };
 
-struct Bars {
-    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_part, s_full[2], p_full[2], o_full[2], done,
-        rec_full[kRecs];
-    uint32_t rec[kRecs];  // pages of a block that are there
-    uint32_t tmem;
-    float top[kTileLanes];
-    int abort;
-};
-
-// How many blocks a part has, and the segments; every warp for itself.
+// How a call's segments are cut (kv16_attn.cuh); every warp for itself.  One CTA for each part, all of about the same length, while there are
+// at most half as many segments as CTAs: parts begin where segments do, and a CTA has one.  Else the line: a CTA has an equal
+// share of all blocks, in one piece more than there are ends of segments in it.
 struct Cut {
-    int share;
-    int64_t segs;
+    int share;       // blocks of a part, 0: a line
+    int64_t length;  // of the line: blocks, and kPieceCost for each segment
+    bool fits;       // as many places as there are; else row_start falls somewhere
 };
 QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
-    const int lane = threadIdx.x & 31;
-    float total = 0.f;
-    int64_t segs = 0;
+    const int lane = threadIdx.x & 31, ctas = (int)gridDim.x;
+    int64_t total = 0, segs = 0;
     int longest = 1;
     for (int i = lane; i < w.spans; i += 32) {
         const Kv16Span s = kv16_span(w.a, i, err);
-        const int u = s.units(G), n = s.blocks();
-        segs += (int64_t)u * Hkv;
-        total += (float)u * (float)Hkv * (float)n;
-        if (u) longest = max(longest, n);
+        const int64_t u = (int64_t)s.units(G) * Hkv;
+        segs += u;
+        total += u * s.blocks();
+        if (u) longest = max(longest, s.blocks());
     }
-    total = warp_sum(total);
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) segs += __shfl_xor_sync(kFullMask, segs, m);
+    for (int m = 16; m > 0; m >>= 1) {
+        segs += __shfl_xor_sync(kFullMask, segs, m);
+        total += __shfl_xor_sync(kFullMask, total, m);
+    }
     longest = __reduce_max_sync(kFullMask, longest);
+    Cut r = {0, total + segs * kPieceCost, segs + ctas <= w.capacity};
+    if (2 * segs > ctas || segs == 0) return r;
     auto items_at = [&](int share) {
         int n = 0;
         for (int i = lane; i < w.spans; i += 32) {
@@ -83,26 +78,104 @@ QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
         }
         return (int)__reduce_add_sync(kFullMask, (unsigned)n);
     };
-    // total / n, a little more rather than less (floats carry 24 bits)
-    auto over = [&](int n) { return (int)fminf(__fdividef(total, (float)n) * 1.00001f + 1.f, (float)longest); };
-    Cut r;
-    r.segs = segs;
-    r.share = min(max(kLeastBlocks, over(w.ctas)), longest);
-    // The smallest share that leaves no more items than SMs, so that all end together; with more segments than half the SMs, or too many
-    // spans to count again, the average load.
-    if (2 * segs <= w.ctas && w.spans <= 256 && items_at(r.share) > w.ctas) {
-        // at total / (ctas - segs) they fit: the sum of ceil(p / s) is at most total / s + segs
-        int bad = r.share, good = max(over(w.ctas - (int)segs), bad);
+    auto over = [&](int64_t n) { return (int)min((total + n - 1) / n, (int64_t)longest); };
+    // the smallest share that leaves no more parts than CTAs: at total / (ctas - segs) they fit, since the sum of ceil(p / s) is at most
+    // total / s + segs
+    int bad = max(kLeastBlocks - 1, over(ctas) - 1), good = max(kLeastBlocks, over(ctas - segs));
+    if (bad + 1 < good && items_at(bad + 1) <= ctas) good = bad + 1;
 #pragma unroll 1
-        for (int i = 0; i < 6 && good - bad > 1; ++i) {
-            const int mid = bad + (good - bad) / 2;
-            if (items_at(mid) <= w.ctas) good = mid;
-            else bad = mid;
-        }
-        r.share = good;
+    for (int i = 0; i < 6 && good - bad > 1; ++i) {
+        const int mid = bad + (good - bad) / 2;
+        if (items_at(mid) <= ctas) good = mid;
+        else bad = mid;
     }
+    r.share = good;
     return r;
 }
+
+// A piece of work: blocks blk0 .. blk1 - 1 of a segment, and the place of its result.
+struct Piece {
+    Kv16Span s;
+    int span, units, unit, head, blk0, blk1;
+    int64_t place;
+};
+// The CTA's piece that begins at `at` (the number of a part, or a place on the line, up to `end`), and at becomes where the next begins.  By
+// the whole warp.  plan: written by the first CTA's first warp as it goes through the spans, which it then does to the last.
+QD_DEV bool next_piece(const WideArgs &w, const Cut &cut, int G, int Hkv, int64_t &at, int64_t end, int4 *plan, Piece &p) {
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0, segs = 0;
+    bool found = false;
+    for (int i0 = 0; i0 < w.spans; i0 += 32) {
+        Kv16Span mine = {0, 0, 0, -1};
+        if (i0 + lane < w.spans) mine = kv16_span(w.a, i0 + lane, nullptr);
+        const int u = cut.fits ? mine.units(G) : 0, n = cut.share ? (mine.blocks() + cut.share - 1) / cut.share : mine.blocks() + kPieceCost;
+        const int64_t my_segs = (int64_t)u * Hkv, items = my_segs * n;
+        int64_t upto = items, upto_segs = my_segs;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t v = __shfl_up_sync(kFullMask, upto, m), x = __shfl_up_sync(kFullMask, upto_segs, m);
+            if (lane >= m) {
+                upto += v;
+                upto_segs += x;
+            }
+        }
+        const int64_t before = base + upto - items, segs_before = segs + upto_segs - my_segs;
+        if (plan && i0 + lane < w.spans)
+            plan[1 + i0 + lane] = cut.share ? make_int4((int)before, u, n, 0) : make_int4((int)segs_before, u, (int)before, (int)(before >> 32));
+        const unsigned hit = __ballot_sync(kFullMask, at < base + upto);
+        if (hit && !found && at < end) {
+            found = true;
+            const int l = __ffs(hit) - 1;
+            const int64_t in = at - __shfl_sync(kFullMask, before, l), seg0 = __shfl_sync(kFullMask, segs_before, l);
+            const int count = __shfl_sync(kFullMask, n, l);
+            p.span = i0 + l;
+            p.units = __shfl_sync(kFullMask, u, l);
+            p.s.row0 = __shfl_sync(kFullMask, mine.row0, l);
+            p.s.rows = __shfl_sync(kFullMask, mine.rows, l);
+            p.s.len = __shfl_sync(kFullMask, mine.len, l);
+            p.s.seq = __shfl_sync(kFullMask, mine.seq, l);
+            const int nb = p.s.blocks();
+            if (cut.share) {
+                // units fastest: those that read the same pages run side by side
+                const int hp = (int)(in / p.units), part = hp % count;
+                p.unit = (int)(in - (int64_t)hp * p.units);
+                p.head = hp / count;
+                p.blk0 = (int)((int64_t)nb * part / count);
+                p.blk1 = (int)((int64_t)nb * (part + 1) / count);
+                p.place = at;
+                at = end;
+            } else {
+                const int64_t seg = in / count;
+                p.head = (int)(seg / p.units);
+                p.unit = (int)(seg - (int64_t)p.head * p.units);
+                if (p.s.seq >= 0) p.unit = kv16_unit_at(p.unit, p.units);
+                const int from = (int)(in - seg * count), to = (int)min((int64_t)count, from + end - at);
+                p.blk0 = max(0, from - kPieceCost);
+                p.blk1 = max(0, to - kPieceCost);  // equal: the CTA's share ends before the segment's first block
+                p.place = (int64_t)blockIdx.x + seg0 + seg;
+                at += to - from;
+            }
+            if (!plan) return true;
+        }
+        base += __shfl_sync(kFullMask, upto, 31);
+        segs += __shfl_sync(kFullMask, upto_segs, 31);
+    }
+    return found;
+}
+
+struct Bars {
+    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], v_part, s_full[2], p_full[2], o_full[2], done,
+        rec_full[kRecs];
+    uint32_t rec[kRecs];  // pages of a block that are there
+    uint32_t tmem;
+    float top[kTileLanes];
+    int abort;
+    // the CTA's place in the work, kept here and not in registers: the softmax needs them all
+    Cut cut;
+    Piece piece;
+    int64_t at, end;
+    int found;
+};
 
 // A row's softmax of a block, by each lane of a warp: 128 scores at s_at in TMEM, weights in their place, m and l
 // brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on, and of pages that are not
@@ -173,343 +246,332 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, R = kv16_tile_rows(G);
     pdl_launch();
-
-    // ---- the item: a scan over the spans, 32 at a time; the first CTA writes the plan down as it goes
-    const Cut cut = cut_spans(w, G, Hkv, blockIdx.x == 0 && warp == 0 ? a.err : nullptr);
-    Kv16Span s = {0, 0, 0, -1};
-    int span = -1, units = 0, parts = 0;
-    int64_t base = 0, in = 0;
-    for (int i0 = 0; i0 < w.spans; i0 += 32) {
-        Kv16Span mine = {0, 0, 0, -1};
-        if (i0 + lane < w.spans) mine = kv16_span(a, i0 + lane, nullptr);
-        const int u = mine.units(G), n = (mine.blocks() + cut.share - 1) / cut.share;
-        const int64_t items = (int64_t)u * Hkv * n;
-        int64_t upto = items;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int64_t v = __shfl_up_sync(kFullMask, upto, m);
-            if (lane >= m) upto += v;
-        }
-        if (blockIdx.x == 0 && warp == 0 && i0 + lane < w.spans) {
-            const bool fits = base + upto <= w.capacity;  // else row_start falls somewhere
-            if (!fits) kv8_report(a.err);
-            w.plan[i0 + lane] = make_int4((int)(base + upto - items), u, fits && u > 0 ? n : 0, 0);
-        }
-        const unsigned hit = __ballot_sync(kFullMask, (int64_t)blockIdx.x < base + upto);
-        if (hit && span < 0) {
-            const int l = __ffs(hit) - 1;
-            span = i0 + l;
-            in = (int64_t)blockIdx.x - base - __shfl_sync(kFullMask, upto - items, l);
-            units = __shfl_sync(kFullMask, u, l);
-            parts = __shfl_sync(kFullMask, n, l);
-            s.row0 = __shfl_sync(kFullMask, mine.row0, l);
-            s.rows = __shfl_sync(kFullMask, mine.rows, l);
-            s.len = __shfl_sync(kFullMask, mine.len, l);
-            s.seq = __shfl_sync(kFullMask, mine.seq, l);
-            if (base + __shfl_sync(kFullMask, upto, l) > w.capacity) units = 0;
-            if (blockIdx.x != 0) break;
-        }
-        base += __shfl_sync(kFullMask, upto, 31);
-    }
-    if (span < 0 || units == 0) return;
-    // units fastest: those that read the same pages run side by side
-    const int hp = (int)(in / units), unit = (int)(in - (int64_t)hp * units), head = hp / parts, part = hp - head * parts;
-    const int row0 = unit * 2 * R, rows = min(2 * R, s.rows - row0);  // of the span
-    const bool pair = rows > R;                                        // two tiles of rows, else one for every other block
-    const bool prefix = s.seq < 0;
-    // tokens that any row of the item sees, and this part's blocks of them; tokens are counted from the first one's on
-    const int all = prefix ? s.len : max(0, s.len - s.rows + row0 + rows);
-    const int nb_span = s.blocks(), blk0 = (int)((int64_t)nb_span * part / parts), blk1 = (int)((int64_t)nb_span * (part + 1) / parts);
-    const int nb = max(0, min(blk1, kv8_blocks(all, kKeyBlock)) - blk0), seen = all - blk0 * kKeyBlock;
-    auto tile_blocks = [&](int t) { return pair ? nb : (nb - t + 1) / 2; };
-    auto block_of = [&](int t, int i) { return pair ? i : 2 * i + t; };
-
-    if (threadIdx.x == 0) {
-        mbar_init(&b.q_full, 1);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&b.k_full[i], 1);
-            mbar_init(&b.k_empty[i], 1);
-            mbar_init(&b.v_full[i], 1);
-            mbar_init(&b.v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_full[i], 4);
-            mbar_init(&b.o_full[i], 1);
-        }
-        for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
-        mbar_init(&b.v_part, 1);
-        mbar_init(&b.done, 1);
-        b.abort = 0;
-        mbar_fence_init();
-    }
-    if (warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = b.tmem;
-    auto s_at = [&](int t) { return tmem + (uint32_t)(t * 128); };
-    auto o_at = [&](int t) { return tmem + (uint32_t)((2 + t) * 128); };
-    auto fail = [&]() {
-        *abort = 1;
-        if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
-    };
-    auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
-        if (!tc_wait(bar, phase & 1u, abort)) {
-            fail();
-            return false;
-        }
-        return true;
-    };
-    auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
-    if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
-
-    if (warp < kSoftmax) {
-        // ================= softmax =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int t = warp >> 2, lane_of = (warp & 3) * 32 + lane;
-        const int i = lane_of / G, row = (pair ? t * R : 0) + i;  // of the unit
-        const bool live = i < R && row < rows;
-        // tokens of this part that the row sees; rows that are not there hide nothing
-        const int limit = prefix ? seen : (live ? max(0, s.len - s.rows + row0 + row + 1) - blk0 * kKeyBlock : INT32_MAX);
-        const int shortest = __reduce_min_sync(kFullMask, limit);
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
-        const int n = tile_blocks(t);
-        float m = -INFINITY, l = 0.f;
-        bool fine = true;
-        for (int k = 0; k < n && fine; ++k) {
-            const int j = block_of(t, k);
-            fine = wait_warp(&b.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)k);
-            if (!fine) break;
-            tc_fence_after();
-            const uint32_t ok = b.rec[j % kRecs];
-            const int left = limit - j * kKeyBlock;
-            if (shortest - j * kKeyBlock < kKeyBlock || ok != 0xffu) block_weights<P, D, true>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
-            else block_weights<P, D, false>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b.p_full[t]);
-        }
-        // both tiles' products have to be done where one's result takes the place of q; `done` comes after a wait that ran out too
-        const bool some = n > 0;
-        if (nb > 0) fine = wait_warp(pair ? &b.o_full[t] : &b.done, 0) && fine && !*abort;
-        tc_fence_after();
-        float k = some ? kv8_row_factor(fine, l) : 0.f;
-        float top = some ? kv8_row_log2(fine, l, m - Bits16<P>::kLift) : -INFINITY;
-        const bool none = top == -INFINITY;
-        float *mine = w.wide + ((int64_t)blockIdx.x) * kv16_place(D);
-        float4 *other = reinterpret_cast<float4 *>(sq);  // [d / 4][lane]
-        const bool direct = !prefix && parts == 1 && a.p.n_groups == 0;
-        if (!pair) {
-            if (t == 1) {
-#pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                    float v[32];
-                    tmem_ld32(o_at(1) + lanes + d, v);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        other[(d + e) / 4 * kTileLanes + lane_of] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
-                }
-                b.top[lane_of] = top;
-            }
-            softmax_sync();
-        }
-        if (pair || t == 0) {
-            float k1 = 0.f;
-            if (!pair) {
-                // the other half's result: weights of the two, which add up to 1
-                const float top1 = b.top[lane_of], most = fmaxf(top, top1), ref = most == -INFINITY ? 0.f : most;
-                const float w0 = none ? 0.f : ex2(top - ref), w1 = top1 == -INFINITY ? 0.f : ex2(top1 - ref), sum = w0 + w1;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                k *= w0 * inv;
-                k1 = w1 * inv;
-                top = sum == 0.f ? -INFINITY : ref + log2f(sum);
-            }
-            const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
-            float *to = mine + (int64_t)t * D * kTileLanes;
-#pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-                float v[32];
-                tmem_ld32(o_at(t) + lanes + d, v);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
-                if (!pair && k1 != 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 x = other[(d + e) / 4 * kTileLanes + lane_of];
-                        v[e] = fmaf(x.x, k1, v[e]);
-                        v[e + 1] = fmaf(x.y, k1, v[e + 1]);
-                        v[e + 2] = fmaf(x.z, k1, v[e + 2]);
-                        v[e + 3] = fmaf(x.w, k1, v[e + 3]);
-                    }
-                }
-                __syncwarp();
-                if (live && direct) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4 *>((P *)a.out + at * D + d + e) =
-                            make_uint4(Bits16<P>::pack(v[e], v[e + 1]), Bits16<P>::pack(v[e + 2], v[e + 3]), Bits16<P>::pack(v[e + 4], v[e + 5]),
-                                       Bits16<P>::pack(v[e + 6], v[e + 7]));
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        __stcg(reinterpret_cast<float4 *>(to + ((int64_t)(d + e) / 4 * kTileLanes + lane_of) * 4), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
-                }
-                __syncwarp();
-            }
-            if (live && !direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + t * kTileLanes + lane_of, top);
-            else if (live && a.lse) a.lse[at] = top * 0.69314718f;
-        }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-        if (warp == kMmaWarp && nb > 0) {
-            // ================= MMA =================
-            const uint32_t type = Bits16<P>::kFormat << 7 | Bits16<P>::kFormat << 10;
-            const uint32_t id_s = umma_idesc_f16_f32(kTileLanes, kKeyBlock) | type, id_o = umma_idesc_f16_f32(kTileLanes, D) | kIdescBMn | type;
-            const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
-            auto scores = [&](int t, int st) {
-                const uint32_t d = s_at(t), qd = q_at + (pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-                    if (kk == 0) mma_ss<false>(d, qd, kd, id_s);
-                    else mma_ss<true>(d, qd + at, kd + at, id_s);
-                }
-            };
-            auto weigh = [&](int t, int st, bool more) {
-                const uint32_t d = o_at(t), p = s_at(t), vd = v_at + st * (C::kTileBytes >> 4);
-                if (more) mma_ts<true>(d, p, vd, id_o);
-                else mma_ts<false>(d, p, vd, id_o);
-#pragma unroll
-                for (int kk = 1; kk < kKeyBlock / 16; ++kk) mma_ts<true>(d, p + kk * 8, vd + kk * (2048 >> 4), id_o);
-            };
-            const bool mine = elect_lane();
-            bool go = wait_warp(&b.q_full, 0);
-            for (int t = 0; t < 2 && go; ++t) {
-                if (tile_blocks(t) == 0) break;
-                const int j = block_of(t, 0);
-                go = wait_warp(&b.k_full[j % kStages], 0);
-                if (!go) break;
-                tc_fence_after();
-                if (mine) {
-                    scores(t, j % kStages);
-                    umma_commit(&b.s_full[t]);
-                    if (!pair || t == 1) umma_commit(&b.k_empty[j % kStages]);
-                }
-                __syncwarp();
-            }
-            for (int k = 0; k < tile_blocks(0) && go; ++k)
-                for (int t = 0; t < 2 && go; ++t) {
-                    const int n = tile_blocks(t);
-                    if (k >= n) break;
-                    const int j = block_of(t, k), jn = block_of(t, k + 1), st = j % kStages, sn = jn % kStages;
-                    const bool last = !pair || t == 1;  // of the tiles that use the block
-                    go = wait_warp(&b.v_full[st], (uint32_t)(j / kStages)) && wait_warp(&b.p_full[t], (uint32_t)k);
-                    if (!go) break;
-                    tc_fence_after();
-                    if (mine) weigh(t, st, k > 0);
-                    __syncwarp();
-                    if (k + 1 < n) {
-                        go = wait_warp(&b.k_full[sn], (uint32_t)(jn / kStages));
-                        if (!go) break;
-                        tc_fence_after();
-                    }
-                    if (mine) {
-                        if (k + 1 < n) {
-                            scores(t, sn);
-                            umma_commit(&b.s_full[t]);
-                            if (last) umma_commit(&b.k_empty[sn]);
-                        } else {
-                            umma_commit(&b.o_full[t]);
-                        }
-                        if (last) umma_commit(&b.v_empty[st]);
-                    }
-                    __syncwarp();
-                }
-            if (mine) umma_commit(&b.done);  // arrives once every MMA issued above has completed
-            __syncwarp();
-            if (!tc_wait(&b.done, 0, nullptr)) fail();
-        }
-        if (warp == kCopyWarp && nb > 0) {
-            // ================= copies =================
-            constexpr uint32_t kPageBytes = kKv8Page * 128;  // of a panel
-            const int page = lane & 7, panel = lane >> 3;
-            const int32_t *table = (prefix ? a.p.page_table + (int64_t)span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
-                                   (int64_t)blk0 * (kKeyBlock / kKv8Page);
-            if (lane == 0) {
-                mbar_expect_tx(&b.q_full, (pair ? 2 : 1) * C::kP * R * G * 128);
-                for (int t = 0; t < (pair ? 2 : 1); ++t)
-                    for (int p = 0; p < C::kP; ++p)
-                        tma_load_3d(smem_u32(sq) + t * C::kTileBytes + p * kPanel, &w.q, p * 64, head * G, s.row0 + row0 + t * R, &b.q_full);
-            }
-            __syncwarp();
-            // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
-            auto entry = [&](int j) {
-                const int p = j * (kKeyBlock / kKv8Page) + page;
-                return j < nb && kv8_page_there(p, seen) ? max(-1, __ldg(table + p)) : -2;
-            };
-            auto checked = [&](int ph) {
-                if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
-                if (panel == 0) kv8_report(a.err);
-                return -1;
-            };
-            const int beyond = a.c.n_pool_pages * Hkv * kKv8Page;  // the row behind the pools: reads as zeros
-            int ph = checked(entry(0)), ph_next = entry(1), started = 0;
-            bool part_started = false, go = true;
-            for (int j = 0; j < nb && go; ++j) {
-                const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + head) * kKv8Page : beyond;
-                const uint32_t use = (uint32_t)(j / kStages), ok = __ballot_sync(kFullMask, ph != -1) & 0xffu;
-                if (use > 0 && !(go = wait_warp(&b.k_empty[st], use - 1))) break;
-                // Record j - kRecs: the scores of block j - kStages, done, were issued behind the weights of a block after it.
-                if (lane == 0) {
-                    b.rec[j % kRecs] = ok;
-                    mbar_arrive(&b.rec_full[j % kRecs]);
-                    mbar_expect_tx(&b.k_full[st], C::kTileBytes);
-                }
-                __syncwarp();
-                if (panel < C::kP) tma_load_rows(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st]);
-                started = 2 * j + 1;
-                const int next = checked(ph_next);
-                ph_next = entry(j + 2);
-                if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
-                // a page of which the last slots hold nothing: they become 0 before V is used
-                const int left = seen - j * kKeyBlock;
-                const bool cut_page = left < kKeyBlock && left % kKv8Page != 0;
-                uint64_t *bar = cut_page ? &b.v_part : &b.v_full[st];
-                if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
-                __syncwarp();
-                if (panel < C::kP) tma_load_rows(smem_u32(sv) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.v, panel * 64, y, bar);
-                if (cut_page) {  // the last block
-                    part_started = true;
-                    if (!(go = wait_warp(bar, 0))) break;
-                    const int end = (left / kKv8Page + 1) * kKv8Page, chunks = (end - left) * 8;
-                    for (int e = lane; e < chunks * C::kP; e += 32)
-                        *reinterpret_cast<uint4 *>(sv + st * C::kTileBytes + e / chunks * kPanel + left * 128 + e % chunks * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.v_full[st]);
-                }
-                started = 2 * j + 2;
-                ph = next;
-            }
-            if (*abort) {  // copies in flight land before the shared memory goes away
-                tc_wait(&b.q_full, 0, nullptr);
-                const int ks = (started + 1) / 2, vs = started / 2;
-                for (int j = max(0, ks - kStages); j < ks; ++j) tc_wait(&b.k_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
-                for (int j = max(0, vs - kStages); j < vs; ++j) tc_wait(&b.v_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
-                if (part_started) tc_wait(&b.v_part, 0, nullptr);
+    if (warp == 0) {
+        const bool first = blockIdx.x == 0;
+        const Cut cut = cut_spans(w, G, Hkv, first ? a.err : nullptr);
+        if (lane == 0) {
+            b.cut = cut;
+            b.at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
+            b.end = cut.share ? (int64_t)blockIdx.x + 1 : cut.length * (blockIdx.x + 1) / gridDim.x;
+            if (first) {
+                w.plan[0] = cut.share ? make_int4(0, 0, 0, 0) : make_int4((int)gridDim.x, 0, (int)max(cut.length, (int64_t)1), (int)(cut.length >> 32));
+                if (!cut.fits) kv8_report(a.err);
             }
         }
         __syncwarp();
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kMmaWarp) {
+    bool working = false;
+    for (;;) {
+        if (warp == 0) {
+            Piece next;
+            int64_t at = b.at;
+            bool found = next_piece(w, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
+            while (found && next.blk0 == next.blk1) found = next_piece(w, b.cut, G, Hkv, at, b.end, nullptr, next);
+            if (lane == 0) {
+                b.at = at;
+                b.found = found;
+                if (found) b.piece = next;
+                if (working)
+                    for (uint64_t *x = &b.q_full; x <= &b.rec_full[kRecs - 1]; ++x) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(x)) : "memory");
+                mbar_init(&b.q_full, 1);
+                for (int i = 0; i < kStages; ++i) {
+                    mbar_init(&b.k_full[i], 1);
+                    mbar_init(&b.k_empty[i], 1);
+                    mbar_init(&b.v_full[i], 1);
+                    mbar_init(&b.v_empty[i], 1);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(&b.s_full[i], 1);
+                    mbar_init(&b.p_full[i], 4);
+                    mbar_init(&b.o_full[i], 1);
+                }
+                for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
+                mbar_init(&b.v_part, 1);
+                mbar_init(&b.done, 1);
+                b.abort = 0;
+                mbar_fence_init();
+            }
+            __syncwarp();
+        }
+        if (!working && warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
+        working = true;
+        tc_fence_before();
+        __syncthreads();
         tc_fence_after();
-        tmem_free(tmem, 512);
+        if (!b.found) break;
+        const Piece &p = b.piece;
+        const Kv16Span &s = p.s;
+        const int head = p.head, row0 = p.unit * 2 * R, rows = min(2 * R, s.rows - row0);  // of the span
+        const bool pair = rows > R;  // two tiles of rows, else one for every other block
+        const bool prefix = s.seq < 0, whole = p.blk0 == 0 && p.blk1 == s.blocks();
+        // tokens that any row of the unit sees, and this piece's blocks of them; tokens are counted from the first one's on
+        const int all = prefix ? s.len : max(0, s.len - s.rows + row0 + rows), blk0 = p.blk0;
+        const int nb = max(0, min(p.blk1, kv8_blocks(all, kKeyBlock)) - blk0), seen = all - blk0 * kKeyBlock;
+        auto tile_blocks = [&](int t) { return pair ? nb : (nb - t + 1) / 2; };
+        auto block_of = [&](int t, int i) { return pair ? i : 2 * i + t; };
+
+        const uint32_t tmem = b.tmem;
+        auto s_at = [&](int t) { return tmem + (uint32_t)(t * 128); };
+        auto o_at = [&](int t) { return tmem + (uint32_t)((2 + t) * 128); };
+        auto fail = [&]() {
+            *abort = 1;
+            if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
+        };
+        auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
+            if (!tc_wait(bar, phase & 1u, abort)) {
+                fail();
+                return false;
+            }
+            return true;
+        };
+        auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
+        if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
+
+        if (warp < kSoftmax) {
+            // ================= softmax =================
+            const int t = warp >> 2, lane_of = (warp & 3) * 32 + lane;
+            const int i = lane_of / G, row = (pair ? t * R : 0) + i;  // of the unit
+            const bool live = i < R && row < rows;
+            // tokens of this part that the row sees; rows that are not there hide nothing
+            const int limit = prefix ? seen : (live ? max(0, s.len - s.rows + row0 + row + 1) - blk0 * kKeyBlock : INT32_MAX);
+            const int shortest = __reduce_min_sync(kFullMask, limit);
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
+            const int n = tile_blocks(t);
+            float m = -INFINITY, l = 0.f;
+            bool fine = true;
+            for (int k = 0; k < n && fine; ++k) {
+                const int j = block_of(t, k);
+                fine = wait_warp(&b.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)k);
+                if (!fine) break;
+                tc_fence_after();
+                const uint32_t ok = b.rec[j % kRecs];
+                const int left = limit - j * kKeyBlock;
+                if (shortest - j * kKeyBlock < kKeyBlock || ok != 0xffu) block_weights<P, D, true>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
+                else block_weights<P, D, false>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_full[t]);
+            }
+            // both tiles' products have to be done where one's result takes the place of q; `done` comes after a wait that ran out too
+            const bool some = n > 0;
+            if (nb > 0) fine = wait_warp(pair ? &b.o_full[t] : &b.done, 0) && fine && !*abort;
+            tc_fence_after();
+            float k = some ? kv8_row_factor(fine, l) : 0.f;
+            float top = some ? kv8_row_log2(fine, l, m - Bits16<P>::kLift) : -INFINITY;
+            const bool none = top == -INFINITY;
+            float *mine = w.wide + p.place * kv16_place(D);
+            float4 *other = reinterpret_cast<float4 *>(sq);  // [d / 4][lane]
+            const bool direct = !prefix && whole && a.p.n_groups == 0;
+            if (!pair) {
+                if (t == 1) {
+    #pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        float v[32];
+                        tmem_ld32(o_at(1) + lanes + d, v);
+    #pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            other[(d + e) / 4 * kTileLanes + lane_of] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
+                    }
+                    b.top[lane_of] = top;
+                }
+                softmax_sync();
+            }
+            if (pair || t == 0) {
+                float k1 = 0.f;
+                if (!pair) {
+                    // the other half's result: weights of the two, which add up to 1
+                    const float top1 = b.top[lane_of], most = fmaxf(top, top1), ref = most == -INFINITY ? 0.f : most;
+                    const float w0 = none ? 0.f : ex2(top - ref), w1 = top1 == -INFINITY ? 0.f : ex2(top1 - ref), sum = w0 + w1;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    k *= w0 * inv;
+                    k1 = w1 * inv;
+                    top = sum == 0.f ? -INFINITY : ref + log2f(sum);
+                }
+                const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
+                float *to = mine + (int64_t)t * D * kTileLanes;
+    #pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    float v[32];
+                    tmem_ld32(o_at(t) + lanes + d, v);
+    #pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
+                    if (!pair && k1 != 0.f) {
+    #pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 x = other[(d + e) / 4 * kTileLanes + lane_of];
+                            v[e] = fmaf(x.x, k1, v[e]);
+                            v[e + 1] = fmaf(x.y, k1, v[e + 1]);
+                            v[e + 2] = fmaf(x.z, k1, v[e + 2]);
+                            v[e + 3] = fmaf(x.w, k1, v[e + 3]);
+                        }
+                    }
+                    __syncwarp();
+                    if (live && direct) {
+    #pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>((P *)a.out + at * D + d + e) =
+                                make_uint4(Bits16<P>::pack(v[e], v[e + 1]), Bits16<P>::pack(v[e + 2], v[e + 3]), Bits16<P>::pack(v[e + 4], v[e + 5]),
+                                           Bits16<P>::pack(v[e + 6], v[e + 7]));
+                    } else if (live) {
+    #pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<float4 *>(to + ((int64_t)(d + e) / 4 * kTileLanes + lane_of) * 4), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                    }
+                    __syncwarp();
+                }
+                if (live && !direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + t * kTileLanes + lane_of, top);
+                else if (live && a.lse) a.lse[at] = top * 0.69314718f;
+            }
+        } else {
+            if (warp == kMmaWarp && nb > 0) {
+                // ================= MMA =================
+                const uint32_t type = Bits16<P>::kFormat << 7 | Bits16<P>::kFormat << 10;
+                const uint32_t id_s = umma_idesc_f16_f32(kTileLanes, kKeyBlock) | type, id_o = umma_idesc_f16_f32(kTileLanes, D) | kIdescBMn | type;
+                const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
+                auto scores = [&](int t, int st) {
+                    const uint32_t d = s_at(t), qd = q_at + (pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
+    #pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                        if (kk == 0) mma_ss<false>(d, qd, kd, id_s);
+                        else mma_ss<true>(d, qd + at, kd + at, id_s);
+                    }
+                };
+                auto weigh = [&](int t, int st, bool more) {
+                    const uint32_t d = o_at(t), x = s_at(t), vd = v_at + st * (C::kTileBytes >> 4);
+                    if (more) mma_ts<true>(d, x, vd, id_o);
+                    else mma_ts<false>(d, x, vd, id_o);
+    #pragma unroll
+                    for (int kk = 1; kk < kKeyBlock / 16; ++kk) mma_ts<true>(d, x + kk * 8, vd + kk * (2048 >> 4), id_o);
+                };
+                const bool mine = elect_lane();
+                bool go = wait_warp(&b.q_full, 0);
+                for (int t = 0; t < 2 && go; ++t) {
+                    if (tile_blocks(t) == 0) break;
+                    const int j = block_of(t, 0);
+                    go = wait_warp(&b.k_full[j % kStages], 0);
+                    if (!go) break;
+                    tc_fence_after();
+                    if (mine) {
+                        scores(t, j % kStages);
+                        umma_commit(&b.s_full[t]);
+                        if (!pair || t == 1) umma_commit(&b.k_empty[j % kStages]);
+                    }
+                    __syncwarp();
+                }
+                for (int k = 0; k < tile_blocks(0) && go; ++k)
+                    for (int t = 0; t < 2 && go; ++t) {
+                        const int n = tile_blocks(t);
+                        if (k >= n) break;
+                        const int j = block_of(t, k), jn = block_of(t, k + 1), st = j % kStages, sn = jn % kStages;
+                        const bool last = !pair || t == 1;  // of the tiles that use the block
+                        go = wait_warp(&b.v_full[st], (uint32_t)(j / kStages)) && wait_warp(&b.p_full[t], (uint32_t)k);
+                        if (!go) break;
+                        tc_fence_after();
+                        if (mine) weigh(t, st, k > 0);
+                        __syncwarp();
+                        if (k + 1 < n) {
+                            go = wait_warp(&b.k_full[sn], (uint32_t)(jn / kStages));
+                            if (!go) break;
+                            tc_fence_after();
+                        }
+                        if (mine) {
+                            if (k + 1 < n) {
+                                scores(t, sn);
+                                umma_commit(&b.s_full[t]);
+                                if (last) umma_commit(&b.k_empty[sn]);
+                            } else {
+                                umma_commit(&b.o_full[t]);
+                            }
+                            if (last) umma_commit(&b.v_empty[st]);
+                        }
+                        __syncwarp();
+                    }
+                if (mine) umma_commit(&b.done);  // arrives once every MMA issued above has completed
+                __syncwarp();
+                if (!tc_wait(&b.done, 0, nullptr)) fail();
+            }
+            if (warp == kCopyWarp && nb > 0) {
+                // ================= copies =================
+                constexpr uint32_t kPageBytes = kKv8Page * 128;  // of a panel
+                const int page = lane & 7, panel = lane >> 3;
+                const int32_t *table = (prefix ? a.p.page_table + (int64_t)p.span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
+                                       (int64_t)blk0 * (kKeyBlock / kKv8Page);
+                if (lane == 0) {
+                    mbar_expect_tx(&b.q_full, (pair ? 2 : 1) * C::kP * R * G * 128);
+                    for (int t = 0; t < (pair ? 2 : 1); ++t)
+                        for (int x = 0; x < C::kP; ++x)
+                            tma_load_3d(smem_u32(sq) + t * C::kTileBytes + x * kPanel, &w.q, x * 64, head * G, s.row0 + row0 + t * R, &b.q_full);
+                }
+                __syncwarp();
+                // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
+                auto entry = [&](int j) {
+                    const int x = j * (kKeyBlock / kKv8Page) + page;
+                    return j < nb && kv8_page_there(x, seen) ? max(-1, __ldg(table + x)) : -2;
+                };
+                auto checked = [&](int ph) {
+                    if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
+                    if (panel == 0) kv8_report(a.err);
+                    return -1;
+                };
+                const int beyond = a.c.n_pool_pages * Hkv * kKv8Page;  // the row behind the pools: reads as zeros
+                int ph = checked(entry(0)), ph_next = entry(1), started = 0;
+                bool part_started = false, go = true;
+                for (int j = 0; j < nb && go; ++j) {
+                    const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + head) * kKv8Page : beyond;
+                    const uint32_t use = (uint32_t)(j / kStages), ok = __ballot_sync(kFullMask, ph != -1) & 0xffu;
+                    if (use > 0 && !(go = wait_warp(&b.k_empty[st], use - 1))) break;
+                    // Record j - kRecs: the scores of block j - kStages, done, were issued behind the weights of a block after it.
+                    if (lane == 0) {
+                        b.rec[j % kRecs] = ok;
+                        mbar_arrive(&b.rec_full[j % kRecs]);
+                        mbar_expect_tx(&b.k_full[st], C::kTileBytes);
+                    }
+                    __syncwarp();
+                    if (panel < C::kP) tma_load_rows(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st]);
+                    started = 2 * j + 1;
+                    const int next = checked(ph_next);
+                    ph_next = entry(j + 2);
+                    if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
+                    // a page of which the last slots hold nothing: they become 0 before V is used
+                    const int left = seen - j * kKeyBlock;
+                    const bool cut_page = left < kKeyBlock && left % kKv8Page != 0;
+                    uint64_t *bar = cut_page ? &b.v_part : &b.v_full[st];
+                    if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
+                    __syncwarp();
+                    if (panel < C::kP) tma_load_rows(smem_u32(sv) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.v, panel * 64, y, bar);
+                    if (cut_page) {  // the last block
+                        part_started = true;
+                        if (!(go = wait_warp(bar, 0))) break;
+                        const int end = (left / kKv8Page + 1) * kKv8Page, chunks = (end - left) * 8;
+                        for (int e = lane; e < chunks * C::kP; e += 32)
+                            *reinterpret_cast<uint4 *>(sv + st * C::kTileBytes + e / chunks * kPanel + left * 128 + e % chunks * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&b.v_full[st]);
+                    }
+                    started = 2 * j + 2;
+                    ph = next;
+                }
+                if (*abort) {  // copies in flight land before the shared memory goes away
+                    tc_wait(&b.q_full, 0, nullptr);
+                    const int ks = (started + 1) / 2, vs = started / 2;
+                    for (int j = max(0, ks - kStages); j < ks; ++j) tc_wait(&b.k_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
+                    for (int j = max(0, vs - kStages); j < vs; ++j) tc_wait(&b.v_full[j % kStages], (uint32_t)(j / kStages) & 1u, nullptr);
+                    if (part_started) tc_wait(&b.v_part, 0, nullptr);
+                }
+            }
+            __syncwarp();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (*abort) break;
     }
+    if (warp == kMmaWarp) tmem_free(b.tmem, 512);
 }
 
 template <typename P, int D>
@@ -517,12 +579,6 @@ cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
     auto kernel = k_wide<P, D>;
     constexpr int kBytes = Cfg<D>::kTiles + (int)sizeof(Bars);
     static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
-    // the warps' split of the registers waits for ever if the launch has fewer
-    static const int regs = [&]() {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (3 * regs < 2 * kRegsSoftmax + kRegsRest) return cudaErrorInvalidConfiguration;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kThreads, kBytes, s>>>(w);
@@ -531,13 +587,12 @@ cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
 
 }  // namespace
 
-cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int32_t *plan, float *space) {
+cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int4 *plan, float *space) {
     WideArgs w{};
     w.a = a;
-    w.plan = (int4 *)plan;
+    w.plan = plan;
     w.wide = space;
     w.spans = a.p.n_groups + (own ? a.c.n_seqs : 0);
-    w.ctas = n_sm;
     const int G = a.Hq / a.c.n_kv_heads, D = a.c.head_dim;
     const int64_t units = (a.p.n_groups ? kv16_units(a.n_rows, G, a.p.n_groups) : 0) + (own ? kv16_units(a.n_rows, G, a.c.n_seqs) : 0);
     w.capacity = units * a.c.n_kv_heads + n_sm;
@@ -545,7 +600,7 @@ cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bo
     if (!kv16_page_map(&w.k, a.c.k_pool, a.c) || !kv16_page_map(&w.v, a.c.v_pool, a.c) ||
         !kv16_row_map(&w.q, a.q, a.q_stride, a.n_rows, a.Hq, G, kv16_tile_rows(G), D))
         return cudaErrorInvalidValue;
-    const unsigned blocks = (unsigned)w.capacity;
+    const unsigned blocks = (unsigned)n_sm;
     if (a.c.dtype == LLM_DTYPE_F16) return D == 128 ? wide<__half, 128>(s, w, blocks) : wide<__half, 64>(s, w, blocks);
     return D == 128 ? wide<__nv_bfloat16, 128>(s, w, blocks) : wide<__nv_bfloat16, 64>(s, w, blocks);
 }

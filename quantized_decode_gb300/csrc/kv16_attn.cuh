@@ -37,18 +37,48 @@ QD_DEV Kv16Span kv16_span(const Kv16AttnArgs &a, int i, int32_t *err) {
     return Kv16Span{s.row0, s.rows, s.kv, i - a.p.n_groups};
 }
 
+// The plan, an int4 for the call and one for each span, tells the wide kernel's CTAs and those who join its results what they need of one
+// another.  Segments are the (head, unit) pairs of a span, units fastest.  Few segments are cut into even parts, one for each
+// CTA: call {0}, span {first place, units, parts, 0}, and part k of segment (h, u) has place first + (h parts + k) units + u.
+// Many lie end to end on a line that the CTAs share evenly, each as long as its blocks and kPieceCost for what a piece costs besides: call {ctas, 0, low and high half of the line's length},
+// span {first segment, units, low and high half of where it begins}; a CTA leaves one result for each segment that it touches, at the
+// place of its number plus the segment's.  Units 0: the span has no results.
+constexpr int kPieceCost = 4;
+struct Kv16Plan {
+    const int4 *at;  // of the call; that of span i is at[1 + i]
+    const float *wide;
+};
+QD_DEV int64_t kv16_long(int lo, int hi) { return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo); }
+// On the line a sequence's units alternate between its last and its first, which see most and least of its tokens.
+QD_DEV int kv16_unit_at(int i, int units) { return i & 1 ? units - 1 - (i >> 1) : i >> 1; }
+QD_DEV int kv16_at_unit(int u, int units) { return 2 * u < units ? 2 * u : 2 * (units - 1 - u) + 1; }
+
 // Where a (row, head) pair's partial results of a span lie: `n` of them, `step` floats apart.
 struct Kv16Parts {
     const float *o, *top;  // of dims 0 .. 3 (those of d4 lie d4 * kTileLanes * 4 further on), and log2 of the sum
     int64_t step;
     int n;
 };
-QD_DEV Kv16Parts kv16_parts(const int4 &plan, const float *wide, int d, int G, int head, int in, int row_in_span) {
+QD_DEV Kv16Parts kv16_parts(const Kv16Plan &plan, int i, bool prefix, int blocks, int d, int G, int head, int in, int row_in_span) {
+    const int4 call = __ldcg(plan.at), s = __ldcg(plan.at + 1 + i);
     const int R = kv16_tile_rows(G), u = row_in_span / (2 * R), r = row_in_span - u * 2 * R, tile = r / R, lane = (r - tile * R) * G + in;
-    const int64_t step = kv16_place(d);
-    const float *p = wide + (plan.x + (int64_t)head * plan.z * plan.y + u) * step;
-    return Kv16Parts{p + ((int64_t)tile * (d / 4) * kTileLanes + lane) * 4, p + 2 * (int64_t)kTileLanes * d + tile * kTileLanes + lane,
-                     step * plan.y, plan.z};
+    const int64_t size = kv16_place(d);
+    int64_t place, step;
+    int n;
+    if (call.x == 0) {
+        place = s.x + (int64_t)head * s.z * s.y + u;
+        step = s.y;
+        n = s.y > 0 ? s.z : 0;
+    } else {
+        const int64_t length = kv16_long(call.z, call.w), seg = (int64_t)head * s.y + (prefix ? u : kv16_at_unit(u, s.y));
+        const int64_t first = kv16_long(s.z, s.w) + seg * (blocks + kPieceCost) + kPieceCost;
+        const int64_t c0 = ((first + 1) * call.x - 1) / length, c1 = ((first + blocks) * call.x - 1) / length;
+        place = c0 + s.x + seg;
+        step = 1;
+        n = s.y > 0 ? (int)(c1 - c0) + 1 : 0;
+    }
+    const float *p = plan.wide + place * size;
+    return Kv16Parts{p + ((int64_t)tile * (d / 4) * kTileLanes + lane) * 4, p + 2 * (int64_t)kTileLanes * d + tile * kTileLanes + lane, step * size, n};
 }
 
 // The group of a sequence: its number, or -1; by the whole warp.
@@ -106,6 +136,6 @@ struct Kv16Join {
 };
 
 bool kv16_few_rows(const llm_kv16_cache &c, int Hq, int n_rows);
-cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int32_t *plan, float *wide);
+cudaError_t launch_kv16_wide(cudaStream_t s, int n_sm, const Kv16AttnArgs &a, bool own, int4 *plan, float *wide);
 
 }  // namespace qd
