@@ -3,6 +3,7 @@
 //   k_evict_select  which slots of a sequence and head stay
 //   k_evict_move    their K and V moved together
 #include "kv16.cuh"
+#include "kv8_tc.cuh"
 
 namespace qd {
 
@@ -347,61 +348,79 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
     }
 }
 
-// The moves.  A slot's new place is never above its old one, so a warp that goes through the slots in order may write
-// a piece once it has read it, and everything behind is still as it was.  Warps share a sequence and head by 32-byte
-// columns (a memory sector), which have nothing to do with one another: 2 D / 32 of them for K and as many for V.
-// Two lanes hold a token's column; 16 tokens are a piece, and kAhead pieces are read before the first is written.
-constexpr int kMoveWarps = 4, kAhead = 4;
-template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32) k_evict_move(const __grid_constant__ Kv16EvictArgs a) {
-    constexpr int kColumns = 2 * D / 32;
-    const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads;
-    const int64_t id = (int64_t)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-    const int64_t seg = id / (2 * kColumns);
-    const int in = (int)(id - seg * (2 * kColumns)), b = (int)(seg / Hkv), head = (int)(seg - (int64_t)b * Hkv);
-    if (b >= a.c.n_seqs) return;
+// The moves.  A slot's new place is never above its old one, and slots keep their order, so what is read before a
+// write begins may be overwritten, and what comes behind is still as it was.  A cluster of kMoveCtas CTAs takes a sequence, head, K or V
+// and a slice of the columns; a round reads the next tokens, up to 64 KB in the shared memory of each CTA, waits until all
+// have read, and writes.  Tokens travel by bulk copies, one thread each: a row of D numbers (or a slice) from where it
+// lay to where it goes.  Slices, that a call of few heads finds all SMs.
+// ---------------------------------------------------------------------------
+constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveBytes = 65536;
+
+__global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_constant__ Kv16EvictArgs a, int slices) {
+    using namespace ptx;
+    extern __shared__ __align__(128) uint8_t buf[];
+    __shared__ uint64_t bar;
+    const int Hkv = a.c.n_kv_heads, D2 = 2 * a.c.head_dim, size = D2 / slices, per = kMoveBytes / size;
+    const int t = threadIdx.x, rank = (int)cluster_rank();
+    int id = (int)(blockIdx.x / kMoveCtas);
+    const int slice = id % slices, is_v = id / slices & 1, seg = id / (2 * slices), b = seg / Hkv, head = seg - b * Hkv;
     const int n = __ldg(a.kv_len + b);
-    if (n <= a.budget || (int64_t)n > (int64_t)a.c.table_stride * kKv8Page || n > a.score_stride) return;
-    const int32_t *kept = a.kept + seg * a.budget, *table = a.c.page_table + (int64_t)b * a.c.table_stride;
-    uint8_t *pool = (uint8_t *)(in < kColumns ? a.c.k_pool : a.c.v_pool) + in % kColumns * 32 + (lane & 1) * 16;
-    // the first slot that moves: kept[j] - j never falls
-    int from = 0, left = a.budget;
-    while (left > 0) {
-        const int step = (left + 31) / 32, i = from + lane * step;
-        const int hit = __popc(__ballot_sync(kFullMask, i < from + left && __ldg(kept + i) == i));
-        if (hit == 0) break;
-        // slots up to from + (hit - 1) * step stay
-        const int at = (hit - 1) * step + 1;
-        from += at;
-        left = min(left - at, step - 1);
+    if (n <= a.budget || (int64_t)n > (int64_t)a.c.table_stride * kKv8Page || n > a.score_stride) return;  // the whole cluster
+    const int32_t *kept = a.kept + (int64_t)seg * a.budget, *table = a.c.page_table + (int64_t)b * a.c.table_stride;
+    uint8_t *pool = (uint8_t *)(is_v ? a.c.v_pool : a.c.k_pool) + slice * size;
+    if (t == 0) {
+        mbar_init(&bar, kMoveThreads);
+        mbar_fence_init();
     }
-    auto cell = [&](int slot) -> uint4 * {  // null: its page is out of range
+    __syncthreads();
+    auto cell = [&](int slot) -> uint8_t * {  // null: its page is out of range
         const int page = __ldg(table + slot / kKv8Page);
         if (page < 0 || page >= a.c.n_pool_pages) {
             kv8_report(a.err);
             return nullptr;
         }
-        return reinterpret_cast<uint4 *>(pool + (((int64_t)page * Hkv + head) * kKv8Page + slot % kKv8Page) * (2 * D));
+        return pool + (((int64_t)page * Hkv + head) * kKv8Page + slot % kKv8Page) * D2;
     };
-    for (int j0 = from; j0 < a.budget; j0 += 16 * kAhead) {
-        uint4 *src[kAhead], *dst[kAhead], v[kAhead];
+    constexpr int kMost = 1024 / kMoveThreads;  // tokens of a thread at most: slices of 64 bytes at least
+    uint32_t phase = 0;
+    for (int j0 = 0; j0 < a.budget; j0 += kMoveCtas * per, phase ^= 1) {
+        const int mine = min(per, (a.budget - j0 - 1) / kMoveCtas + 1), from = j0 + rank * mine;
+        uint8_t *to[kMost];
+        uint32_t bytes = 0;
+        const uint8_t *src[kMost];
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x) {
-            const int j = j0 + 16 * x + (lane >> 1);
-            src[x] = dst[x] = nullptr;
-            if (j < a.budget) {
-                src[x] = cell(__ldg(kept + j));
-                dst[x] = cell(j);
-            }
+        for (int x = 0; x < kMost; ++x) {
+            const int i = x * kMoveThreads + t, j = from + i;
+            src[x] = to[x] = nullptr;
+            if (i >= mine || j >= a.budget) continue;
+            const int slot = __ldg(kept + j);
+            if (slot == j) continue;  // stays where it is
+            src[x] = cell(slot);
+            to[x] = cell(j);
+            if (!src[x] || !to[x]) src[x] = to[x] = nullptr;
+            else bytes += size;
         }
+        if (bytes) mbar_expect_tx(&bar, bytes);
+        else mbar_arrive(&bar);
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x)
-            if (src[x]) v[x] = __ldcg(src[x]);
-        __syncwarp();
+        for (int x = 0; x < kMost; ++x)
+            if (src[x]) bulk_load(smem_u32(buf) + (x * kMoveThreads + t) * size, src[x], size, &bar);
+        // Longer than any copy takes: without its token's place nothing could be written.
+        bool here = mbar_wait(&bar, phase, 1000000000ull);
+        if (!here) {  // a copy in flight lands before the shared memory goes away
+            if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
+            mbar_wait(&bar, phase, 1000000000ull);
+        }
+        here = __syncthreads_and(here);
+        cluster_sync();  // everything that this round overwrites has been read
+        if (!here) break;
 #pragma unroll
-        for (int x = 0; x < kAhead; ++x)
-            if (src[x] && dst[x]) __stcg(dst[x], v[x]);
-        __syncwarp();
+        for (int x = 0; x < kMost; ++x)
+            if (to[x])
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to[x]), "r"(smem_u32(buf) + (x * kMoveThreads + t) * size), "r"(size)
+                             : "memory");
+        bulk_commit_wait_read();  // the buffer is free for the next round
+        __syncthreads();
     }
 }
 
@@ -419,11 +438,23 @@ cudaError_t launch_kv16_evict(cudaStream_t s, const Kv16EvictArgs &a) {
     k_evict_select<<<(unsigned)segs, kSelThreads, kSelKeys * 4, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t warps = (int64_t)segs * 2 * (2 * a.c.head_dim / 32);
-    const unsigned blocks = (unsigned)((warps + kMoveWarps - 1) / kMoveWarps);
-    if (a.c.head_dim == 128) k_evict_move<128><<<blocks, kMoveWarps * 32, 0, s>>>(a);
-    else k_evict_move<64><<<blocks, kMoveWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    e = cudaFuncSetAttribute(k_evict_move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes);
+    if (e != cudaSuccess) return e;
+    int slices = 1;
+    while (segs * 2 * slices * 2 * kMoveCtas <= 2 * 152 && 2 * a.c.head_dim / (2 * slices) >= 64) slices *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(segs * 2 * slices * kMoveCtas));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMoveCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_evict_move, a, slices);
 }
 
 }  // namespace qd

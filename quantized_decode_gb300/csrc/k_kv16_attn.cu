@@ -26,7 +26,7 @@ namespace qd {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
-constexpr int kLeast = 2 * kWarps;  // pages of a part at least
+constexpr int kLeast = 4 * kWarps;  // pages of a part at least
 // Partial results joined at once: up to kMaxJoin in one step, else in groups.
 constexpr int kGroupJoin = 8, kMaxJoin = 24;
 constexpr float kLag = 4.f;

@@ -51,16 +51,19 @@ struct Cut {
     int64_t length;  // of the line: blocks, and kPieceCost for each segment
     bool fits;       // as many places as there are; else row_start falls somewhere
 };
-QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
+QD_DEV Kv16Span span_of(const WideArgs &w, const Kv16Span *held, int i) { return w.spans <= 32 ? held[i] : kv16_span(w.a, i, nullptr); }
+QD_DEV Cut cut_spans(const WideArgs &w, Kv16Span *held, int G, int Hkv, int32_t *err) {
     const int lane = threadIdx.x & 31, ctas = (int)gridDim.x;
     int64_t total = 0, segs = 0;
-    int longest = 1;
+    int longest = 1, my_segs = 0, my_blocks = 1;  // of lane's span, read once in calls of few
     for (int i = lane; i < w.spans; i += 32) {
         const Kv16Span s = kv16_span(w.a, i, err);
-        const int64_t u = (int64_t)s.units(G) * Hkv;
-        segs += u;
-        total += u * s.blocks();
-        if (u) longest = max(longest, s.blocks());
+        if (w.spans <= 32) held[i] = s;
+        my_blocks = s.blocks();
+        my_segs = s.units(G) * Hkv;
+        segs += my_segs;
+        total += (int64_t)my_segs * my_blocks;
+        if (my_segs) longest = max(longest, my_blocks);
     }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
@@ -68,24 +71,29 @@ QD_DEV Cut cut_spans(const WideArgs &w, int G, int Hkv, int32_t *err) {
         total += __shfl_xor_sync(kFullMask, total, m);
     }
     longest = __reduce_max_sync(kFullMask, longest);
+    __syncwarp();
     Cut r = {0, total + segs * kPieceCost, segs + ctas <= w.capacity};
     if (2 * segs > ctas || segs == 0) return r;
     auto items_at = [&](int share) {
         int n = 0;
-        for (int i = lane; i < w.spans; i += 32) {
-            const Kv16Span s = kv16_span(w.a, i, nullptr);
-            n += s.units(G) * Hkv * ((s.blocks() + share - 1) / share);
+        if (w.spans <= 32) {
+            n = my_segs * (int)((unsigned)(my_blocks + share - 1) / (unsigned)share);
+        } else {
+            for (int i = lane; i < w.spans; i += 32) {
+                const Kv16Span s = kv16_span(w.a, i, nullptr);
+                n += s.units(G) * Hkv * (int)((unsigned)(s.blocks() + share - 1) / (unsigned)share);
+            }
         }
         return (int)__reduce_add_sync(kFullMask, (unsigned)n);
     };
-    auto over = [&](int64_t n) { return (int)min((total + n - 1) / n, (int64_t)longest); };
+    // total / n, a little more rather than less (floats carry 24 bits)
+    auto over = [&](int n) { return (int)fminf(__fdividef((float)total, (float)n) * 1.00001f + 1.f, (float)longest); };
     // the smallest share that leaves no more parts than CTAs: at total / (ctas - segs) they fit, since the sum of ceil(p / s) is at most
     // total / s + segs
-    int bad = max(kLeastBlocks - 1, over(ctas) - 1), good = max(kLeastBlocks, over(ctas - segs));
-    if (bad + 1 < good && items_at(bad + 1) <= ctas) good = bad + 1;
+    int bad = max(kLeastBlocks - 1, over(ctas) - 2), good = max(kLeastBlocks, over(ctas - (int)segs));
 #pragma unroll 1
-    for (int i = 0; i < 6 && good - bad > 1; ++i) {
-        const int mid = bad + (good - bad) / 2;
+    for (int i = 0; i < 8 && good - bad > 1; ++i) {
+        const int mid = i < 2 ? bad + 1 : bad + (good - bad) / 2;  // it is mostly the first or second
         if (items_at(mid) <= ctas) good = mid;
         else bad = mid;
     }
@@ -101,13 +109,13 @@ struct Piece {
 };
 // The CTA's piece that begins at `at` (the number of a part, or a place on the line, up to `end`), and at becomes where the next begins.  By
 // the whole warp.  plan: written by the first CTA's first warp as it goes through the spans, which it then does to the last.
-QD_DEV bool next_piece(const WideArgs &w, const Cut &cut, int G, int Hkv, int64_t &at, int64_t end, int4 *plan, Piece &p) {
+QD_DEV bool next_piece(const WideArgs &w, const Kv16Span *held, const Cut &cut, int G, int Hkv, int64_t &at, int64_t end, int4 *plan, Piece &p) {
     const int lane = threadIdx.x & 31;
     int64_t base = 0, segs = 0;
     bool found = false;
     for (int i0 = 0; i0 < w.spans; i0 += 32) {
         Kv16Span mine = {0, 0, 0, -1};
-        if (i0 + lane < w.spans) mine = kv16_span(w.a, i0 + lane, nullptr);
+        if (i0 + lane < w.spans) mine = span_of(w, held, i0 + lane);
         const int u = cut.fits ? mine.units(G) : 0, n = cut.share ? (mine.blocks() + cut.share - 1) / cut.share : mine.blocks() + kPieceCost;
         const int64_t my_segs = (int64_t)u * Hkv, items = my_segs * n;
         int64_t upto = items, upto_segs = my_segs;
@@ -137,11 +145,12 @@ QD_DEV bool next_piece(const WideArgs &w, const Cut &cut, int G, int Hkv, int64_
             const int nb = p.s.blocks();
             if (cut.share) {
                 // units fastest: those that read the same pages run side by side
-                const int hp = (int)(in / p.units), part = hp % count;
-                p.unit = (int)(in - (int64_t)hp * p.units);
-                p.head = hp / count;
-                p.blk0 = (int)((int64_t)nb * part / count);
-                p.blk1 = (int)((int64_t)nb * (part + 1) / count);
+                const unsigned hp = (unsigned)in / (unsigned)p.units, head = hp / (unsigned)count, part = hp - head * (unsigned)count;
+                p.unit = (int)((unsigned)in - hp * (unsigned)p.units);
+                p.head = (int)head;
+                // 2^24 blocks times 2^8 parts at most
+                p.blk0 = (int)((unsigned)nb * part / (unsigned)count);
+                p.blk1 = (int)((unsigned)nb * (part + 1) / (unsigned)count);
                 p.place = at;
                 at = end;
             } else {
@@ -168,13 +177,14 @@ struct Bars {
         rec_full[kRecs];
     uint32_t rec[kRecs];  // pages of a block that are there
     uint32_t tmem;
-    float top[kTileLanes];
+    float top[2][kTileLanes];
     int abort;
     // the CTA's place in the work, kept here and not in registers: the softmax needs them all
     Cut cut;
     Piece piece;
     int64_t at, end;
     int found;
+    Kv16Span held[32];
 };
 
 // A row's softmax of a block, by each lane of a warp: 128 scores at s_at in TMEM, weights in their place, m and l
@@ -246,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, R = kv16_tile_rows(G);
     pdl_launch();
-    if (warp == 0) {
+    if (warp == kCopyWarp) {
+        if (lane < 3) tma_prefetch_desc(lane == 0 ? &w.q : (lane == 1 ? &w.k : &w.v));
         const bool first = blockIdx.x == 0;
-        const Cut cut = cut_spans(w, G, Hkv, first ? a.err : nullptr);
+        const Cut cut = cut_spans(w, b.held, G, Hkv, first ? a.err : nullptr);
         if (lane == 0) {
             b.cut = cut;
             b.at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
@@ -260,41 +271,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
         }
         __syncwarp();
     }
+    if (warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
     bool working = false;
-    for (;;) {
-        if (warp == 0) {
+    for (;; working = true) {
+        if (warp == kCopyWarp) {
             Piece next;
             int64_t at = b.at;
-            bool found = next_piece(w, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
-            while (found && next.blk0 == next.blk1) found = next_piece(w, b.cut, G, Hkv, at, b.end, nullptr, next);
+            bool found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
+            while (found && next.blk0 == next.blk1) found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, nullptr, next);
             if (lane == 0) {
                 b.at = at;
                 b.found = found;
                 if (found) b.piece = next;
-                if (working)
-                    for (uint64_t *x = &b.q_full; x <= &b.rec_full[kRecs - 1]; ++x) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(x)) : "memory");
-                mbar_init(&b.q_full, 1);
-                for (int i = 0; i < kStages; ++i) {
-                    mbar_init(&b.k_full[i], 1);
-                    mbar_init(&b.k_empty[i], 1);
-                    mbar_init(&b.v_full[i], 1);
-                    mbar_init(&b.v_empty[i], 1);
-                }
-                for (int i = 0; i < 2; ++i) {
-                    mbar_init(&b.s_full[i], 1);
-                    mbar_init(&b.p_full[i], 4);
-                    mbar_init(&b.o_full[i], 1);
-                }
-                for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
-                mbar_init(&b.v_part, 1);
-                mbar_init(&b.done, 1);
-                b.abort = 0;
-                mbar_fence_init();
             }
             __syncwarp();
         }
-        if (!working && warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
-        working = true;
+        if (warp == kMmaWarp && lane == 0) {
+            if (working)
+                for (uint64_t *x = &b.q_full; x <= &b.rec_full[kRecs - 1]; ++x) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(x)) : "memory");
+            mbar_init(&b.q_full, 1);
+            for (int i = 0; i < kStages; ++i) {
+                mbar_init(&b.k_full[i], 1);
+                mbar_init(&b.k_empty[i], 1);
+                mbar_init(&b.v_full[i], 1);
+                mbar_init(&b.v_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&b.s_full[i], 1);
+                mbar_init(&b.p_full[i], 4);
+                mbar_init(&b.o_full[i], 1);
+            }
+            for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
+            mbar_init(&b.v_part, 1);
+            mbar_init(&b.done, 1);
+            b.abort = 0;
+            mbar_fence_init();
+        }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
@@ -364,65 +376,64 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
             float *mine = w.wide + p.place * kv16_place(D);
             float4 *other = reinterpret_cast<float4 *>(sq);  // [d / 4][lane]
             const bool direct = !prefix && whole && a.p.n_groups == 0;
+            // Tiles that hold the same rows: each tile's threads hand over one half of the dims and put the other half together.
+            const int d0 = !pair && t == 1 ? D / 2 : 0, d1 = !pair && t == 0 ? D / 2 : D;
+            float k1 = 0.f;
             if (!pair) {
-                if (t == 1) {
-    #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
-                        float v[32];
-                        tmem_ld32(o_at(1) + lanes + d, v);
-    #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            other[(d + e) / 4 * kTileLanes + lane_of] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
-                    }
-                    b.top[lane_of] = top;
-                }
-                softmax_sync();
-            }
-            if (pair || t == 0) {
-                float k1 = 0.f;
-                if (!pair) {
-                    // the other half's result: weights of the two, which add up to 1
-                    const float top1 = b.top[lane_of], most = fmaxf(top, top1), ref = most == -INFINITY ? 0.f : most;
-                    const float w0 = none ? 0.f : ex2(top - ref), w1 = top1 == -INFINITY ? 0.f : ex2(top1 - ref), sum = w0 + w1;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    k *= w0 * inv;
-                    k1 = w1 * inv;
-                    top = sum == 0.f ? -INFINITY : ref + log2f(sum);
-                }
-                const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
-                float *to = mine + (int64_t)t * D * kTileLanes;
-    #pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
+#pragma unroll 1
+                for (int d = D / 2 - d0; d < D - d0; d += 32) {
                     float v[32];
                     tmem_ld32(o_at(t) + lanes + d, v);
-    #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
-                    if (!pair && k1 != 0.f) {
-    #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 x = other[(d + e) / 4 * kTileLanes + lane_of];
-                            v[e] = fmaf(x.x, k1, v[e]);
-                            v[e + 1] = fmaf(x.y, k1, v[e + 1]);
-                            v[e + 2] = fmaf(x.z, k1, v[e + 2]);
-                            v[e + 3] = fmaf(x.w, k1, v[e + 3]);
-                        }
-                    }
-                    __syncwarp();
-                    if (live && direct) {
-    #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>((P *)a.out + at * D + d + e) =
-                                make_uint4(Bits16<P>::pack(v[e], v[e + 1]), Bits16<P>::pack(v[e + 2], v[e + 3]), Bits16<P>::pack(v[e + 4], v[e + 5]),
-                                           Bits16<P>::pack(v[e + 6], v[e + 7]));
-                    } else if (live) {
-    #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<float4 *>(to + ((int64_t)(d + e) / 4 * kTileLanes + lane_of) * 4), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
-                    }
-                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        other[(d + e) / 4 * kTileLanes + lane_of] = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
                 }
-                if (live && !direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + t * kTileLanes + lane_of, top);
-                else if (live && a.lse) a.lse[at] = top * 0.69314718f;
+                b.top[t][lane_of] = top;
+                softmax_sync();
+                // the other tile's result: weights of the two, which add up to 1
+                const float top1 = b.top[t ^ 1][lane_of], most = fmaxf(top, top1), ref = most == -INFINITY ? 0.f : most;
+                const float w0 = none ? 0.f : ex2(top - ref), w1 = top1 == -INFINITY ? 0.f : ex2(top1 - ref), sum = t == 0 ? w0 + w1 : w1 + w0;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                k *= w0 * inv;
+                k1 = w1 * inv;
+                top = sum == 0.f ? -INFINITY : ref + log2f(sum);
+            }
+            const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
+            const int tile = pair ? t : 0;
+            float *to = mine + (int64_t)tile * D * kTileLanes;
+#pragma unroll 1
+            for (int d = d0; d < d1; d += 32) {
+                float v[32];
+                tmem_ld32(o_at(t) + lanes + d, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = none ? 0.f : v[e] * k;
+                if (k1 != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 x = other[(d + e) / 4 * kTileLanes + lane_of];
+                        v[e] = fmaf(x.x, k1, v[e]);
+                        v[e + 1] = fmaf(x.y, k1, v[e + 1]);
+                        v[e + 2] = fmaf(x.z, k1, v[e + 2]);
+                        v[e + 3] = fmaf(x.w, k1, v[e + 3]);
+                    }
+                }
+                __syncwarp();
+                if (live && direct) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>((P *)a.out + at * D + d + e) =
+                            make_uint4(Bits16<P>::pack(v[e], v[e + 1]), Bits16<P>::pack(v[e + 2], v[e + 3]), Bits16<P>::pack(v[e + 4], v[e + 5]),
+                                       Bits16<P>::pack(v[e + 6], v[e + 7]));
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        __stcg(reinterpret_cast<float4 *>(to + ((int64_t)(d + e) / 4 * kTileLanes + lane_of) * 4), make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                }
+                __syncwarp();
+            }
+            if (live && (pair || t == 0)) {
+                if (!direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + tile * kTileLanes + lane_of, top);
+                else if (a.lse) a.lse[at] = top * 0.69314718f;
             }
         } else {
             if (warp == kMmaWarp && nb > 0) {
@@ -432,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
                 auto scores = [&](int t, int st) {
                     const uint32_t d = s_at(t), qd = q_at + (pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
                         if (kk == 0) mma_ss<false>(d, qd, kd, id_s);
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                     const uint32_t d = o_at(t), x = s_at(t), vd = v_at + st * (C::kTileBytes >> 4);
                     if (more) mma_ts<true>(d, x, vd, id_o);
                     else mma_ts<false>(d, x, vd, id_o);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 1; kk < kKeyBlock / 16; ++kk) mma_ts<true>(d, x + kk * 8, vd + kk * (2048 >> 4), id_o);
                 };
                 const bool mine = elect_lane();
@@ -499,6 +510,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 const int page = lane & 7, panel = lane >> 3;
                 const int32_t *table = (prefix ? a.p.page_table + (int64_t)p.span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
                                        (int64_t)blk0 * (kKeyBlock / kKv8Page);
+                // lane l knows page l of four blocks, and of the next four: -2 where there is none, -1 for one that is out of range
+                auto entry = [&](int j) {
+                    const int x = j * (kKeyBlock / kKv8Page) + lane;
+                    return x < nb * (kKeyBlock / kKv8Page) && kv8_page_there(x, seen) ? max(-1, __ldg(table + x)) : -2;
+                };
+                auto checked = [&](int ph) {
+                    if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
+                    kv8_report(a.err);
+                    return -1;
+                };
+                const int beyond = a.c.n_pool_pages * Hkv * kKv8Page;  // the row behind the pools: reads as zeros
+                int four = entry(0), next_four = entry(4), started = 0;
+                four = checked(four);
+                bool part_started = false, go = true;
                 if (lane == 0) {
                     mbar_expect_tx(&b.q_full, (pair ? 2 : 1) * C::kP * R * G * 128);
                     for (int t = 0; t < (pair ? 2 : 1); ++t)
@@ -506,20 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                             tma_load_3d(smem_u32(sq) + t * C::kTileBytes + x * kPanel, &w.q, x * 64, head * G, s.row0 + row0 + t * R, &b.q_full);
                 }
                 __syncwarp();
-                // lane p % 8 knows page p of a block: -2 where there is none, -1 for one that is out of range
-                auto entry = [&](int j) {
-                    const int x = j * (kKeyBlock / kKv8Page) + page;
-                    return j < nb && kv8_page_there(x, seen) ? max(-1, __ldg(table + x)) : -2;
-                };
-                auto checked = [&](int ph) {
-                    if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
-                    if (panel == 0) kv8_report(a.err);
-                    return -1;
-                };
-                const int beyond = a.c.n_pool_pages * Hkv * kKv8Page;  // the row behind the pools: reads as zeros
-                int ph = checked(entry(0)), ph_next = entry(1), started = 0;
-                bool part_started = false, go = true;
                 for (int j = 0; j < nb && go; ++j) {
+                    if (j > 0 && j % 4 == 0) {
+                        four = checked(next_four);
+                        next_four = entry(j + 4);
+                    }
+                    const int ph = __shfl_sync(kFullMask, four, j % 4 * 8 + page);
                     const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + head) * kKv8Page : beyond;
                     const uint32_t use = (uint32_t)(j / kStages), ok = __ballot_sync(kFullMask, ph != -1) & 0xffu;
                     if (use > 0 && !(go = wait_warp(&b.k_empty[st], use - 1))) break;
@@ -532,8 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                     __syncwarp();
                     if (panel < C::kP) tma_load_rows(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st]);
                     started = 2 * j + 1;
-                    const int next = checked(ph_next);
-                    ph_next = entry(j + 2);
                     if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
                     // a page of which the last slots hold nothing: they become 0 before V is used
                     const int left = seen - j * kKeyBlock;
@@ -553,7 +568,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                         if (lane == 0) mbar_arrive(&b.v_full[st]);
                     }
                     started = 2 * j + 2;
-                    ph = next;
                 }
                 if (*abort) {  // copies in flight land before the shared memory goes away
                     tc_wait(&b.q_full, 0, nullptr);

@@ -61,7 +61,9 @@ template <int WARPS, typename LineOf>
 QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32_t *err) {
     __shared__ int scratch[WARPS], s_run[WARPS][2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per_thread = (B + 32 * WARPS - 1) / (32 * WARPS), b0 = threadIdx.x * per_thread, b1 = min(b0 + per_thread, B);
+    // up to 32 sequences: one for each lane, and every warp counts for itself
+    const bool small = B <= 32;
+    const int per_thread = small ? 1 : (B + 32 * WARPS - 1) / (32 * WARPS), b0 = (small ? lane : (int)threadIdx.x) * per_thread, b1 = min(b0 + per_thread, B);
     Kv16Line one = {0, 1, true};  // of b0, read once in calls of few sequences
     int segs = 0, longest = 1;
     float total = 0.f;
@@ -73,13 +75,16 @@ QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32
         total += (float)s.segs * (float)s.pages;
         if (s.segs) longest = max(longest, s.pages);
     }
-    total = block_sum(total, scratch, WARPS);
-    segs = block_sum(segs, scratch, WARPS);
+    auto sum_of = [&](int x) { return small ? (int)__reduce_add_sync(kFullMask, (unsigned)x) : block_sum(x, scratch, WARPS); };
+    total = small ? warp_sum(total) : block_sum(total, scratch, WARPS);
+    segs = sum_of(segs);
     longest = (int)__reduce_max_sync(kFullMask, (unsigned)longest);
-    __syncthreads();
-    if (lane == 0) scratch[warp] = longest;
-    __syncthreads();
-    for (int w = 0; w < WARPS; ++w) longest = max(longest, scratch[w]);
+    if (!small) {
+        __syncthreads();
+        if (lane == 0) scratch[warp] = longest;
+        __syncthreads();
+        for (int w = 0; w < WARPS; ++w) longest = max(longest, scratch[w]);
+    }
     // total / n, a little more rather than less (floats carry 24 bits)
     auto over = [&](int n) { return (int)fminf(__fdividef(total, (float)n) * 1.00001f + 1.f, (float)longest); };
     auto items_at = [&](int share) {
@@ -88,7 +93,7 @@ QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32
             const Kv16Line s = line_of(b);
             n += s.segs * kv16_parts_of(s.pages, share);
         }
-        return block_sum(n, scratch, WARPS);
+        return sum_of(n);
     };
     int share = min(max(least, over(ctas)), longest);
     if (2 * segs <= ctas && items_at(share) > ctas) {
@@ -109,6 +114,7 @@ QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32
         const int n = kv16_parts_of(s.pages, share);
         mine += s.segs * n;
         mine_cut += n > 1 ? s.segs * n : 0;
+        if (small) continue;
         upto[b] = mine;
         upto[B + b] = mine_cut;
     }
@@ -120,6 +126,14 @@ QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32
             run += v;
             run_cut += w;
         }
+    }
+    if (small) {
+        if (warp == 0 && lane < B) {
+            upto[lane] = run;
+            upto[B + lane] = run_cut;
+        }
+        __syncthreads();
+        return share;
     }
     if (lane == 31) {
         s_run[warp][0] = run;
