@@ -21,7 +21,9 @@ namespace qd {
 
 namespace {
 
-constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 10 * 32;  // 200 registers a thread
+constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 12 * 32;
+constexpr int kRegsSoftmax = 208, kRegsRest = 88;  // 168 at launch
+static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "no more than the launch has");
 constexpr int kStages = 2, kRecs = 4;
 constexpr int kLeastBlocks = 2;  // of a part: one for each tile
 constexpr float kLag = 8.f;
@@ -244,6 +246,26 @@ QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, ui
 
 QD_DEV void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// A piece as the warps work on it.
+struct View {
+    int head, row0, rows, blk0, nb, seen;  // rows row0 .. of the span; nb blocks that any of them sees, seen tokens from the first block's on
+    bool pair, prefix, whole;              // pair: two tiles of rows, else one for every other block
+    QD_DEV View(const Piece &p, int R) {
+        head = p.head;
+        row0 = p.unit * 2 * R;
+        rows = min(2 * R, p.s.rows - row0);
+        pair = rows > R;
+        prefix = p.s.seq < 0;
+        whole = p.blk0 == 0 && p.blk1 == p.s.blocks();
+        const int all = prefix ? p.s.len : max(0, p.s.len - p.s.rows + row0 + rows);
+        blk0 = p.blk0;
+        nb = max(0, min(p.blk1, kv8_blocks(all, kKeyBlock)) - blk0);
+        seen = all - blk0 * kKeyBlock;
+    }
+    QD_DEV int blocks(int t) const { return pair ? nb : (nb - t + 1) / 2; }  // of tile t
+    QD_DEV int block(int t, int i) const { return pair ? i : 2 * i + t; }
+};
+
 template <typename P, int D>
 __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ WideArgs w) {
     using namespace ptx;
@@ -255,105 +277,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
     const Kv16AttnArgs &a = w.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, R = kv16_tile_rows(G);
-    pdl_launch();
-    if (warp == kCopyWarp) {
-        if (lane < 3) tma_prefetch_desc(lane == 0 ? &w.q : (lane == 1 ? &w.k : &w.v));
-        const bool first = blockIdx.x == 0;
-        const Cut cut = cut_spans(w, b.held, G, Hkv, first ? a.err : nullptr);
-        if (lane == 0) {
-            b.cut = cut;
-            b.at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
-            b.end = cut.share ? (int64_t)blockIdx.x + 1 : cut.length * (blockIdx.x + 1) / gridDim.x;
-            if (first) {
-                w.plan[0] = cut.share ? make_int4(0, 0, 0, 0) : make_int4((int)gridDim.x, 0, (int)max(cut.length, (int64_t)1), (int)(cut.length >> 32));
-                if (!cut.fits) kv8_report(a.err);
-            }
+    auto s_at = [&](int t) { return b.tmem + (uint32_t)(t * 128); };
+    auto o_at = [&](int t) { return b.tmem + (uint32_t)((2 + t) * 128); };
+    auto fail = [&]() {
+        *abort = 1;
+        if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
+    };
+    auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
+        if (!tc_wait(bar, phase & 1u, abort)) {
+            fail();
+            return false;
         }
-        __syncwarp();
-    }
-    if (warp == kMmaWarp) tmem_alloc(&b.tmem, 512);
-    bool working = false;
-    for (;; working = true) {
-        if (warp == kCopyWarp) {
-            Piece next;
-            int64_t at = b.at;
-            bool found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
-            while (found && next.blk0 == next.blk1) found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, nullptr, next);
-            if (lane == 0) {
-                b.at = at;
-                b.found = found;
-                if (found) b.piece = next;
-            }
-            __syncwarp();
-        }
-        if (warp == kMmaWarp && lane == 0) {
-            if (working)
-                for (uint64_t *x = &b.q_full; x <= &b.rec_full[kRecs - 1]; ++x) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(x)) : "memory");
-            mbar_init(&b.q_full, 1);
-            for (int i = 0; i < kStages; ++i) {
-                mbar_init(&b.k_full[i], 1);
-                mbar_init(&b.k_empty[i], 1);
-                mbar_init(&b.v_full[i], 1);
-                mbar_init(&b.v_empty[i], 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&b.s_full[i], 1);
-                mbar_init(&b.p_full[i], 4);
-                mbar_init(&b.o_full[i], 1);
-            }
-            for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
-            mbar_init(&b.v_part, 1);
-            mbar_init(&b.done, 1);
-            b.abort = 0;
-            mbar_fence_init();
-        }
+        return true;
+    };
+    auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
+    // Each kind of warp has a loop of its own over the pieces, with the CTA's barrier before and behind the work on each.
+    auto begin = [&]() {
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (!b.found) break;
-        const Piece &p = b.piece;
-        const Kv16Span &s = p.s;
-        const int head = p.head, row0 = p.unit * 2 * R, rows = min(2 * R, s.rows - row0);  // of the span
-        const bool pair = rows > R;  // two tiles of rows, else one for every other block
-        const bool prefix = s.seq < 0, whole = p.blk0 == 0 && p.blk1 == s.blocks();
-        // tokens that any row of the unit sees, and this piece's blocks of them; tokens are counted from the first one's on
-        const int all = prefix ? s.len : max(0, s.len - s.rows + row0 + rows), blk0 = p.blk0;
-        const int nb = max(0, min(p.blk1, kv8_blocks(all, kKeyBlock)) - blk0), seen = all - blk0 * kKeyBlock;
-        auto tile_blocks = [&](int t) { return pair ? nb : (nb - t + 1) / 2; };
-        auto block_of = [&](int t, int i) { return pair ? i : 2 * i + t; };
-
-        const uint32_t tmem = b.tmem;
-        auto s_at = [&](int t) { return tmem + (uint32_t)(t * 128); };
-        auto o_at = [&](int t) { return tmem + (uint32_t)((2 + t) * 128); };
-        auto fail = [&]() {
-            *abort = 1;
-            if (a.err) atomicCAS(a.err, 0, LLM_ERR_TIMEOUT);
-        };
-        auto wait = [&](uint64_t *bar, uint32_t phase) {  // false once anything timed out
-            if (!tc_wait(bar, phase & 1u, abort)) {
-                fail();
-                return false;
-            }
-            return true;
-        };
-        auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
-        if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
-
-        if (warp < kSoftmax) {
-            // ================= softmax =================
+        return b.found != 0;
+    };
+    auto end = [&]() {
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        return !*abort;
+    };
+    pdl_launch();
+    if (warp < kSoftmax) {
+        // ================= softmax =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        while (begin()) {
+            const View p(b.piece, R);
+            const Kv16Span &s = b.piece.s;
             const int t = warp >> 2, lane_of = (warp & 3) * 32 + lane;
-            const int i = lane_of / G, row = (pair ? t * R : 0) + i;  // of the unit
-            const bool live = i < R && row < rows;
+            const int i = lane_of / G, row = (p.pair ? t * R : 0) + i;  // of the unit
+            const bool live = i < R && row < p.rows;
             // tokens of this part that the row sees; rows that are not there hide nothing
-            const int limit = prefix ? seen : (live ? max(0, s.len - s.rows + row0 + row + 1) - blk0 * kKeyBlock : INT32_MAX);
+            const int limit = p.prefix ? p.seen : (live ? max(0, s.len - s.rows + p.row0 + row + 1) - p.blk0 * kKeyBlock : INT32_MAX);
             const int shortest = __reduce_min_sync(kFullMask, limit);
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
-            const int n = tile_blocks(t);
+            const int n = p.blocks(t);
             float m = -INFINITY, l = 0.f;
             bool fine = true;
             for (int k = 0; k < n && fine; ++k) {
-                const int j = block_of(t, k);
+                const int j = p.block(t, k);
                 fine = wait_warp(&b.rec_full[j % kRecs], (uint32_t)(j / kRecs)) && wait_warp(&b.s_full[t], (uint32_t)k);
                 if (!fine) break;
                 tc_fence_after();
@@ -368,18 +339,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
             }
             // both tiles' products have to be done where one's result takes the place of q; `done` comes after a wait that ran out too
             const bool some = n > 0;
-            if (nb > 0) fine = wait_warp(pair ? &b.o_full[t] : &b.done, 0) && fine && !*abort;
+            if (p.nb > 0) fine = wait_warp(p.pair ? &b.o_full[t] : &b.done, 0) && fine && !*abort;
             tc_fence_after();
             float k = some ? kv8_row_factor(fine, l) : 0.f;
             float top = some ? kv8_row_log2(fine, l, m - Bits16<P>::kLift) : -INFINITY;
             const bool none = top == -INFINITY;
-            float *mine = w.wide + p.place * kv16_place(D);
+            float *mine = w.wide + b.piece.place * kv16_place(D);
             float4 *other = reinterpret_cast<float4 *>(sq);  // [d / 4][lane]
-            const bool direct = !prefix && whole && a.p.n_groups == 0;
+            const bool direct = !p.prefix && p.whole && a.p.n_groups == 0;
             // Tiles that hold the same rows: each tile's threads hand over one half of the dims and put the other half together.
-            const int d0 = !pair && t == 1 ? D / 2 : 0, d1 = !pair && t == 0 ? D / 2 : D;
+            const int d0 = !p.pair && t == 1 ? D / 2 : 0, d1 = !p.pair && t == 0 ? D / 2 : D;
             float k1 = 0.f;
-            if (!pair) {
+            if (!p.pair) {
 #pragma unroll 1
                 for (int d = D / 2 - d0; d < D - d0; d += 32) {
                     float v[32];
@@ -398,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 k1 = w1 * inv;
                 top = sum == 0.f ? -INFINITY : ref + log2f(sum);
             }
-            const int64_t at = (int64_t)(s.row0 + row0 + row) * a.Hq + head * G + (lane_of - i * G);
-            const int tile = pair ? t : 0;
+            const int64_t at = (int64_t)(s.row0 + p.row0 + row) * a.Hq + p.head * G + (lane_of - i * G);
+            const int tile = p.pair ? t : 0;
             float *to = mine + (int64_t)tile * D * kTileLanes;
 #pragma unroll 1
             for (int d = d0; d < d1; d += 32) {
@@ -431,18 +402,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 }
                 __syncwarp();
             }
-            if (live && (pair || t == 0)) {
+            if (live && (p.pair || t == 0)) {
                 if (!direct) __stcg(mine + 2 * (int64_t)kTileLanes * D + tile * kTileLanes + lane_of, top);
                 else if (a.lse) a.lse[at] = top * 0.69314718f;
             }
-        } else {
-            if (warp == kMmaWarp && nb > 0) {
-                // ================= MMA =================
+            if (!end()) break;
+        }
+        return;
+    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kMmaWarp) {
+        // ================= MMA =================
+        tmem_alloc(&b.tmem, 512);
+        for (bool working = false;; working = true) {
+            if (lane == 0) {
+                if (working)
+                    for (uint64_t *x = &b.q_full; x <= &b.rec_full[kRecs - 1]; ++x) asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(x)) : "memory");
+                mbar_init(&b.q_full, 1);
+                for (int i = 0; i < kStages; ++i) {
+                    mbar_init(&b.k_full[i], 1);
+                    mbar_init(&b.k_empty[i], 1);
+                    mbar_init(&b.v_full[i], 1);
+                    mbar_init(&b.v_empty[i], 1);
+                }
+                for (int i = 0; i < 2; ++i) {
+                    mbar_init(&b.s_full[i], 1);
+                    mbar_init(&b.p_full[i], 4);
+                    mbar_init(&b.o_full[i], 1);
+                }
+                for (int i = 0; i < kRecs; ++i) mbar_init(&b.rec_full[i], 1);
+                mbar_init(&b.v_part, 1);
+                mbar_init(&b.done, 1);
+                b.abort = 0;
+                mbar_fence_init();
+                if (smem_u32(smem) & 1023) fail();  // the swizzle goes by the address
+            }
+            __syncwarp();
+            if (!begin()) break;
+            const View p(b.piece, R);
+            if (p.nb > 0) {
                 const uint32_t type = Bits16<P>::kFormat << 7 | Bits16<P>::kFormat << 10;
                 const uint32_t id_s = umma_idesc_f16_f32(kTileLanes, kKeyBlock) | type, id_o = umma_idesc_f16_f32(kTileLanes, D) | kIdescBMn | type;
                 const uint32_t q_at = desc_k(smem_u32(sq)), k_at = desc_k(smem_u32(sk)), v_at = desc_mn(smem_u32(sv));
                 auto scores = [&](int t, int st) {
-                    const uint32_t d = s_at(t), qd = q_at + (pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
+                    const uint32_t d = s_at(t), qd = q_at + (p.pair ? t * (C::kTileBytes >> 4) : 0), kd = k_at + st * (C::kTileBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t at = (uint32_t)((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
@@ -460,24 +463,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 const bool mine = elect_lane();
                 bool go = wait_warp(&b.q_full, 0);
                 for (int t = 0; t < 2 && go; ++t) {
-                    if (tile_blocks(t) == 0) break;
-                    const int j = block_of(t, 0);
+                    if (p.blocks(t) == 0) break;
+                    const int j = p.block(t, 0);
                     go = wait_warp(&b.k_full[j % kStages], 0);
                     if (!go) break;
                     tc_fence_after();
                     if (mine) {
                         scores(t, j % kStages);
                         umma_commit(&b.s_full[t]);
-                        if (!pair || t == 1) umma_commit(&b.k_empty[j % kStages]);
+                        if (!p.pair || t == 1) umma_commit(&b.k_empty[j % kStages]);
                     }
                     __syncwarp();
                 }
-                for (int k = 0; k < tile_blocks(0) && go; ++k)
+                for (int k = 0; k < p.blocks(0) && go; ++k)
                     for (int t = 0; t < 2 && go; ++t) {
-                        const int n = tile_blocks(t);
+                        const int n = p.blocks(t);
                         if (k >= n) break;
-                        const int j = block_of(t, k), jn = block_of(t, k + 1), st = j % kStages, sn = jn % kStages;
-                        const bool last = !pair || t == 1;  // of the tiles that use the block
+                        const int j = p.block(t, k), jn = p.block(t, k + 1), st = j % kStages, sn = jn % kStages;
+                        const bool last = !p.pair || t == 1;  // of the tiles that use the block
                         go = wait_warp(&b.v_full[st], (uint32_t)(j / kStages)) && wait_warp(&b.p_full[t], (uint32_t)k);
                         if (!go) break;
                         tc_fence_after();
@@ -504,16 +507,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 __syncwarp();
                 if (!tc_wait(&b.done, 0, nullptr)) fail();
             }
-            if (warp == kCopyWarp && nb > 0) {
-                // ================= copies =================
+            __syncwarp();
+            if (!end()) break;
+        }
+        tmem_free(b.tmem, 512);
+    } else if (warp == kCopyWarp) {
+        // ================= the plan, and copies =================
+        if (lane < 3) tma_prefetch_desc(lane == 0 ? &w.q : (lane == 1 ? &w.k : &w.v));
+        const bool first = blockIdx.x == 0;
+        const Cut cut = cut_spans(w, b.held, G, Hkv, first ? a.err : nullptr);
+        if (lane == 0) {
+            b.cut = cut;
+            b.at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
+            b.end = cut.share ? (int64_t)blockIdx.x + 1 : cut.length * (blockIdx.x + 1) / gridDim.x;
+            if (first) {
+                w.plan[0] = cut.share ? make_int4(0, 0, 0, 0) : make_int4((int)gridDim.x, 0, (int)max(cut.length, (int64_t)1), (int)(cut.length >> 32));
+                if (!cut.fits) kv8_report(a.err);
+            }
+        }
+        __syncwarp();
+        for (bool working = false;; working = true) {
+            Piece next;
+            int64_t at = b.at;
+            bool found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
+            while (found && next.blk0 == next.blk1) found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, nullptr, next);
+            if (lane == 0) {
+                b.at = at;
+                b.found = found;
+                if (found) b.piece = next;
+            }
+            __syncwarp();
+            if (!begin()) break;
+            const View p(b.piece, R);
+            const Kv16Span &s = b.piece.s;
+            if (p.nb > 0) {
                 constexpr uint32_t kPageBytes = kKv8Page * 128;  // of a panel
                 const int page = lane & 7, panel = lane >> 3;
-                const int32_t *table = (prefix ? a.p.page_table + (int64_t)p.span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
-                                       (int64_t)blk0 * (kKeyBlock / kKv8Page);
+                const int32_t *table = (p.prefix ? a.p.page_table + (int64_t)b.piece.span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
+                                       (int64_t)p.blk0 * (kKeyBlock / kKv8Page);
                 // lane l knows page l of four blocks, and of the next four: -2 where there is none, -1 for one that is out of range
                 auto entry = [&](int j) {
                     const int x = j * (kKeyBlock / kKv8Page) + lane;
-                    return x < nb * (kKeyBlock / kKv8Page) && kv8_page_there(x, seen) ? max(-1, __ldg(table + x)) : -2;
+                    return x < p.nb * (kKeyBlock / kKv8Page) && kv8_page_there(x, p.seen) ? max(-1, __ldg(table + x)) : -2;
                 };
                 auto checked = [&](int ph) {
                     if (ph == -2 || (ph >= 0 && ph < a.c.n_pool_pages)) return ph;
@@ -525,19 +560,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 four = checked(four);
                 bool part_started = false, go = true;
                 if (lane == 0) {
-                    mbar_expect_tx(&b.q_full, (pair ? 2 : 1) * C::kP * R * G * 128);
-                    for (int t = 0; t < (pair ? 2 : 1); ++t)
+                    mbar_expect_tx(&b.q_full, (p.pair ? 2 : 1) * C::kP * R * G * 128);
+                    for (int t = 0; t < (p.pair ? 2 : 1); ++t)
                         for (int x = 0; x < C::kP; ++x)
-                            tma_load_3d(smem_u32(sq) + t * C::kTileBytes + x * kPanel, &w.q, x * 64, head * G, s.row0 + row0 + t * R, &b.q_full);
+                            tma_load_3d(smem_u32(sq) + t * C::kTileBytes + x * kPanel, &w.q, x * 64, p.head * G, s.row0 + p.row0 + t * R, &b.q_full);
                 }
                 __syncwarp();
-                for (int j = 0; j < nb && go; ++j) {
+                for (int j = 0; j < p.nb && go; ++j) {
                     if (j > 0 && j % 4 == 0) {
                         four = checked(next_four);
                         next_four = entry(j + 4);
                     }
                     const int ph = __shfl_sync(kFullMask, four, j % 4 * 8 + page);
-                    const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + head) * kKv8Page : beyond;
+                    const int st = j % kStages, y = ph >= 0 ? (ph * Hkv + p.head) * kKv8Page : beyond;
                     const uint32_t use = (uint32_t)(j / kStages), ok = __ballot_sync(kFullMask, ph != -1) & 0xffu;
                     if (use > 0 && !(go = wait_warp(&b.k_empty[st], use - 1))) break;
                     // Record j - kRecs: the scores of block j - kStages, done, were issued behind the weights of a block after it.
@@ -551,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                     started = 2 * j + 1;
                     if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
                     // a page of which the last slots hold nothing: they become 0 before V is used
-                    const int left = seen - j * kKeyBlock;
+                    const int left = p.seen - j * kKeyBlock;
                     const bool cut_page = left < kKeyBlock && left % kKv8Page != 0;
                     uint64_t *bar = cut_page ? &b.v_part : &b.v_full[st];
                     if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
@@ -578,14 +613,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 }
             }
             __syncwarp();
+            if (!end()) break;
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (*abort) break;
+    } else {
+        while (begin() && end()) {
+        }
     }
-    if (warp == kMmaWarp) tmem_free(b.tmem, 512);
 }
 
 template <typename P, int D>
@@ -593,6 +626,12 @@ cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
     auto kernel = k_wide<P, D>;
     constexpr int kBytes = Cfg<D>::kTiles + (int)sizeof(Bars);
     static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
+    // the warps' split of the registers would wait for ever if a launch had fewer
+    static const int regs = [&]() {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (3 * regs < 2 * kRegsSoftmax + kRegsRest) return cudaErrorInvalidConfiguration;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kThreads, kBytes, s>>>(w);
