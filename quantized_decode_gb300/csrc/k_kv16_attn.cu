@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     constexpr int kRow = D + 4;  // floats of a row in the merge buffer
     __shared__ __align__(16) float merge_o[kWarps][kRows][kRow];
     __shared__ float s_top[kWarps][kRows];
-    __shared__ int s_last;
+    __shared__ int s_last, s_front[3];  // s_front: the group, blocks of its prefix, the sequence's first row among its rows
     extern __shared__ int upto[];  // items that end with sequence b: [n_seqs], and of those the cut ones
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs, ctas = (int)gridDim.x;
@@ -127,6 +127,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
         int ph = __shfl_sync(kFullMask, phys, 0);
         load_k(ph);
         load_v(ph);
+        if (warp == 0) {  // the sequence's group, while the first page comes
+            int group = kv16_group_of(a, b);
+            Kv16Group gr = {0, 0, 0, false};
+            if (group >= 0) gr = kv16_group(a, group);
+            if (!gr.ok || gr.len == 0 || s.row0 < gr.row0 || s.row0 + s.rows > gr.row0 + gr.rows) group = -1;
+            if (lane == 0) {
+                s_front[0] = group;
+                s_front[1] = (gr.len - 1) / kKeyBlock + 1;
+                s_front[2] = s.row0 - gr.row0;
+            }
+        }
 
         const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[OT][4];
@@ -248,22 +259,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
                         make_float4(o[4 * i + y][z] * k, o[4 * i + y][2 + z] * k, o[4 * i + y + 1][z] * k, o[4 * i + y + 1][2 + z] * k);
         }
         __syncthreads();
-        // the group's plan, for the results of its prefix
-        int front = -1, front_row = 0, front_blocks = 0;
-        auto look_ahead = [&]() {  // by the whole warp, before results are written
-            const int group = kv16_group_of(a, b);
-            if (group < 0) return;
-            const Kv16Group gr = kv16_group(a, group);
-            if (!gr.ok || gr.len == 0 || s.row0 < gr.row0 || s.row0 + s.rows > gr.row0 + gr.rows) return;
-            if (!waited) pdl_wait();
+        auto look_ahead = [&]() {  // before results of the prefix are read
+            if (s_front[0] < 0 || waited) return;
+            pdl_wait();
             waited = true;
-            front = group;
-            front_row = s.row0 - gr.row0;
-            front_blocks = (gr.len - 1) / kKeyBlock + 1;
         };
         auto write_out = [&](Kv16Join &join, int row, int d4) {
             const int rr = tile * kRows + row, i = rr / G, hq = rr % G;
-            if (front >= 0) join.add_parts(kv16_parts(plan, front, true, front_blocks, D, G, head, hq, front_row + i), d4);
+            if (s_front[0] >= 0) join.add_parts(kv16_parts(plan, s_front[0], true, s_front[1], D, G, head, hq, s_front[2] + i), d4);
             const int64_t at = (int64_t)(s.row0 + i) * a.Hq + head * G + hq;
             store_out4((P *)a.out + at * D + 4 * d4, join.value());
             if (d4 == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
@@ -277,8 +280,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
             if (d4 == 0) __stcg(to + kRows * D + row, join.log_sum());
         };
         if (parts == 1) look_ahead();
-        for (int e = threadIdx.x; e < n_live * (D / 4); e += kThreads) {
-            const int row = e / (D / 4), d4 = e % (D / 4);
+        // rows fastest, as they lie next to one another in the prefix's results
+        for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
+            const int row = e % kRows, d4 = e / kRows;
+            if (row >= n_live) continue;
             Kv16Join join;
             const float t[kWarps] = {s_top[0][row], s_top[1][row], s_top[2][row], s_top[3][row]};
             float4 v[kWarps];
@@ -308,17 +313,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
             auto join_all = [&](const float *from, int k0, int step, int count, bool final) {
                 if (final) look_ahead();
                 const int64_t stride = (int64_t)step * tiles * kPartFloats<D>;
-                for (int e = threadIdx.x; e < n_live * (D / 4); e += kThreads) {
-                    const int row = e / (D / 4), d4 = e % (D / 4);
+                for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
+                    const int row = e % kRows, d4 = e / kRows;
+                    if (row >= n_live) continue;
                     Kv16Join join;
                     for (int i0 = 0; i0 < count; i0 += 8) {
                         float t[8];
                         float4 v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float *p = from + (i0 + i) * stride;
-                            t[i] = i0 + i < count ? __ldcg(p + kRows * D + row) : -INFINITY;
-                            v[i] = i0 + i < count ? __ldcg(reinterpret_cast<const float4 *>(p + row * D + 4 * d4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float *p = from + min(i0 + i, count - 1) * stride;
+                            t[i] = ld_part(p + kRows * D + row);
+                            v[i] = ld_part4(p + row * D + 4 * d4);
+                            if (i0 + i >= count) t[i] = -INFINITY;
                         }
                         join.add(t, v);
                     }
@@ -336,30 +343,72 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     if (!waited) pdl_wait();  // so that this kernel's end is that of both
 }
 
-// ---- the rows of wide calls: their partial results joined, one warp for each row and head
+// ---- the rows of wide calls: their partial results joined.  A thread takes a quarter of the dims of a (row, query head) pair,
+// a warp 32 pairs of a K/V head that mostly lie next to one another in the results.
 template <typename P, int D>
 __global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan) {
-    const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads, G = a.Hq / Hkv;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), row = id / a.Hq;
+    constexpr int kFours = D / 16;  // float4s of a thread
+    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, quarter = threadIdx.x >> 5;
     pdl_wait();
+    const int64_t pair = (int64_t)(blockIdx.x / Hkv) * 32 + (threadIdx.x & 31);
+    const int head = (int)(blockIdx.x % Hkv);
+    const int64_t row = pair / G;
     if (row >= a.n_rows) return;
-    const int h = (int)(id - row * a.Hq), b = kv16_seq_of_row(a.row_start, a.c.n_seqs, (int)row);
+    const int in = (int)(pair - row * G);
+    auto last_at = [](const int32_t *from, int n, int x) {  // the largest i with from[i] <= x, 0 if there is none
+        int lo = 0;
+        while (n > 1) {
+            const int half = n / 2;
+            if (__ldg(from + lo + half) <= x) {
+                lo += half;
+                n -= half;
+            } else {
+                n = half;
+            }
+        }
+        return lo;
+    };
+    const int b = last_at(a.row_start, a.c.n_seqs, (int)row);
     const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
     if (row < s.row0 || row >= s.row0 + s.rows) return;
-    const int group = kv16_group_of(a, b), d4 = lane % (D / 4);
     const int own_blocks = s.kv > 0 ? (s.kv - 1) / kKeyBlock + 1 : 1;
-    const Kv16Parts own = kv16_parts(plan, a.p.n_groups + b, false, own_blocks, D, G, h / G, h % G, (int)row - s.row0);
+    const Kv16Parts own = kv16_parts(plan, a.p.n_groups + b, false, own_blocks, D, G, head, in, (int)row - s.row0);
     if (a.p.n_groups == 0 && own.n == 1) return;  // written already
-    Kv16Join join;
-    if (group >= 0) {
+    float top = -INFINITY, sum = 0.f;
+    float4 v[kFours];
+#pragma unroll
+    for (int i = 0; i < kFours; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const Kv16Parts &p) {
+        for (int k = 0; k < p.n; ++k) {
+            float4 x[kFours];
+            const float t = ld_part(p.top + k * p.step);
+#pragma unroll
+            for (int i = 0; i < kFours; ++i) x[i] = ld_part4(p.o + k * p.step + (int64_t)(quarter * kFours + i) * kTileLanes * 4);
+            if (t == -INFINITY) continue;
+            const float to = fmaxf(top, t), k0 = top == to ? 1.f : ex2(top - to), w = ex2(t - to);
+            top = to;
+            sum = fmaf(sum, k0, w);
+#pragma unroll
+            for (int i = 0; i < kFours; ++i)
+                v[i] = make_float4(fmaf(x[i].x, w, v[i].x * k0), fmaf(x[i].y, w, v[i].y * k0), fmaf(x[i].z, w, v[i].z * k0), fmaf(x[i].w, w, v[i].w * k0));
+        }
+    };
+    if (a.p.n_groups > 0) {
+        const int group = last_at(a.p.seq_start, a.p.n_groups, b);
         const Kv16Group gr = kv16_group(a, group);
-        if (gr.ok && gr.len > 0 && row >= gr.row0 && row < gr.row0 + gr.rows)
-            join.add_parts(kv16_parts(plan, group, true, (gr.len - 1) / kKeyBlock + 1, D, G, h / G, h % G, (int)row - gr.row0), d4);
+        if (b >= __ldg(a.p.seq_start + group) && b < __ldg(a.p.seq_start + group + 1) && gr.ok && gr.len > 0 && row >= gr.row0 && row < gr.row0 + gr.rows)
+            add(kv16_parts(plan, group, true, (gr.len - 1) / kKeyBlock + 1, D, G, head, in, (int)row - gr.row0));
     }
-    join.add_parts(own, d4);
-    const int64_t at = row * a.Hq + h;
-    if (lane < D / 4) store_out4((P *)a.out + at * D + 4 * d4, join.value());
-    if (lane == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
+    add(own);
+    const int64_t at = row * a.Hq + head * G + in;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    P *out = (P *)a.out + at * D + quarter * kFours * 4;
+#pragma unroll
+    for (int i = 0; i < kFours; i += 2)
+        *reinterpret_cast<uint4 *>(out + 4 * i) =
+            make_uint4(Bits16<P>::pack(v[i].x * inv, v[i].y * inv), Bits16<P>::pack(v[i].z * inv, v[i].w * inv),
+                       Bits16<P>::pack(v[i + 1].x * inv, v[i + 1].y * inv), Bits16<P>::pack(v[i + 1].z * inv, v[i + 1].w * inv));
+    if (quarter == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
 }
 
 // A launch that may begin while the one before it ends; what it reads of that one waits for its end.
@@ -409,7 +458,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
         if (e != cudaSuccess) return e;
     }
     if (own) {
-        const int64_t blocks = ((int64_t)a.n_rows * a.Hq + 3) / 4;
+        const int64_t blocks = ((int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) + 31) / 32 * a.c.n_kv_heads;
         if (blocks > INT32_MAX) return cudaErrorInvalidValue;
         return launch_behind(true, k_join<P, D>, (unsigned)blocks, 128, 0, s, a, plan);
     }
