@@ -15,9 +15,9 @@
 // tokens up with byte permutations.  No shuffles, no shared memory; the next page is loaded as soon as a page's registers are free.
 //
 // The split.  A segment (sequence, head, 8 pairs) of p pages is cut into ceil(p / share) even parts, one work item
-// each; the warps of a CTA take its pages in turn.  A segment of one part is written at once; else its parts leave partial results
-// in the workspace, and the last to arrive (a counter) joins them in the order of the parts: the result does not
-// depend on who is last.
+// each; the warps of a CTA take its pages in turn.  CTAs take items one after another (a counter): with prefixes there is one on each SM
+// beside the wide kernel's, with which it shares the memory's time, and more when those end.  An item leaves a partial result
+// in the workspace, unless it is all that its rows have to see, and k_join puts them together, in a fixed order.
 #include "kv16_attn.cuh"
 #include "kv16_line.cuh"
 
@@ -27,16 +27,39 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
 constexpr int kLeast = 4 * kWarps;  // pages of a part at least
-// Partial results joined at once: up to kMaxJoin in one step, else in groups.
-constexpr int kGroupJoin = 8, kMaxJoin = 24;
+constexpr int kCutFor = 2 * kCtasPerSm;  // parts for each SM: two for each CTA, which draw them
 constexpr float kLag = 4.f;
 
+// The part of the workspace that has to do with sequences' own tokens in calls of few rows.
+struct Own {
+    int32_t *next, *none_left;  // the next item; set once there is none.  Both 0 between calls
+    int4 *plan;                 // two of each sequence: its first item, parts of its segments (0: it has no results), its first row, tiles;
+                                // its group (-1: none), blocks of the prefix, its first row among the group's
+    int32_t *seq_of;            // of each row, or -1
+    float *parts;               // results by item: [d / 4][row][4], [row] log2 of the sums
+    int64_t capacity;           // items that have a place
+    int cut_for;                // parts to cut the sequences into
+};
 template <int D>
-constexpr int kPartFloats = kRows * (D + 1);  // [row][D], [row] log2 of the sum
+constexpr int kPartFloats = kRows * (D + 1);
+
+// the largest i with from[i] <= x, 0 if there is none
+QD_DEV int last_at(const int32_t *from, int n, int x) {
+    int lo = 0;
+    while (n > 1) {
+        const int half = n / 2;
+        if (__ldg(from + lo + half) <= x) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    return lo;
+}
 
 template <typename P, int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_constant__ Kv16AttnArgs a, int32_t *counters, float *parts_at,
-                                                                 const Kv16Plan plan) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_constant__ Kv16AttnArgs a, const Own own) {
     using T = Bits16<P>;
     constexpr int KP = D / 32;   // 16-byte pieces of a token's K that a lane holds
     constexpr int VP = D / 64;   // of its V
@@ -44,26 +67,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     constexpr int kRow = D + 4;  // floats of a row in the merge buffer
     __shared__ __align__(16) float merge_o[kWarps][kRows][kRow];
     __shared__ float s_top[kWarps][kRows];
-    __shared__ int s_last, s_front[3];  // s_front: the group, blocks of its prefix, the sequence's first row among its rows
-    extern __shared__ int upto[];  // items that end with sequence b: [n_seqs], and of those the cut ones
+    __shared__ int s_item[2];
+    extern __shared__ int upto[];  // items that end with sequence b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs, ctas = (int)gridDim.x;
-
+    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs;
+    pdl_launch();
+    if (threadIdx.x == 0) s_item[0] = *(volatile int32_t *)own.none_left ? INT32_MAX : atomicAdd(own.next, 1);
+    __syncthreads();
+    if (s_item[0] == INT32_MAX) {  // begun when all was taken
+        pdl_wait();
+        return;
+    }
     const int share = kv16_cut<kWarps>(
-        B, ctas, kLeast,
+        B, own.cut_for, kLeast,
         [&](int b) {
             const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
             return Kv16Line{(s.rows * G + kRows - 1) / kRows * Hkv, kv8_pages(s.kv), s.ok};
         },
         upto, blockIdx.x == 0 ? a.err : nullptr);
-    const int items = upto[B - 1];
-    bool waited = false;
+    const bool fits = upto[B - 1] <= own.capacity;  // else row_start falls somewhere
+    const int items = fits ? upto[B - 1] : 0;
+    if (s_item[0] == 0) {  // the CTA that has the first item tells k_join about rows and sequences
+        for (int i = threadIdx.x; i < a.n_rows; i += kThreads) own.seq_of[i] = -1;
+        __syncthreads();
+        for (int b = threadIdx.x; b < B; b += kThreads) {
+            const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+            int group = -1;
+            Kv16Group gr = {0, 0, 0, false};
+            if (a.p.n_groups > 0) {
+                group = last_at(a.p.seq_start, a.p.n_groups, b);
+                gr = kv16_group(a, group);
+                if (b < __ldg(a.p.seq_start + group) || b >= __ldg(a.p.seq_start + group + 1) || !gr.ok || gr.len == 0 || s.row0 < gr.row0 ||
+                    s.row0 + s.rows > gr.row0 + gr.rows)
+                    group = -1;
+            }
+            own.plan[2 * b] = make_int4(b > 0 ? upto[b - 1] : 0, fits ? kv16_parts_of(kv8_pages(s.kv), share) : 0, s.row0, (s.rows * G + kRows - 1) / kRows);
+            own.plan[2 * b + 1] = make_int4(group, (gr.len - 1) / kKeyBlock + 1, s.row0 - gr.row0, 0);
+            for (int i = 0; i < s.rows; ++i) own.seq_of[s.row0 + i] = b;
+        }
+        if (!fits && threadIdx.x == 0) kv8_report(a.err);
+    }
 
-    for (int item = (int)blockIdx.x; item < items; item += ctas) {
-        // ---- the item's sequence: the first whose items end behind it
+    for (int turn = 0;; turn ^= 1) {
+        const int item = s_item[turn];
+        if (item >= items) break;
         const int b = kv16_find(upto, B, item);
         const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
-        const int in = item - (b > 0 ? upto[b - 1] : 0), place = b > 0 ? upto[B + b - 1] : 0;
+        const int in = item - (b > 0 ? upto[b - 1] : 0);
         // tiles fastest: those that read the same pages run side by side
         const int pages = kv8_pages(s.kv), tiles = (s.rows * G + kRows - 1) / kRows, parts = kv16_parts_of(pages, share);
         const int hp = (int)((unsigned)in / (unsigned)tiles), tile = in - hp * tiles;
@@ -127,17 +177,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
         int ph = __shfl_sync(kFullMask, phys, 0);
         load_k(ph);
         load_v(ph);
-        if (warp == 0) {  // the sequence's group, while the first page comes
-            int group = kv16_group_of(a, b);
-            Kv16Group gr = {0, 0, 0, false};
-            if (group >= 0) gr = kv16_group(a, group);
-            if (!gr.ok || gr.len == 0 || s.row0 < gr.row0 || s.row0 + s.rows > gr.row0 + gr.rows) group = -1;
-            if (lane == 0) {
-                s_front[0] = group;
-                s_front[1] = (gr.len - 1) / kKeyBlock + 1;
-                s_front[2] = s.row0 - gr.row0;
-            }
-        }
 
         const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[OT][4];
@@ -242,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
             if (more) load_v(ph);
         }
 
+        if (threadIdx.x == 0) s_item[turn ^ 1] = atomicAdd(own.next, 1);  // the next one
         // ---- the warps' results together, each divided by its own sum so that none leaves fp32's range
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
@@ -259,28 +299,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
                         make_float4(o[4 * i + y][z] * k, o[4 * i + y][2 + z] * k, o[4 * i + y + 1][z] * k, o[4 * i + y + 1][2 + z] * k);
         }
         __syncthreads();
-        auto look_ahead = [&]() {  // before results of the prefix are read
-            if (s_front[0] < 0 || waited) return;
-            pdl_wait();
-            waited = true;
-        };
-        auto write_out = [&](Kv16Join &join, int row, int d4) {
-            const int rr = tile * kRows + row, i = rr / G, hq = rr % G;
-            if (s_front[0] >= 0) join.add_parts(kv16_parts(plan, s_front[0], true, s_front[1], D, G, head, hq, s_front[2] + i), d4);
-            const int64_t at = (int64_t)(s.row0 + i) * a.Hq + head * G + hq;
-            store_out4((P *)a.out + at * D + 4 * d4, join.value());
-            if (d4 == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
-        };
-        // of this segment's part k: places of one tile's parts are `tiles` apart, as its items are
-        auto place_of = [&](int k) { return place + (head * parts + k) * tiles + tile; };
-        auto part_at = [&](int k) { return parts_at + (int64_t)place_of(k) * kPartFloats<D>; };
-        auto group_at = [&](int k) { return parts_at + (int64_t)(kKv16Counters / 2 + place_of(k)) * kPartFloats<D>; };  // from part k on
-        auto write_part = [&](float *to, const Kv16Join &join, int row, int d4) {
-            __stcg(reinterpret_cast<float4 *>(to + row * D + 4 * d4), join.value());
-            if (d4 == 0) __stcg(to + kRows * D + row, join.log_sum());
-        };
-        if (parts == 1) look_ahead();
-        // rows fastest, as they lie next to one another in the prefix's results
+        const bool whole = parts == 1 && a.p.n_groups == 0;
+        float *to = own.parts + (int64_t)item * kPartFloats<D>;
+        // rows fastest, as they lie in the results
         for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
             const int row = e % kRows, d4 = e / kRows;
             if (row >= n_live) continue;
@@ -290,125 +311,141 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v[w] = *reinterpret_cast<const float4 *>(&merge_o[w][row][4 * d4]);
             join.add(t, v);
-            if (parts == 1) write_out(join, row, d4);
-            else write_part(part_at(part), join, row, d4);
-        }
-        if (parts > 1) {
-            // groups of `per` parts are joined by their last to arrive, the groups by the last of those: two short
-            // chains instead of one long.  per <= kMaxJoin, and as many groups.
-            const int per = parts <= kMaxJoin ? parts : max(kGroupJoin, (parts + kMaxJoin - 1) / kMaxJoin);
-            const int group = part / per, groups = (parts + per - 1) / per, n = min(per, parts - group * per);
-            auto arrive = [&](int32_t *at, int of) {  // whether this CTA is the last of `of`
-                __threadfence();
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    s_last = atomicAdd(at, 1) == of - 1;
-                    if (s_last) *at = 0;
-                    __threadfence();
-                }
-                __syncthreads();
-                return s_last != 0;
-            };
-            // results k0, k0 + step, ... (n of them) to the output or to the group's place
-            auto join_all = [&](const float *from, int k0, int step, int count, bool final) {
-                if (final) look_ahead();
-                const int64_t stride = (int64_t)step * tiles * kPartFloats<D>;
-                for (int e = threadIdx.x; e < kRows * (D / 4); e += kThreads) {
-                    const int row = e % kRows, d4 = e / kRows;
-                    if (row >= n_live) continue;
-                    Kv16Join join;
-                    for (int i0 = 0; i0 < count; i0 += 8) {
-                        float t[8];
-                        float4 v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float *p = from + min(i0 + i, count - 1) * stride;
-                            t[i] = ld_part(p + kRows * D + row);
-                            v[i] = ld_part4(p + row * D + 4 * d4);
-                            if (i0 + i >= count) t[i] = -INFINITY;
-                        }
-                        join.add(t, v);
-                    }
-                    if (final) write_out(join, row, d4);
-                    else write_part(group_at(k0), join, row, d4);
-                }
-            };
-            if (arrive(counters + place_of(group * per), n)) {
-                join_all(part_at(group * per), group * per, 1, n, groups == 1);
-                if (groups > 1 && arrive(counters + kKv16Counters / 2 + place_of(0), groups)) join_all(group_at(0), 0, per, groups, true);
+            if (whole) {
+                const int rr = tile * kRows + row;
+                const int64_t at = (int64_t)(s.row0 + rr / G) * a.Hq + head * G + rr % G;
+                store_out4((P *)a.out + at * D + 4 * d4, join.value());
+                if (d4 == 0 && a.lse) a.lse[at] = join.log_sum() * 0.69314718f;
+            } else {
+                __stcg(reinterpret_cast<float4 *>(to + (d4 * kRows + row) * 4), join.value());
+                if (d4 == 0) __stcg(to + kRows * D + row, join.log_sum());
             }
         }
-        __syncthreads();  // the merge buffer is free again
+        __syncthreads();  // the merge buffer is free again, and the next item known
     }
-    if (!waited) pdl_wait();  // so that this kernel's end is that of both
+    if (threadIdx.x == 0) *(volatile int32_t *)own.none_left = 1;
+    pdl_wait();  // so that this kernel's end is that of the wide one too
 }
 
-// ---- the rows of wide calls: their partial results joined.  A thread takes a quarter of the dims of a (row, query head) pair,
-// a warp 32 pairs of a K/V head that mostly lie next to one another in the results.
-template <typename P, int D>
-__global__ void __launch_bounds__(128) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan) {
-    constexpr int kFours = D / 16;  // float4s of a thread
-    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, quarter = threadIdx.x >> 5;
-    pdl_wait();
-    const int64_t pair = (int64_t)(blockIdx.x / Hkv) * 32 + (threadIdx.x & 31);
-    const int head = (int)(blockIdx.x % Hkv);
-    const int64_t row = pair / G;
-    if (row >= a.n_rows) return;
-    const int in = (int)(pair - row * G);
-    auto last_at = [](const int32_t *from, int n, int x) {  // the largest i with from[i] <= x, 0 if there is none
-        int lo = 0;
-        while (n > 1) {
-            const int half = n / 2;
-            if (__ldg(from + lo + half) <= x) {
-                lo += half;
-                n -= half;
-            } else {
-                n = half;
+// ---- Partial results joined: 32 (row, query head) pairs of a K/V head to a CTA, that mostly lie next to one another in the results; each
+// warp takes some of the dims, and SLICES CTAs them all.  What the first warp has to look up about the pairs it finds out before the
+// kernels before end.  F: float4s of a thread, N: results read at a time.  (The code is kept short: a kernel's first pass through it waits
+// for its instructions.)
+template <typename P, int D, int F, int N, int SLICES>
+__global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan, const Own own) {
+    struct Found {
+        const float *o, *top;
+        int64_t step, size4;  // floats from part to part, and from d4 to d4
+        int n;
+    };
+    __shared__ Found found[2][32];  // of the prefix and of the sequence's own tokens
+    const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned block = blockIdx.x / SLICES;
+    const int part = (int)(blockIdx.x % SLICES) * (D / 4 / F / SLICES) + warp;  // of the dims
+    const int64_t pair = (int64_t)(block / (unsigned)Hkv) * 32 + lane, row = pair / G;
+    const int head = (int)(block % (unsigned)Hkv), in = (int)(pair - row * G);
+    if (warp == 0) {
+        Found f[2] = {{nullptr, nullptr, 0, 0, -1}, {nullptr, nullptr, 0, 0, 0}};  // -1: nothing to write
+        if (own.plan) {
+            pdl_wait();
+            const int b = row < a.n_rows ? __ldcg(own.seq_of + row) : -1;
+            if (b >= 0) {
+                const int4 x = __ldcg(own.plan + 2 * b), y = __ldcg(own.plan + 2 * b + 1);
+                const int i = (int)row - x.z, rr = i * G + in, tile = rr / kRows, r = rr - tile * kRows;
+                f[0].n = 0;
+                if (y.x >= 0) {
+                    const Kv16Parts p = kv16_parts(plan, y.x, true, y.y, D, G, head, in, y.z + i);
+                    f[0] = Found{p.o, p.top, p.step, kTileLanes * 4, p.n};
+                }
+                const float *p = own.parts + (x.x + (int64_t)head * x.y * x.w + tile) * kPartFloats<D>;
+                f[1] = Found{p + r * 4, p + kRows * D + r, (int64_t)x.w * kPartFloats<D>, kRows * 4, x.y};
+            }
+        } else if (row < a.n_rows) {
+            const int b = last_at(a.row_start, a.c.n_seqs, (int)row);
+            const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
+            int group = -1;
+            Kv16Group gr = {0, 0, 0, false};
+            if (a.p.n_groups > 0) {
+                group = last_at(a.p.seq_start, a.p.n_groups, b);
+                gr = kv16_group(a, group);
+                if (b < __ldg(a.p.seq_start + group) || b >= __ldg(a.p.seq_start + group + 1) || !gr.ok || gr.len == 0 || row < gr.row0 ||
+                    row >= gr.row0 + gr.rows)
+                    group = -1;
+            }
+            pdl_wait();
+            if (row >= s.row0 && row < s.row0 + s.rows) {
+                f[0].n = 0;
+                if (group >= 0) {
+                    const Kv16Parts p = kv16_parts(plan, group, true, (gr.len - 1) / kKeyBlock + 1, D, G, head, in, (int)row - gr.row0);
+                    f[0] = Found{p.o, p.top, p.step, kTileLanes * 4, p.n};
+                }
+                const Kv16Parts p = kv16_parts(plan, a.p.n_groups + b, false, s.kv > 0 ? (s.kv - 1) / kKeyBlock + 1 : 1, D, G, head, in, (int)row - s.row0);
+                f[1] = Found{p.o, p.top, p.step, kTileLanes * 4, p.n};
             }
         }
-        return lo;
-    };
-    const int b = last_at(a.row_start, a.c.n_seqs, (int)row);
-    const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
-    if (row < s.row0 || row >= s.row0 + s.rows) return;
-    const int own_blocks = s.kv > 0 ? (s.kv - 1) / kKeyBlock + 1 : 1;
-    const Kv16Parts own = kv16_parts(plan, a.p.n_groups + b, false, own_blocks, D, G, head, in, (int)row - s.row0);
-    if (a.p.n_groups == 0 && own.n == 1) return;  // written already
-    float top = -INFINITY, sum = 0.f;
-    float4 v[kFours];
-#pragma unroll
-    for (int i = 0; i < kFours; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const Kv16Parts &p) {
-        for (int k = 0; k < p.n; ++k) {
-            float4 x[kFours];
-            const float t = ld_part(p.top + k * p.step);
-#pragma unroll
-            for (int i = 0; i < kFours; ++i) x[i] = ld_part4(p.o + k * p.step + (int64_t)(quarter * kFours + i) * kTileLanes * 4);
-            if (t == -INFINITY) continue;
-            const float to = fmaxf(top, t), k0 = top == to ? 1.f : ex2(top - to), w = ex2(t - to);
-            top = to;
-            sum = fmaf(sum, k0, w);
-#pragma unroll
-            for (int i = 0; i < kFours; ++i)
-                v[i] = make_float4(fmaf(x[i].x, w, v[i].x * k0), fmaf(x[i].y, w, v[i].y * k0), fmaf(x[i].z, w, v[i].z * k0), fmaf(x[i].w, w, v[i].w * k0));
-        }
-    };
-    if (a.p.n_groups > 0) {
-        const int group = last_at(a.p.seq_start, a.p.n_groups, b);
-        const Kv16Group gr = kv16_group(a, group);
-        if (b >= __ldg(a.p.seq_start + group) && b < __ldg(a.p.seq_start + group + 1) && gr.ok && gr.len > 0 && row >= gr.row0 && row < gr.row0 + gr.rows)
-            add(kv16_parts(plan, group, true, (gr.len - 1) / kKeyBlock + 1, D, G, head, in, (int)row - gr.row0));
+        if (a.p.n_groups == 0 && f[1].n == 1) f[0].n = -1;  // written already
+        found[0][lane] = f[0];
+        found[1][lane] = f[1];
+        // ready for the next call
+        if (blockIdx.x == 0 && lane == 0 && own.plan) *own.next = *own.none_left = 0;
+    } else {
+        pdl_wait();
     }
-    add(own);
+    __syncthreads();
+    if (found[0][lane].n < 0) return;
+    float top = -INFINITY, sum = 0.f;
+    float4 v[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int z = 0; z < 2; ++z) {
+        const Found f = found[z][lane];
+#pragma unroll 1
+        for (int k0 = 0; k0 < f.n; k0 += N) {
+            float t[N];
+            float4 x[N][F];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int64_t at = min(k0 + k, f.n - 1) * f.step;
+                t[k] = ld_part(f.top + at);
+#pragma unroll
+                for (int i = 0; i < F; ++i) x[k][i] = ld_part4(f.o + at + (part * F + i) * f.size4);
+            }
+            float to = top;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (k0 + k >= f.n) t[k] = -INFINITY;
+                to = fmaxf(to, t[k]);
+            }
+            const float ref = to == -INFINITY ? 0.f : to, down = ex2(top - ref);
+            top = to;
+            sum *= down;
+#pragma unroll
+            for (int i = 0; i < F; ++i) v[i] = make_float4(v[i].x * down, v[i].y * down, v[i].z * down, v[i].w * down);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (t[k] == -INFINITY) continue;
+                const float w = ex2(t[k] - ref);
+                sum += w;
+#pragma unroll
+                for (int i = 0; i < F; ++i)
+                    v[i] = make_float4(fmaf(x[k][i].x, w, v[i].x), fmaf(x[k][i].y, w, v[i].y), fmaf(x[k][i].z, w, v[i].z), fmaf(x[k][i].w, w, v[i].w));
+            }
+        }
+    }
     const int64_t at = row * a.Hq + head * G + in;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    P *out = (P *)a.out + at * D + quarter * kFours * 4;
+    P *out = (P *)a.out + at * D + part * F * 4;
+    if (F == 1) {
+        store_out4(out, make_float4(v[0].x * inv, v[0].y * inv, v[0].z * inv, v[0].w * inv));
+    } else {
 #pragma unroll
-    for (int i = 0; i < kFours; i += 2)
-        *reinterpret_cast<uint4 *>(out + 4 * i) =
-            make_uint4(Bits16<P>::pack(v[i].x * inv, v[i].y * inv), Bits16<P>::pack(v[i].z * inv, v[i].w * inv),
-                       Bits16<P>::pack(v[i + 1].x * inv, v[i + 1].y * inv), Bits16<P>::pack(v[i + 1].z * inv, v[i + 1].w * inv));
-    if (quarter == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
+        for (int i = 0; i + 1 < F; i += 2)
+            *reinterpret_cast<uint4 *>(out + 4 * i) =
+                make_uint4(Bits16<P>::pack(v[i].x * inv, v[i].y * inv), Bits16<P>::pack(v[i].z * inv, v[i].w * inv),
+                           Bits16<P>::pack(v[i + 1].x * inv, v[i + 1].y * inv), Bits16<P>::pack(v[i + 1].z * inv, v[i + 1].w * inv));
+    }
+    if (part == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
 }
 
 // A launch that may begin while the one before it ends; what it reads of that one waits for its end.
@@ -427,22 +464,35 @@ cudaError_t launch_behind(bool behind, void (*kernel)(Args...), unsigned blocks,
     return cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
 }
 
-// Fields of the workspace behind the counters: the partial results of the kernel for few rows, the plan, the wide kernel's partial results.
+// The workspace: two counters; the plan of the sequences, and their results (calls of few rows); the plan of the wide kernel, and its results.
 struct Space {
-    int64_t parts, plan, wide, bytes;
+    int64_t own_plan, seq_of, own, plan, wide, bytes;
+    int64_t own_items;
 };
 Space space_of(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_rows) {
     auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-    const bool own = !kv16_few_rows(c, Hq, n_rows);
-    Space s;
-    s.parts = kKv16Counters * 4;
-    s.plan = up(s.parts + (int64_t)kKv16Counters * (c.head_dim == 128 ? kPartFloats<128> : kPartFloats<64>) * 4);
-    s.wide = up(s.plan + 16 * (1 + (int64_t)n_groups + c.n_seqs));
+    const bool few = kv16_few_rows(c, Hq, n_rows);
     const int G = Hq / c.n_kv_heads;
+    Space s;
+    s.own_plan = 256;
+    s.seq_of = s.own_plan + 32 * (int64_t)c.n_seqs;
+    s.own = up(s.seq_of + 4 * (int64_t)n_rows);
+    // a sequence has rows G / 8 + 1 tiles at most; and cutting them adds one part for each CTA (kv16_cut)
+    s.own_items = ((int64_t)n_rows * G / kRows + c.n_seqs) * c.n_kv_heads + kCutFor * n_sm;
+    // (for calls of fewer rows too, which may be few where these are many)
+    const int64_t most = few ? s.own_items : ((int64_t)48 * c.n_seqs / kRows + c.n_seqs) * c.n_kv_heads + kCutFor * n_sm;
+    s.plan = up(s.own + most * (c.head_dim == 128 ? kPartFloats<128> : kPartFloats<64>) * 4);
+    s.wide = up(s.plan + 16 * (1 + (int64_t)n_groups + c.n_seqs));
     int64_t units = n_groups ? kv16_units(n_rows, G, n_groups) : 0;
-    if (own) units += kv16_units(n_rows, G, c.n_seqs);
+    if (!few) units += kv16_units(n_rows, G, c.n_seqs);
     s.bytes = up(s.wide + (units ? (units * c.n_kv_heads + n_sm) * kv16_place(c.head_dim) * 4 : 0));
     return s;
+}
+
+// A kernel whose CTAs may share an SM with the wide kernel's: only those that want the same division of its memory do.
+template <typename Kernel>
+cudaError_t with_wide(Kernel kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
 template <typename P, int D>
@@ -452,25 +502,34 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
     int4 *plan_at = (int4 *)(space + at.plan);
     float *wide = (float *)(space + at.wide);
     const Kv16Plan plan = {plan_at, wide};
-    const bool own = !kv16_few_rows(a.c, a.Hq, a.n_rows);
-    if (own || a.p.n_groups) {
-        const cudaError_t e = launch_kv16_wide(s, n_sm, a, own, plan_at, wide);
+    const bool few = kv16_few_rows(a.c, a.Hq, a.n_rows);
+    Own own = {};
+    if (!few || a.p.n_groups) {
+        const cudaError_t e = launch_kv16_wide(s, n_sm, a, !few, plan_at, wide);
         if (e != cudaSuccess) return e;
     }
-    if (own) {
-        const int64_t blocks = ((int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) + 31) / 32 * a.c.n_kv_heads;
-        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        return launch_behind(true, k_join<P, D>, (unsigned)blocks, 128, 0, s, a, plan);
+    const int64_t pairs = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads);
+    if (few) {
+        auto kernel = k_attend<P, D>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kKv8MaxSeqs);
+        if (e == cudaSuccess) e = with_wide(kernel);
+        if (e != cudaSuccess) return e;
+        const int ctas = kCtasPerSm * n_sm;
+        own = Own{(int32_t *)space, (int32_t *)space + 1, (int4 *)(space + at.own_plan), (int32_t *)(space + at.seq_of), (float *)(space + at.own), at.own_items, kCutFor * n_sm};
+        // no more CTAs than there can be parts of the longest sequences
+        const int64_t segs = (pairs / kRows + a.c.n_seqs) * a.c.n_kv_heads;
+        const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
+        e = launch_behind(a.p.n_groups > 0, kernel, (unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s, a, own);
+        if (e != cudaSuccess) return e;
     }
-    auto kernel = k_attend<P, D>;
-    const size_t bytes = 8 * (size_t)a.c.n_seqs;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kKv8MaxSeqs);
-    if (e != cudaSuccess) return e;
-    // no more CTAs than there can be parts of the longest sequences
-    const int64_t segs = ((int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads) / kRows + a.c.n_seqs) * a.c.n_kv_heads, ctas = kCtasPerSm * n_sm;
-    const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
-    return launch_behind(a.p.n_groups > 0, kernel, (unsigned)(most < ctas ? most : ctas), kThreads, bytes, s, a, (int32_t *)space,
-                         (float *)(space + at.parts), plan);
+    const int64_t blocks = (pairs + 31) / 32 * a.c.n_kv_heads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    // few pairs: many threads and CTAs for each, and many results at a time, since what they wait for is the chain of reads
+    auto join = [&](auto kernel, int slices, int threads) {
+        const cudaError_t e = with_wide(kernel);
+        return e != cudaSuccess ? e : launch_behind(true, kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
+    };
+    return blocks <= n_sm ? join(k_join<P, D, 1, 8, D / 16>, D / 16, 128) : join(k_join<P, D, 4, 3, 1>, 1, D / 16 * 32);
 }
 
 }  // namespace
@@ -487,8 +546,6 @@ int64_t kv16_attention_workspace(int n_sm, const llm_kv16_cache &c, int n_groups
 }
 
 cudaError_t launch_kv16_attention(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
-    // a segment cut into c >= 2 parts has more than (c - 1) share pages, so there are at most two parts for each CTA's share
-    if (2 * kCtasPerSm * n_sm > kKv16Counters / 2 || kCtasPerSm * n_sm > kMaxJoin * kMaxJoin) return cudaErrorInvalidConfiguration;
     if (a.c.dtype == LLM_DTYPE_F16) return a.c.head_dim == 128 ? attend<__half, 128>(s, n_sm, a) : attend<__half, 64>(s, n_sm, a);
     return a.c.head_dim == 128 ? attend<__nv_bfloat16, 128>(s, n_sm, a) : attend<__nv_bfloat16, 64>(s, n_sm, a);
 }

@@ -470,11 +470,11 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_weigh_wide(const __grid_con
 template <typename P, int D>
 cudaError_t few(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     auto kernel = k_weigh<P, D>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kKv8MaxSeqs);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kKv8MaxSeqs);
     if (e != cudaSuccess) return e;
     const int64_t segs = (int64_t)a.c.n_seqs * a.c.n_kv_heads, ctas = kCtasPerSm * n_sm;
     const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
-    kernel<<<(unsigned)(most < ctas ? most : ctas), kThreads, 8 * (size_t)a.c.n_seqs, s>>>(a);
+    kernel<<<(unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -7,7 +7,7 @@
 //   warps 0-7     softmax, four for each tile: a thread owns a row (a TMEM lane) and holds its 128 scores in registers;
 //                 the 16-bit weights go back over the scores in TMEM, where they are the A operand of the second product
 //   warp 8        issues the MMAs (one lane) and owns the 512 TMEM columns: two score tiles and two outputs
-//   warp 9        copies q, K and V by TMA: the pages as they lie, each 64 dims a panel of 128-byte swizzled rows, K the
+//   warp 9        plans, and copies q, K and V by TMA: the pages as they lie, each 64 dims a panel of 128-byte swizzled rows, K the
 //                 K-major and V the MN-major B operand
 // For each block of a tile the tensor cores do O += P V and then S = Q K of the tile's next block, tile after tile, in order, so
 // the next scores may take the place of weights that the product issued before still reads.
@@ -21,9 +21,8 @@ namespace qd {
 
 namespace {
 
-constexpr int kSoftmax = 8, kMmaWarp = 8, kCopyWarp = 9, kThreads = 12 * 32;
-constexpr int kRegsSoftmax = 208, kRegsRest = 88;  // 168 at launch
-static_assert(2 * kRegsSoftmax + kRegsRest <= 3 * 168, "no more than the launch has");
+constexpr int kSoftmax = 8, kMmaWarp = 8, kThreads = 10 * 32;
+constexpr int kRegs = 112;  // of a thread: so that a CTA of the kernel for the sequences' own tokens fits beside this one's
 constexpr int kStages = 2, kRecs = 4;
 constexpr int kLeastBlocks = 2;  // of a part: one for each tile
 constexpr float kLag = 8.f;
@@ -190,34 +189,40 @@ struct Bars {
 };
 
 // A row's softmax of a block, by each lane of a warp: 128 scores at s_at in TMEM, weights in their place, m and l
-// brought up to date, the output at o_at rescaled where that is due.  CUT: tokens from `limit` on, and of pages that are not
-// there, have no weight.
-template <typename P, int D, bool CUT>
-QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, uint32_t ok, bool have_o, float &m, float &l) {
-    uint32_t raw[4][32];
+// brought up to date, the output at o_at rescaled where that is due.  cut: tokens from `limit` on, and of pages that are not
+// there, have no weight.  Scores are read twice, 64 at a time, and the loops are not unrolled: with all 128 in registers a turn is 100 cycles
+// shorter, which the products hide, but the code four times as long, whose first pass waits for its instructions (6000 cycles
+// instead of 3000), and there is no room on the SM for the kernel of the sequences' own tokens.
+template <typename P, int D>
+QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, uint32_t ok, bool cut, bool have_o, float &m, float &l) {
+    uint32_t raw[2][32];
+    auto load = [&](int h) {
+        tmem_ld32_start(s_at + 64 * h, raw[0]);
+        tmem_ld32_start(s_at + 64 * h + 32, raw[1]);
+        tmem_ld32_end<true>(raw[0]);
+        tmem_ld32_end<false>(raw[1]);
+        if (cut) {
+            const int vis = limit - 64 * h;
+            const uint32_t there = ok >> (4 * h);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32_start(s_at + 32 * c, raw[c]);
-    tmem_ld32_end<true>(raw[0]);
-#pragma unroll
-    for (int c = 1; c < 4; ++c) tmem_ld32_end<false>(raw[c]);
-    if (CUT) {
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-            if (e >= limit || !((ok >> (e / kKv8Page)) & 1u)) raw[e / 32][e % 32] = 0xff800000u;
-    }
-    auto x = [&](int e) { return __uint_as_float(raw[e / 32][e % 32]); };
-    float tops[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float u = fmaxf(x(32 * c), x(32 * c + 1)), v = fmaxf(x(32 * c + 2), x(32 * c + 3));
-#pragma unroll
-        for (int e = 4; e < 32; e += 4) {  // three operands to an instruction
-            u = fmaxf(fmaxf(u, x(32 * c + e)), x(32 * c + e + 1));
-            v = fmaxf(fmaxf(v, x(32 * c + e + 2)), x(32 * c + e + 3));
+            for (int e = 0; e < 64; ++e)
+                if (e >= vis || !((there >> (e / kKv8Page)) & 1u)) raw[e / 32][e % 32] = 0xff800000u;
         }
-        tops[c] = fmaxf(u, v);
+    };
+    auto x = [&](int e) { return __uint_as_float(raw[e / 32][e % 32]); };
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        load(h);
+        float u = fmaxf(x(0), x(1)), v = fmaxf(x(2), x(3));
+#pragma unroll
+        for (int e = 4; e < 64; e += 4) {  // three operands to an instruction
+            u = fmaxf(fmaxf(u, x(e)), x(e + 1));
+            v = fmaxf(fmaxf(v, x(e + 2)), x(e + 3));
+        }
+        most = fmaxf(most, fmaxf(u, v));
     }
-    const float most = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * fac;
+    most *= fac;
     const bool grow = most > m + kLag || (m == -INFINITY && most > m);
     if (__any_sync(kFullMask, grow)) {
         const float to = grow ? most : m, k = m == to ? 1.f : ex2(m - to);
@@ -227,18 +232,22 @@ QD_DEV void block_weights(uint32_t s_at, uint32_t o_at, float fac, int limit, ui
     }
     const float off = Bits16<P>::kLift - (m == -INFINITY ? 0.f : m);
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        load(h);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t w16[16];
+        for (int c = 0; c < 2; ++c) {
+            uint32_t w16[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            float2 w = fma2(make_float2(x(32 * c + e), x(32 * c + e + 1)), make_float2(fac, fac), make_float2(off, off));
-            w.x = ex2(w.x);
-            w.y = ex2(w.y);
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
-            w16[e / 2] = Bits16<P>::pack(w.x, w.y);
+            for (int e = 0; e < 32; e += 2) {
+                float2 w = fma2(make_float2(x(32 * c + e), x(32 * c + e + 1)), make_float2(fac, fac), make_float2(off, off));
+                w.x = ex2(w.x);
+                w.y = ex2(w.y);
+                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
+                w16[e / 2] = Bits16<P>::pack(w.x, w.y);
+            }
+            tmem_st16(s_at + 32 * h + 16 * c, w16);
         }
-        tmem_st16(s_at + 16 * c, w16);
     }
     sum[0] = add2(sum[0], sum[1]);
     l += sum[0].x + sum[0].y;
@@ -267,7 +276,7 @@ struct View {
 };
 
 template <typename P, int D>
-__global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ WideArgs w) {
+__global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
     using namespace ptx;
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -308,7 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
     pdl_launch();
     if (warp < kSoftmax) {
         // ================= softmax =================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         while (begin()) {
             const View p(b.piece, R);
             const Kv16Span &s = b.piece.s;
@@ -330,8 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
                 tc_fence_after();
                 const uint32_t ok = b.rec[j % kRecs];
                 const int left = limit - j * kKeyBlock;
-                if (shortest - j * kKeyBlock < kKeyBlock || ok != 0xffu) block_weights<P, D, true>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
-                else block_weights<P, D, false>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, k > 0, m, l);
+                block_weights<P, D>(s_at(t) + lanes, o_at(t) + lanes, fac, left, ok, shortest - j * kKeyBlock < kKeyBlock || ok != 0xffu, k > 0, m, l);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -410,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
         }
         return;
     }
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kMmaWarp) {
         // ================= MMA =================
         tmem_alloc(&b.tmem, 512);
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
             if (!end()) break;
         }
         tmem_free(b.tmem, 512);
-    } else if (warp == kCopyWarp) {
+    } else {
         // ================= the plan, and copies =================
         if (lane < 3) tma_prefetch_desc(lane == 0 ? &w.q : (lane == 1 ? &w.k : &w.v));
         const bool first = blockIdx.x == 0;
@@ -615,9 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_wide(const __grid_constant__ Wi
             __syncwarp();
             if (!end()) break;
         }
-    } else {
-        while (begin() && end()) {
-        }
     }
 }
 
@@ -626,13 +629,8 @@ cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
     auto kernel = k_wide<P, D>;
     constexpr int kBytes = Cfg<D>::kTiles + (int)sizeof(Bars);
     static_assert(kBytes <= (int)kMaxSmemOptin, "fits an SM");
-    // the warps' split of the registers would wait for ever if a launch had fewer
-    static const int regs = [&]() {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kernel) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (3 * regs < 2 * kRegsSoftmax + kRegsRest) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kThreads, kBytes, s>>>(w);
     return cudaGetLastError();

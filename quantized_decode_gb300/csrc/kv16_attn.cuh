@@ -12,7 +12,6 @@
 namespace qd {
 
 constexpr int kTileLanes = 128, kKeyBlock = 128;  // lanes of a tile, tokens of a block of keys
-constexpr int kKv16Counters = 4096;
 
 inline __host__ __device__ int kv16_tile_rows(int G) { return kTileLanes / G; }
 // floats of a wide item's result: [tile][d / 4][lane][4] and [tile][lane] log2 of the sums
@@ -126,20 +125,6 @@ struct Kv16Join {
             const float w = ex2(t[i] - ref);
             sum += w;
             v = make_float4(fmaf(o[i].x, w, v.x), fmaf(o[i].y, w, v.y), fmaf(o[i].z, w, v.z), fmaf(o[i].w, w, v.w));
-        }
-    }
-    QD_DEV void add_parts(const Kv16Parts &p, int d4) {
-        for (int i0 = 0; i0 < p.n; i0 += 8) {
-            float t[8];
-            float4 o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t at = min(i0 + i, p.n - 1) * p.step;
-                t[i] = ld_part(p.top + at);
-                o[i] = ld_part4(p.o + at + (int64_t)d4 * kTileLanes * 4);
-                if (i0 + i >= p.n) t[i] = -INFINITY;
-            }
-            add(t, o);
         }
     }
     QD_DEV float4 value() const {

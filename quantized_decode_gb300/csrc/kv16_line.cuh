@@ -55,11 +55,11 @@ struct Kv16Line {
 };
 // Segments of p pages are cut into ceil(p / share) even parts, one work item each.  Returns the smallest share, but at
 // least `least`, that leaves no more items than CTAs; where the segments alone are more than half the CTAs, items are taken in
-// turn and the share is the average load.  upto[b]: the items that end with sequence b; upto[B + b]: those of cut
-// segments.  By the whole CTA, each thread for B / threads sequences.
+// turn and the share is the average load.  upto[b]: the items that end with sequence b.  By the whole CTA, each thread for
+// B / threads sequences.
 template <int WARPS, typename LineOf>
 QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32_t *err) {
-    __shared__ int scratch[WARPS], s_run[WARPS][2];
+    __shared__ int scratch[WARPS], s_run[WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // up to 32 sequences: one for each lane, and every warp counts for itself
     const bool small = B <= 32;
@@ -107,48 +107,29 @@ QD_DEV int kv16_cut(int B, int ctas, int least, LineOf line_of, int *upto, int32
         }
         share = good;
     }
-    // ---- running sums of the items, and of those of cut segments
-    int mine = 0, mine_cut = 0;
+    // ---- running sums of the items
+    int mine = 0;
     for (int b = b0; b < b1; ++b) {
         const Kv16Line s = b == b0 ? one : line_of(b);
-        const int n = kv16_parts_of(s.pages, share);
-        mine += s.segs * n;
-        mine_cut += n > 1 ? s.segs * n : 0;
-        if (small) continue;
-        upto[b] = mine;
-        upto[B + b] = mine_cut;
+        mine += s.segs * kv16_parts_of(s.pages, share);
+        if (!small) upto[b] = mine;
     }
-    int run = mine, run_cut = mine_cut;
+    int run = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const int v = __shfl_up_sync(kFullMask, run, m), w = __shfl_up_sync(kFullMask, run_cut, m);
-        if (lane >= m) {
-            run += v;
-            run_cut += w;
-        }
+        const int v = __shfl_up_sync(kFullMask, run, m);
+        if (lane >= m) run += v;
     }
     if (small) {
-        if (warp == 0 && lane < B) {
-            upto[lane] = run;
-            upto[B + lane] = run_cut;
-        }
+        if (warp == 0 && lane < B) upto[lane] = run;
         __syncthreads();
         return share;
     }
-    if (lane == 31) {
-        s_run[warp][0] = run;
-        s_run[warp][1] = run_cut;
-    }
+    if (lane == 31) s_run[warp] = run;
     __syncthreads();
-    int before = run - mine, before_cut = run_cut - mine_cut;
-    for (int w = 0; w < warp; ++w) {
-        before += s_run[w][0];
-        before_cut += s_run[w][1];
-    }
-    for (int b = b0; b < b1; ++b) {
-        upto[b] += before;
-        upto[B + b] += before_cut;
-    }
+    int before = run - mine;
+    for (int w = 0; w < warp; ++w) before += s_run[w];
+    for (int b = b0; b < b1; ++b) upto[b] += before;
     __syncthreads();
     return share;
 }
