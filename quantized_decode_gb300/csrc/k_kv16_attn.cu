@@ -174,9 +174,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int i = 0; i < VP; ++i) vw[r][i] = make_uint4(0, 0, 0, 0);
+        // the 128-byte lines of a page's K and V of the head, one or two of each for every lane, into L2
+        auto ahead = [&](int ph) {
+            if (ph < 0) return;
+            const int64_t at = head_at + ph * page_step;
+#pragma unroll
+            for (int x = 0; x < kKv8Page * D * 2 / 128; x += 32) {
+                if (kKv8Page * D * 2 / 128 < 32 && lane >= kKv8Page * D * 2 / 128) break;
+                prefetch_l2((const P *)a.c.k_pool + at + (x + lane) * 64);
+                prefetch_l2((const P *)a.c.v_pool + at + (x + lane) * 64);
+            }
+        };
         int ph = __shfl_sync(kFullMask, phys, 0);
         load_k(ph);
         load_v(ph);
+        ahead(__shfl_sync(kFullMask, phys, 1));
 
         const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[OT][4];
@@ -204,6 +216,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
                 phys_next = entry(j + 33 + lane);
             }
             ph = __shfl_sync(kFullMask, phys, (at + 1) & 31);
+            const int ph2 = __shfl_sync(kFullMask, phys, (at + 2) & 31);
+            if (at < 30 || at == 31) ahead(ph2);
             // ---- scores of tokens g, g + 8 and rows 2 c, 2 c + 1
             float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -397,40 +411,40 @@ __global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_c
     float4 v[F];
 #pragma unroll
     for (int i = 0; i < F; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const Found f = found[0][lane], own_f = found[1][lane];
+    const int n = f.n + own_f.n;
 #pragma unroll 1
-    for (int z = 0; z < 2; ++z) {
-        const Found f = found[z][lane];
-#pragma unroll 1
-        for (int k0 = 0; k0 < f.n; k0 += N) {
-            float t[N];
-            float4 x[N][F];
+    for (int k0 = 0; k0 < n; k0 += N) {
+        float t[N];
+        float4 x[N][F];
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const int64_t at = min(k0 + k, f.n - 1) * f.step;
-                t[k] = ld_part(f.top + at);
+        for (int k = 0; k < N; ++k) {
+            const int i = min(k0 + k, n - 1);
+            const bool front = i < f.n;
+            const int64_t at = front ? i * f.step : (i - f.n) * own_f.step;
+            t[k] = ld_part((front ? f.top : own_f.top) + at);
 #pragma unroll
-                for (int i = 0; i < F; ++i) x[k][i] = ld_part4(f.o + at + (part * F + i) * f.size4);
-            }
-            float to = top;
+            for (int y = 0; y < F; ++y) x[k][y] = ld_part4((front ? f.o : own_f.o) + at + (part * F + y) * (front ? f.size4 : own_f.size4));
+        }
+        float to = top;
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                if (k0 + k >= f.n) t[k] = -INFINITY;
-                to = fmaxf(to, t[k]);
-            }
-            const float ref = to == -INFINITY ? 0.f : to, down = ex2(top - ref);
-            top = to;
-            sum *= down;
+        for (int k = 0; k < N; ++k) {
+            if (k0 + k >= n) t[k] = -INFINITY;
+            to = fmaxf(to, t[k]);
+        }
+        const float ref = to == -INFINITY ? 0.f : to, down = ex2(top - ref);
+        top = to;
+        sum *= down;
 #pragma unroll
-            for (int i = 0; i < F; ++i) v[i] = make_float4(v[i].x * down, v[i].y * down, v[i].z * down, v[i].w * down);
+        for (int i = 0; i < F; ++i) v[i] = make_float4(v[i].x * down, v[i].y * down, v[i].z * down, v[i].w * down);
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                if (t[k] == -INFINITY) continue;
-                const float w = ex2(t[k] - ref);
-                sum += w;
+        for (int k = 0; k < N; ++k) {
+            if (t[k] == -INFINITY) continue;
+            const float w = ex2(t[k] - ref);
+            sum += w;
 #pragma unroll
-                for (int i = 0; i < F; ++i)
-                    v[i] = make_float4(fmaf(x[k][i].x, w, v[i].x), fmaf(x[k][i].y, w, v[i].y), fmaf(x[k][i].z, w, v[i].z), fmaf(x[k][i].w, w, v[i].w));
-            }
+            for (int i = 0; i < F; ++i)
+                v[i] = make_float4(fmaf(x[k][i].x, w, v[i].x), fmaf(x[k][i].y, w, v[i].y), fmaf(x[k][i].z, w, v[i].z), fmaf(x[k][i].w, w, v[i].w));
         }
     }
     const int64_t at = row * a.Hq + head * G + in;
@@ -529,7 +543,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
         const cudaError_t e = with_wide(kernel);
         return e != cudaSuccess ? e : launch_behind(true, kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
     };
-    return blocks <= n_sm ? join(k_join<P, D, 1, 8, D / 16>, D / 16, 128) : join(k_join<P, D, 4, 3, 1>, 1, D / 16 * 32);
+    return blocks <= n_sm ? join(k_join<P, D, 1, 10, D / 16>, D / 16, 128) : join(k_join<P, D, 4, 3, 1>, 1, D / 16 * 32);
 }
 
 }  // namespace
