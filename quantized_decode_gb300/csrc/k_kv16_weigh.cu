@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_weigh(const __grid_con
 // ---------------------------------------------------------------------------
 // Many rows, on tcgen05: S^T = K q^T with a block of 128 tokens as A, which stays, and a tile of up to 128 (row, head) pairs
 // after another as B.  A thread owns a token (a TMEM lane) and sums over the columns of each tile; the tiles' sums are added
-// with their rounding errors carried along.  Two CTAs on an SM, two score buffers each:
+// with their rounding errors carried along.  Two CTAs on an SM (128 registers a thread: of 168 only one fits), two score buffers each:
 //   warps 0-3  exponentials and sums
 //   warp 4     MMAs and 256 TMEM columns
 //   warp 5     copies: a block of K, then q tile after tile
@@ -220,38 +220,56 @@ QD_DEV bool weigh_item(const Kv16WeighArgs &a, int64_t n, int R, WeighItem &it) 
     return false;
 }
 
-// The sum of a lane's 128 weights of a tile, columns lo .. hi - 1.
-template <bool CUT>
-QD_DEV float tile_sum(uint32_t s_at, const float *ref, float fac, int lo, int hi, uint64_t *empty) {
-    uint32_t raw[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_ld32_start(s_at + 32 * c, raw[c]);
-    tmem_ld32_end<true>(raw[0]);
-#pragma unroll
-    for (int c = 1; c < 4; ++c) tmem_ld32_end<false>(raw[c]);
-    ptx::tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(empty);  // the next scores may come
+// The sum of a lane's weights of a tile, columns lo .. hi - 1 of 128; cut_lo: the warp's largest lo.  32 columns at a time, which only are looked
+// at one by one where a bound lies among them.
+QD_DEV float tile_sum(uint32_t s_at, const float *ref, float fac, int lo, int cut_lo, int hi, uint64_t *empty) {
     float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int e = 0; e < kTile; e += 4) {
-        const float4 r = *reinterpret_cast<const float4 *>(ref + e);
-        const float x[4] = {__uint_as_float(raw[e / 32][e % 32]), __uint_as_float(raw[e / 32][e % 32 + 1]), __uint_as_float(raw[e / 32][e % 32 + 2]),
-                            __uint_as_float(raw[e / 32][e % 32 + 3])};
-        float2 u = fma2(make_float2(x[0], x[1]), make_float2(fac, fac), make_float2(r.x, r.y));
-        float2 v = fma2(make_float2(x[2], x[3]), make_float2(fac, fac), make_float2(r.z, r.w));
-        u.x = ex2(u.x);
-        u.y = ex2(u.y);
-        v.x = ex2(v.x);
-        v.y = ex2(v.y);
-        if (CUT) {
-            u.x = e >= lo && e < hi ? u.x : 0.f;
-            u.y = e + 1 >= lo && e + 1 < hi ? u.y : 0.f;
-            v.x = e + 2 >= lo && e + 2 < hi ? v.x : 0.f;
-            v.y = e + 3 >= lo && e + 3 < hi ? v.y : 0.f;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t raw[2][32];
+        tmem_ld32_start(s_at + 64 * half, raw[0]);
+        tmem_ld32_start(s_at + 64 * half + 32, raw[1]);
+        tmem_ld32_end<true>(raw[0]);
+        tmem_ld32_end<false>(raw[1]);
+        if (half == 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(empty);  // the next scores may come
         }
-        sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
-        sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int first = 64 * half + 32 * c, l = lo - first, h = hi - first;
+            auto weights = [&](int e, float2 &u, float2 &v) {  // columns e .. e + 3 of the 32
+                const float4 r = *reinterpret_cast<const float4 *>(ref + first + e);
+                u = fma2(make_float2(__uint_as_float(raw[c][e]), __uint_as_float(raw[c][e + 1])), make_float2(fac, fac), make_float2(r.x, r.y));
+                v = fma2(make_float2(__uint_as_float(raw[c][e + 2]), __uint_as_float(raw[c][e + 3])), make_float2(fac, fac), make_float2(r.z, r.w));
+                u.x = ex2(u.x);
+                u.y = ex2(u.y);
+                v.x = ex2(v.x);
+                v.y = ex2(v.y);
+            };
+            if (first >= cut_lo && 32 <= h) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float2 u, v;
+                    weights(e, u, v);
+                    sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
+                    sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
+                }
+            } else if (h > 0) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float2 u, v;
+                    weights(e, u, v);
+                    u.x = e >= l && e < h ? u.x : 0.f;
+                    u.y = e + 1 >= l && e + 1 < h ? u.y : 0.f;
+                    v.x = e + 2 >= l && e + 2 < h ? v.x : 0.f;
+                    v.y = e + 3 >= l && e + 3 < h ? v.y : 0.f;
+                    sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
+                    sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
+                }
+            }
+        }
     }
     const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
     return all.x + all.y;
@@ -264,7 +282,7 @@ QD_DEV void add_exact(float &s, float &lost, float x) {
 }
 
 template <typename P, int D>
-__global__ void __launch_bounds__(kWideThreads, 2) k_weigh_wide(const __grid_constant__ WideArgs w) {
+__global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w) {
     using namespace ptx;
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -336,26 +354,25 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_weigh_wide(const __grid_con
                 there = ph >= 0 && ph < a.c.n_pool_pages;
                 old = weigh_old(a, it.s, scores, tok);
             }
-            // the statistics of a tile's column tid: on their way while the tile before is worked on
-            auto ref_of = [&](int i) {
+            // the statistics of a tile's column tid, as they are: on their way while the tile before is worked on
+            auto has_ref = [&](int i) { return i < mine && tid < R * G && (it.tile0 + rank + i * share) * R + tid / G < it.s.rows; };
+            auto lse_of = [&](int i) {
                 const int row = (it.tile0 + rank + i * share) * R + tid / G;
-                return i < mine && tid < R * G && row < it.s.rows ? -lse_ref(__ldg(a.lse + (int64_t)(it.s.row0 + row) * a.Hq + it.head * G + tid % G)) : 0.f;
+                return has_ref(i) ? __ldg(a.lse + (int64_t)(it.s.row0 + row) * a.Hq + it.head * G + tid % G) : 0.f;
             };
-            float sum = 0.f, lost = 0.f, next = ref_of(0);
+            float sum = 0.f, lost = 0.f, next = lse_of(0);
             for (int i = 0; i < mine; ++i, ++n_tile) {
                 const int row0 = (it.tile0 + rank + i * share) * R;
                 float *ref = b.ref[n_tile & 1];
-                ref[tid] = next;
-                next = ref_of(i + 1);
+                ref[tid] = has_ref(i) ? -lse_ref(next) : 0.f;
+                next = lse_of(i + 1);
                 asm volatile("bar.sync 1, 128;" ::: "memory");  // also: the tile before last's have been read
                 fine = wait_warp(&b.s_full[n_tile & 1], n_tile >> 1);
                 if (!fine) break;
                 tc_fence_after();
                 // rows from tok - (kv - rows) on see the token
                 const int hi = min(R, it.s.rows - row0) * G, lo = live ? max(0, tok - (it.s.kv - it.s.rows) - row0) * G : 0;
-                const bool cut = __any_sync(kFullMask, lo > 0) || hi < kTile;
-                const uint32_t at = tmem + (n_tile & 1) * kTile + lanes;
-                const float x = cut ? tile_sum<true>(at, ref, fac, lo, hi, &b.s_empty[n_tile & 1]) : tile_sum<false>(at, ref, fac, lo, hi, &b.s_empty[n_tile & 1]);
+                const float x = tile_sum(tmem + (n_tile & 1) * kTile + lanes, ref, fac, lo, __reduce_max_sync(kFullMask, lo), hi, &b.s_empty[n_tile & 1]);
                 add_exact(sum, lost, x);
             }
             sum += lost;
@@ -484,6 +501,7 @@ cudaError_t wide(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     constexpr int kBytes = Cfg<D>::kTiles + (int)sizeof(Bars);
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs on an SM");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     WideArgs w{};
     w.a = a;
@@ -502,7 +520,18 @@ cudaError_t wide(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const int64_t items = (int64_t)a.c.n_seqs * a.c.n_kv_heads * ((a.c.table_stride + 7) / 8), most = 2 * n_sm >> w.log_share;
+    const int64_t items = (int64_t)a.c.n_seqs * a.c.n_kv_heads * ((a.c.table_stride + 7) / 8);
+    int64_t most = 2 * n_sm;
+    if (w.log_share > 0) {
+        // No more clusters than run at a time, a second round would take as long as the first: two for each place that the device has
+        // for one with an SM to each CTA.  (72; with 76, which 152 SMs seem to hold, two prompts of 4000 rows take 254 us instead of 190.)
+        static const int places = [&]() {
+            cfg.gridDim = dim3(1u << w.log_share);
+            int n = 0;
+            return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : 1;
+        }();
+        most = 2 * places;
+    }
     cfg.gridDim = dim3((unsigned)(items < most ? items : most) << w.log_share);
     return cudaLaunchKernelEx(&cfg, kernel, w);
 }
