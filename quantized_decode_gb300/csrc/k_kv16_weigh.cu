@@ -153,15 +153,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_weigh(const __grid_con
 
 // ---------------------------------------------------------------------------
 // Many rows, on tcgen05: S^T = K q^T with a block of 128 tokens as A, which stays, and a tile of up to 128 (row, head) pairs
-// after another as B.  A thread owns a token (a TMEM lane) and sums over the columns of each tile; the tiles' sums are added
-// with their rounding errors carried along.  Two CTAs on an SM (128 registers a thread: of 168 only one fits), two score buffers each:
-//   warps 0-3  exponentials and sums
-//   warp 4     MMAs and 256 TMEM columns
-//   warp 5     copies: a block of K, then q tile after tile
+// after another as B.  Two threads own a token (a TMEM lane), each half of the columns of each tile, and sum over them; the tiles' sums are added
+// with their rounding errors carried along.  Two CTAs on an SM (96 registers a thread), two score buffers each:
+//   warps 0-7  exponentials and sums, four for each half
+//   warp 8     MMAs and 256 TMEM columns
+//   warp 9     copies: a block of K, then q tile after tile
 // With long prompts a cluster shares a block of tokens, every CTA a part of the tiles, and its first CTA adds up what
 // the others bring through distributed shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, kWideThreads = 192, kMmaWarp = 4, kCopyWarp = 5, kStages = 2, kMaxShare = 4;
+constexpr int kTile = 128, kSumWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kWideThreads = 320, kStages = 2, kMaxShare = 4;
 
 struct WideArgs {
     Kv16WeighArgs a;
@@ -177,9 +177,9 @@ struct Cfg {
 struct Bars {
     uint64_t k_full, k_empty, q_full[kStages], q_empty[kStages], s_full[2], s_empty[2], share_full, share_empty, done;
     alignas(16) float ref[2][kTile];  // by tile: what is added to a column's exponent, read four at a time
-    float shared[kMaxShare][kTile];   // sums of the cluster's other CTAs
+    float shared[kMaxShare][kTile];   // sums of the cluster's other CTAs; first, of the second half's threads
     uint32_t tmem;
-    int abort;
+    int abort, stop;
 };
 
 // The n-th item: a sequence, a block of its tokens and a head.
@@ -220,54 +220,49 @@ QD_DEV bool weigh_item(const Kv16WeighArgs &a, int64_t n, int R, WeighItem &it) 
     return false;
 }
 
-// The sum of a lane's weights of a tile, columns lo .. hi - 1 of 128; cut_lo: the warp's largest lo.  32 columns at a time, which only are looked
-// at one by one where a bound lies among them.
-QD_DEV float tile_sum(uint32_t s_at, const float *ref, float fac, int lo, int cut_lo, int hi, uint64_t *empty) {
+// The sum of a lane's weights in 64 columns of a tile from `from` on, of which columns lo .. hi - 1 count; cut_lo: the warp's largest lo.  32 columns at a
+// time, which only are looked at one by one where a bound lies among them.
+QD_DEV float half_sum(uint32_t s_at, int from, const float *ref, float fac, int lo, int cut_lo, int hi, uint64_t *empty) {
     float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        uint32_t raw[2][32];
-        tmem_ld32_start(s_at + 64 * half, raw[0]);
-        tmem_ld32_start(s_at + 64 * half + 32, raw[1]);
-        tmem_ld32_end<true>(raw[0]);
-        tmem_ld32_end<false>(raw[1]);
-        if (half == 1) {
+    for (int c = 0; c < 2; ++c) {
+        const int first = from + 32 * c, l = lo - first, h = hi - first;
+        uint32_t raw[32];
+        tmem_ld32_start(s_at + first, raw);
+        tmem_ld32_end<true>(raw);
+        if (c == 1) {
             ptx::tc_fence_before();
             __syncwarp();
             if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(empty);  // the next scores may come
         }
+        auto weights = [&](int e, float2 &u, float2 &v) {  // columns e .. e + 3 of the 32
+            const float4 r = *reinterpret_cast<const float4 *>(ref + first + e);
+            u = fma2(make_float2(__uint_as_float(raw[e]), __uint_as_float(raw[e + 1])), make_float2(fac, fac), make_float2(r.x, r.y));
+            v = fma2(make_float2(__uint_as_float(raw[e + 2]), __uint_as_float(raw[e + 3])), make_float2(fac, fac), make_float2(r.z, r.w));
+            u.x = ex2(u.x);
+            u.y = ex2(u.y);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+        };
+        if (first >= cut_lo && 32 <= h) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int first = 64 * half + 32 * c, l = lo - first, h = hi - first;
-            auto weights = [&](int e, float2 &u, float2 &v) {  // columns e .. e + 3 of the 32
-                const float4 r = *reinterpret_cast<const float4 *>(ref + first + e);
-                u = fma2(make_float2(__uint_as_float(raw[c][e]), __uint_as_float(raw[c][e + 1])), make_float2(fac, fac), make_float2(r.x, r.y));
-                v = fma2(make_float2(__uint_as_float(raw[c][e + 2]), __uint_as_float(raw[c][e + 3])), make_float2(fac, fac), make_float2(r.z, r.w));
-                u.x = ex2(u.x);
-                u.y = ex2(u.y);
-                v.x = ex2(v.x);
-                v.y = ex2(v.y);
-            };
-            if (first >= cut_lo && 32 <= h) {
+            for (int e = 0; e < 32; e += 4) {
+                float2 u, v;
+                weights(e, u, v);
+                sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
+                sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
+            }
+        } else if (h > 0) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float2 u, v;
-                    weights(e, u, v);
-                    sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
-                    sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
-                }
-            } else if (h > 0) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float2 u, v;
-                    weights(e, u, v);
-                    u.x = e >= l && e < h ? u.x : 0.f;
-                    u.y = e + 1 >= l && e + 1 < h ? u.y : 0.f;
-                    v.x = e + 2 >= l && e + 2 < h ? v.x : 0.f;
-                    v.y = e + 3 >= l && e + 3 < h ? v.y : 0.f;
-                    sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
-                    sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
-                }
+            for (int e = 0; e < 32; e += 4) {
+                float2 u, v;
+                weights(e, u, v);
+                u.x = e >= l && e < h ? u.x : 0.f;
+                u.y = e + 1 >= l && e + 1 < h ? u.y : 0.f;
+                v.x = e + 2 >= l && e + 2 < h ? v.x : 0.f;
+                v.y = e + 3 >= l && e + 3 < h ? v.y : 0.f;
+                sum[(e >> 2 & 1) * 2] = add2(sum[(e >> 2 & 1) * 2], u);
+                sum[(e >> 2 & 1) * 2 + 1] = add2(sum[(e >> 2 & 1) * 2 + 1], v);
             }
         }
     }
@@ -282,7 +277,7 @@ QD_DEV void add_exact(float &s, float &lost, float x) {
 }
 
 template <typename P, int D>
-__global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w) {
+__global__ void __maxnreg__(96) k_weigh_wide(const __grid_constant__ WideArgs w) {
     using namespace ptx;
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -303,7 +298,7 @@ __global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.s_empty[i], 4);
+            mbar_init(&b.s_empty[i], kSumWarps);
         }
         mbar_init(&b.share_full, 4 * (share - 1) + (share == 1));
         mbar_init(&b.share_empty, 1);
@@ -338,24 +333,26 @@ __global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w
     uint32_t n_tile = 0, n_block = 0;  // tiles and blocks of K so far
     int started_q = 0, started_k = 0;
 
-    if (warp < 4) {
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    if (warp < kSumWarps) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const float fac = kLog2e * (D == 128 ? 0.08838834764831845f : 0.125f);
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x & (kTile - 1), half = warp >> 2;
+        auto sync = []() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
         bool fine = true;
-        for (int n = 0; fine && weigh_item(a, nth(n), R, it); ++n) {
+        // A wait that ran out changes nothing of who comes to which barrier: these warps go on, without work, to the item's end.
+        for (int n = 0; weigh_item(a, nth(n), R, it); ++n) {
             const int mine = my_tiles(it), t0 = it.block * kTile, tok = t0 + tid;
             float *scores = a.scores + ((int64_t)it.b * a.c.n_kv_heads + it.head) * a.score_stride;
             const bool live = tok < it.s.kv;
             float old = 0.f;
             bool there = true;
-            if (rank == 0 && live) {
+            if (rank == 0 && half == 0 && live) {
                 const int ph = __ldg(a.c.page_table + (int64_t)it.b * a.c.table_stride + tok / kKv8Page);
                 there = ph >= 0 && ph < a.c.n_pool_pages;
                 old = weigh_old(a, it.s, scores, tok);
             }
             // the statistics of a tile's column tid, as they are: on their way while the tile before is worked on
-            auto has_ref = [&](int i) { return i < mine && tid < R * G && (it.tile0 + rank + i * share) * R + tid / G < it.s.rows; };
+            auto has_ref = [&](int i) { return half == 0 && i < mine && tid < R * G && (it.tile0 + rank + i * share) * R + tid / G < it.s.rows; };
             auto lse_of = [&](int i) {
                 const int row = (it.tile0 + rank + i * share) * R + tid / G;
                 return has_ref(i) ? __ldg(a.lse + (int64_t)(it.s.row0 + row) * a.Hq + it.head * G + tid % G) : 0.f;
@@ -364,23 +361,31 @@ __global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w
             for (int i = 0; i < mine; ++i, ++n_tile) {
                 const int row0 = (it.tile0 + rank + i * share) * R;
                 float *ref = b.ref[n_tile & 1];
-                ref[tid] = has_ref(i) ? -lse_ref(next) : 0.f;
+                if (half == 0) ref[tid] = has_ref(i) ? -lse_ref(next) : 0.f;
                 next = lse_of(i + 1);
-                asm volatile("bar.sync 1, 128;" ::: "memory");  // also: the tile before last's have been read
-                fine = wait_warp(&b.s_full[n_tile & 1], n_tile >> 1);
-                if (!fine) break;
+                sync();  // also: the tile before last's have been read
+                fine = fine && wait_warp(&b.s_full[n_tile & 1], n_tile >> 1);
+                if (!fine) continue;
                 tc_fence_after();
                 // rows from tok - (kv - rows) on see the token
                 const int hi = min(R, it.s.rows - row0) * G, lo = live ? max(0, tok - (it.s.kv - it.s.rows) - row0) * G : 0;
-                const float x = tile_sum(tmem + (n_tile & 1) * kTile + lanes, ref, fac, lo, __reduce_max_sync(kFullMask, lo), hi, &b.s_empty[n_tile & 1]);
+                const float x =
+                    half_sum(tmem + (n_tile & 1) * kTile + lanes, 64 * half, ref, fac, lo, __reduce_max_sync(kFullMask, lo), hi, &b.s_empty[n_tile & 1]);
                 add_exact(sum, lost, x);
             }
             sum += lost;
             if (!fine) sum = NAN;
-            if (share > 1) {
+            // the halves together; what is read here was written, and will be again, beyond barriers
+            if (half == 1) b.shared[0][tid] = sum;
+            sync();
+            if (half == 0) sum += b.shared[0][tid];
+            if (share > 1 && half == 0) {
                 // what the others bring: their place is free once the first CTA has read the item before
                 if (rank > 0) {
-                    if (n > 0) fine = fine && __all_sync(kFullMask, mbar_wait_cluster(&b.share_empty, (uint32_t)(n - 1) & 1u, kWaitNs));
+                    if (n > 0 && !__all_sync(kFullMask, mbar_wait_cluster(&b.share_empty, (uint32_t)(n - 1) & 1u, kWaitNs))) {
+                        fail();
+                        fine = false;
+                    }
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_map(&b.shared[rank][tid], 0)), "f"(sum) : "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(cluster_map(&b.share_full, 0));
@@ -389,14 +394,16 @@ __global__ void __maxnreg__(128) k_weigh_wide(const __grid_constant__ WideArgs w
                     if (!got) fail();
                     fine = fine && got;
                     for (int r = 1; r < share; ++r) sum += b.shared[r][tid];
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    asm volatile("bar.sync 2, 128;" ::: "memory");
                     if (tid > 0 && tid < share) mbar_arrive_cluster(cluster_map(&b.share_empty, tid));
                     if (!fine) sum = NAN;
                 }
             }
-            if (rank == 0 && live) scores[tok] = old + (there ? sum : 0.f);
+            if (threadIdx.x == 0) b.stop = *abort;
+            sync();
+            if (rank == 0 && half == 0 && live) scores[tok] = old + (there ? sum : 0.f);
+            if (b.stop) break;
         }
-        if (!fine) *abort = 1;
     } else if (warp == kMmaWarp) {
         const uint32_t type = Bits16<P>::kFormat << 7 | Bits16<P>::kFormat << 10, id = umma_idesc_f16_f32(kTile, kTile) | type;
         const uint32_t k_at = desc_k(smem_u32(sk)), q_at = desc_k(smem_u32(sq));
