@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_rope_append(const __grid_consta
     const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
     const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int64_t row = id / a.chunks;
+    pdl_launch();
+    pdl_wait();
     const int Hkv = a.c.n_kv_heads, heads = a.Hq + 2 * Hkv, B = a.c.n_seqs;
     if (id < (B + 31) / 32) kv16_check_seqs(a.row_start, a.kv_len, a.n_rows, a.c, (int)id, true, a.err);
     if (row >= a.n_rows) return;
@@ -193,8 +195,7 @@ cudaError_t rope(cudaStream_t s, Kv16RopeArgs a) {
     if (warps < (a.c.n_seqs + 31) / 32) warps = (a.c.n_seqs + 31) / 32;  // those that look the sequences over
     const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    k_rope_append<T, P, D><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(k_rope_append<T, P, D>, (unsigned)blocks, kWarps * 32, 0, s, a);
 }
 template <typename T>
 cudaError_t rope(cudaStream_t s, const Kv16RopeArgs &a) {
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
     __shared__ uint32_t s_prefix, s_need, s_count;
     const int Hkv = a.c.n_kv_heads, b = blockIdx.x / Hkv, head = blockIdx.x - b * Hkv, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     pdl_launch();
+    pdl_wait();
     const int n = __ldg(a.kv_len + b);
     const bool ok = n >= 0 && (int64_t)n <= (int64_t)a.c.table_stride * kKv8Page && n <= a.score_stride;
     if (t == 0 && head == 0) {
@@ -366,10 +368,10 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_consta
     __shared__ uint64_t bar;
     const int Hkv = a.c.n_kv_heads, D2 = 2 * a.c.head_dim, size = D2 / slices, per = kMoveBytes / size;
     const int t = threadIdx.x, rank = (int)cluster_rank();
-    int id = (int)(blockIdx.x / kMoveCtas);
+    const int id = (int)(blockIdx.x / kMoveCtas);
+    pdl_wait();
     const int slice = id % slices, is_v = id / slices & 1, seg = id / (2 * slices), b = seg / Hkv, head = seg - b * Hkv;
     const int n = __ldg(a.kv_len + b);
-    pdl_wait();
     if (n <= a.budget || (int64_t)n > (int64_t)a.c.table_stride * kKv8Page || n > a.score_stride) return;  // the whole cluster
     const int32_t *kept = a.kept + (int64_t)seg * a.budget, *table = a.c.page_table + (int64_t)b * a.c.table_stride;
     uint8_t *pool = (uint8_t *)(is_v ? a.c.v_pool : a.c.k_pool) + slice * size;
@@ -440,8 +442,7 @@ cudaError_t launch_kv16_evict(cudaStream_t s, const Kv16EvictArgs &a) {
     cudaError_t e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
     if (e != cudaSuccess) return e;
     const int segs = a.c.n_seqs * a.c.n_kv_heads;
-    k_evict_select<<<(unsigned)segs, kSelThreads, kSelKeys * 4, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_behind(k_evict_select, (unsigned)segs, kSelThreads, kSelKeys * 4, s, a);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(k_evict_move, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveBytes);
     if (e != cudaSuccess) return e;

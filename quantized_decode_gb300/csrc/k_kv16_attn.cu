@@ -71,6 +71,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     extern __shared__ int upto[];  // items that end with sequence b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs;
+    // Behind the wide kernel this one reads nothing of it, and what came before has ended: the wide kernel lets it begin when it has waited
+    // for that itself.  It takes nothing from the wide kernel but has to end after it.
+    if (a.p.n_groups == 0) pdl_wait();
     pdl_launch();
     if (threadIdx.x == 0) s_item[0] = *(volatile int32_t *)own.none_left ? INT32_MAX : atomicAdd(own.next, 1);
     __syncthreads();
@@ -462,22 +465,6 @@ __global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_c
     if (part == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718f;
 }
 
-// A launch that may begin while the one before it ends; what it reads of that one waits for its end.
-template <typename... Args, typename... Given>
-cudaError_t launch_behind(bool behind, void (*kernel)(Args...), unsigned blocks, unsigned threads, size_t bytes, cudaStream_t s, Given... given) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = behind ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
-}
-
 // The workspace: two counters; the plan of the sequences, and their results (calls of few rows); the plan of the wide kernel, and its results.
 struct Space {
     int64_t own_plan, seq_of, own, plan, wide, bytes;
@@ -533,7 +520,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
         // no more CTAs than there can be parts of the longest sequences
         const int64_t segs = (pairs / kRows + a.c.n_seqs) * a.c.n_kv_heads;
         const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
-        e = launch_behind(a.p.n_groups > 0, kernel, (unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s, a, own);
+        e = launch_behind(kernel, (unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s, a, own);
         if (e != cudaSuccess) return e;
     }
     const int64_t blocks = (pairs + 31) / 32 * a.c.n_kv_heads;
@@ -541,7 +528,7 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
     // few pairs: many threads and CTAs for each, and many results at a time, since what they wait for is the chain of reads
     auto join = [&](auto kernel, int slices, int threads) {
         const cudaError_t e = with_wide(kernel);
-        return e != cudaSuccess ? e : launch_behind(true, kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
+        return e != cudaSuccess ? e : launch_behind(kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
     };
     return blocks <= n_sm ? join(k_join<P, D, 1, 10, D / 16>, D / 16, 128) : join(k_join<P, D, 4, 3, 1>, 1, D / 16 * 32);
 }

@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_weigh(const __grid_con
     extern __shared__ int upto[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, B = a.c.n_seqs, ctas = (int)gridDim.x;
+    pdl_launch();
+    pdl_wait();
     const int share = kv16_cut<kWarps>(
         B, ctas, kLeast,
         [&](int b) {
@@ -311,6 +313,8 @@ __global__ void __maxnreg__(96) k_weigh_wide(const __grid_constant__ WideArgs w)
     __syncthreads();
     if (share > 1) cluster_sync();
     tc_fence_after();
+    pdl_launch();
+    pdl_wait();
     const uint32_t tmem = b.tmem;
     auto fail = [&]() {
         *abort = 1;
@@ -498,8 +502,7 @@ cudaError_t few(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     if (e != cudaSuccess) return e;
     const int64_t segs = (int64_t)a.c.n_seqs * a.c.n_kv_heads, ctas = kCtasPerSm * n_sm;
     const int64_t most = segs < ctas ? segs * (a.c.table_stride / kLeast + 1) : ctas;
-    kernel<<<(unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(kernel, (unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s, a);
 }
 
 template <typename P, int D>
@@ -520,13 +523,15 @@ cudaError_t wide(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     cfg.blockDim = dim3(kWideThreads);
     cfg.dynamicSmemBytes = kBytes;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1u << w.log_share;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const int64_t items = (int64_t)a.c.n_seqs * a.c.n_kv_heads * ((a.c.table_stride + 7) / 8);
     int64_t most = 2 * n_sm;
     if (w.log_share > 0) {

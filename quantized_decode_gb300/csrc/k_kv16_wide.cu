@@ -314,7 +314,6 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
         tc_fence_after();
         return !*abort;
     };
-    pdl_launch();
     if (warp < kSoftmax) {
         // ================= softmax =================
         while (begin()) {
@@ -520,6 +519,8 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
     } else {
         // ================= the plan, and copies =================
         if (lane < 3) tma_prefetch_desc(lane == 0 ? &w.q : (lane == 1 ? &w.k : &w.v));
+        pdl_wait();    // the others wait for this warp's plan
+        pdl_launch();  // not before: k_attend relies on it
         const bool first = blockIdx.x == 0;
         const Cut cut = cut_spans(w, b.held, G, Hkv, first ? a.err : nullptr);
         if (lane == 0) {
@@ -632,8 +633,7 @@ cudaError_t wide(cudaStream_t s, const WideArgs &w, unsigned blocks) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, kThreads, kBytes, s>>>(w);
-    return cudaGetLastError();
+    return launch_behind(kernel, blocks, kThreads, kBytes, s, w);
 }
 
 }  // namespace

@@ -71,4 +71,21 @@ struct Bits16<__half> {
     QD_DEV static float2 unpack(uint32_t w) { return __half22float2(u32_as_h2(w)); }
 };
 
+// A launch that may begin while the one before it in the stream ends: such kernels begin with pdl_wait, before they read anything that
+// one may have written (k_attend of k_kv16_attn.cu, which waits at its end, says why it may).
+template <typename... Args, typename... Given>
+cudaError_t launch_behind(void (*kernel)(Args...), unsigned blocks, unsigned threads, size_t bytes, cudaStream_t s, Given... given) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
+}
+
 }  // namespace qd
