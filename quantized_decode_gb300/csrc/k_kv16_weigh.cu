@@ -443,7 +443,6 @@ __global__ void __maxnreg__(96) k_weigh_wide(const __grid_constant__ WideArgs w)
         if (!tc_wait(&b.done, 0, nullptr)) fail();
     } else {
         const int page = lane & 7, panel = lane >> 3, beyond = a.c.n_pool_pages * a.c.n_kv_heads * kKv8Page;
-        const uint64_t policy = l2_policy(share == 1);
         bool go = true;
         for (int n = 0; go && weigh_item(a, nth(n), R, it); ++n) {
             const int tiles = my_tiles(it);
@@ -461,7 +460,7 @@ __global__ void __maxnreg__(96) k_weigh_wide(const __grid_constant__ WideArgs w)
             __syncwarp();
             if (panel < C::kP)
                 tma_load_rows(smem_u32(sk) + panel * kPanel + page * (kKv8Page * 128), &w.k, panel * 64,
-                              ph >= 0 ? (ph * a.c.n_kv_heads + it.head) * kKv8Page : beyond, &b.k_full, policy);
+                              ph >= 0 ? (ph * a.c.n_kv_heads + it.head) * kKv8Page : beyond, &b.k_full);
             started_k = ++n_block;
             for (int i = 0; i < tiles; ++i, ++n_tile) {
                 const uint32_t st = n_tile % kStages;

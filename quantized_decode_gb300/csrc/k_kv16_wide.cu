@@ -550,8 +550,13 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
             if (p.nb > 0) {
                 constexpr uint32_t kPageBytes = kKv8Page * 128;  // of a panel
                 const int page = lane & 7, panel = lane >> 3;
-                // keys of two units are read side by side: 32 users 40.1 us without this policy, 37.3 with it
-                const uint64_t policy = l2_policy(b.piece.units <= 2);
+                // Keys of two units are read side by side, those of more again and again.  (32 users: 40.1 us without the policy for lines that are
+                // read once, 37.3 with it; 8 x 200 rows, 25 units: 477 and 527.)
+                const bool once = b.piece.units <= 2;
+                auto copy = [&](uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+                    if (once) tma_load_rows_once(dst, map, x, y, bar);
+                    else tma_load_rows(dst, map, x, y, bar);
+                };
                 const int32_t *table = (p.prefix ? a.p.page_table + (int64_t)b.piece.span * a.p.table_stride : a.c.page_table + (int64_t)s.seq * a.c.table_stride) +
                                        (int64_t)p.blk0 * (kKeyBlock / kKv8Page);
                 // lane l knows page l of four blocks, and of the next four: -2 where there is none, -1 for one that is out of range
@@ -591,7 +596,7 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
                         mbar_expect_tx(&b.k_full[st], C::kTileBytes);
                     }
                     __syncwarp();
-                    if (panel < C::kP) tma_load_rows(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st], policy);
+                    if (panel < C::kP) copy(smem_u32(sk) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.k, panel * 64, y, &b.k_full[st]);
                     started = 2 * j + 1;
                     if (use > 0 && !(go = wait_warp(&b.v_empty[st], use - 1))) break;
                     // a page of which the last slots hold nothing: they become 0 before V is used
@@ -600,7 +605,7 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
                     uint64_t *bar = cut_page ? &b.v_part : &b.v_full[st];
                     if (lane == 0) mbar_expect_tx(bar, C::kTileBytes);
                     __syncwarp();
-                    if (panel < C::kP) tma_load_rows(smem_u32(sv) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.v, panel * 64, y, bar, policy);
+                    if (panel < C::kP) copy(smem_u32(sv) + st * C::kTileBytes + panel * kPanel + page * kPageBytes, &w.v, panel * 64, y, bar);
                     if (cut_page) {  // the last block
                         part_started = true;
                         if (!(go = wait_warp(bar, 0))) break;

@@ -36,17 +36,19 @@ QD_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int 
         "r"(x), "r"(y), "r"(z), "r"(ptx::smem_u32(bar))
         : "memory");
 }
-// What a copy's lines are to L2: read once, and first to go (the kernels' own results stay there then), or as any others.
-QD_DEV uint64_t l2_policy(bool once) {
-    uint64_t first, normal;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
-    return once ? first : normal;
-}
-QD_DEV void tma_load_rows(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint64_t policy) {
+QD_DEV void tma_load_rows(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x),
-        "r"(y), "r"(ptx::smem_u32(bar)), "l"(policy)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x),
+        "r"(y), "r"(ptx::smem_u32(bar))
+        : "memory");
+}
+// The same where the lines are read once: they are the first to leave L2, and the kernels' own results stay.
+QD_DEV void tma_load_rows_once(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(ptx::smem_u32(bar)), "l"(policy)
         : "memory");
 }
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
