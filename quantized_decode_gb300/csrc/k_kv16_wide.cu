@@ -180,11 +180,8 @@ struct Bars {
     uint32_t tmem;
     float top[2][kTileLanes];
     int abort;
-    // the CTA's place in the work, kept here and not in registers: the softmax needs them all
-    Cut cut;
     Piece piece;
-    int64_t at, end;
-    int found;
+    int found;  // whether there is one
     Kv16Span held[32];
 };
 
@@ -523,23 +520,20 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
         pdl_launch();  // not before: k_attend relies on it
         const bool first = blockIdx.x == 0;
         const Cut cut = cut_spans(w, b.held, G, Hkv, first ? a.err : nullptr);
-        if (lane == 0) {
-            b.cut = cut;
-            b.at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
-            b.end = cut.share ? (int64_t)blockIdx.x + 1 : cut.length * (blockIdx.x + 1) / gridDim.x;
-            if (first) {
-                w.plan[0] = cut.share ? make_int4(0, 0, 0, 0) : make_int4((int)gridDim.x, 0, (int)max(cut.length, (int64_t)1), (int)(cut.length >> 32));
-                if (!cut.fits) kv8_report(a.err);
-            }
+        int64_t at = cut.share ? (int64_t)blockIdx.x : cut.length * blockIdx.x / gridDim.x;
+        const int64_t last = cut.share ? (int64_t)blockIdx.x + 1 : cut.length * (blockIdx.x + 1) / gridDim.x;
+        if (first && lane == 0) {
+            w.plan[0] = cut.share ? make_int4(0, 0, 0, 0) : make_int4((int)gridDim.x, 0, (int)max(cut.length, (int64_t)1), (int)(cut.length >> 32));
+            if (!cut.fits) kv8_report(a.err);
         }
-        __syncwarp();
-        for (bool working = false;; working = true) {
-            Piece next;
-            int64_t at = b.at;
-            bool found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, blockIdx.x == 0 && !working ? w.plan : nullptr, next);
-            while (found && next.blk0 == next.blk1) found = next_piece(w, b.held, b.cut, G, Hkv, at, b.end, nullptr, next);
+        Piece next;
+        bool found = next_piece(w, b.held, cut, G, Hkv, at, last, first ? w.plan : nullptr, next);
+        auto skip_empty = [&]() {
+            while (found && next.blk0 == next.blk1) found = next_piece(w, b.held, cut, G, Hkv, at, last, nullptr, next);
+        };
+        skip_empty();
+        for (;;) {
             if (lane == 0) {
-                b.at = at;
                 b.found = found;
                 if (found) b.piece = next;
             }
@@ -626,6 +620,9 @@ __global__ void __maxnreg__(kRegs) k_wide(const __grid_constant__ WideArgs w) {
                     if (part_started) tc_wait(&b.v_part, 0, nullptr);
                 }
             }
+            // the next piece, while this one's products are made
+            found = next_piece(w, b.held, cut, G, Hkv, at, last, nullptr, next);
+            skip_empty();
             __syncwarp();
             if (!end()) break;
         }
