@@ -34,7 +34,8 @@ QD_DEV void store_vec(P *p, const float (&v)[8]) {
 // time; kLanes lanes hold a head, each one 16-byte piece of its first half and the same piece of its second, so that
 // the two elements of a pair are in one lane.  Each of the D / 2 angles is computed once in a warp, on its own axis, and
 // handed round.  In turns it is pos * turns[i] modulo 1, in 64-bit integers exact at any position.  The row's data and
-// positions are on their way while its sequence and page are looked up.
+// positions are on their way while its sequence and page are looked up.  About 8000 rows of 28 + 4 + 4 heads of 128 in bf16 (150 MB): 31 us, 4.8 TB/s, bound by the
+// latency of loads over 17 warps an SM; eight rows 4.4 us, bound by the chain row_start, table, store.
 // ---------------------------------------------------------------------------
 template <typename T, typename P, int D>
 __global__ void __launch_bounds__(kWarps * 32) k_rope_append(const __grid_constant__ Kv16RopeArgs a) {
@@ -207,7 +208,8 @@ cudaError_t rope(cudaStream_t s, const Kv16RopeArgs &a) {
 // Eviction.  One CTA chooses for one sequence and head.  Scores become keys, 32-bit numbers that order as they do; the
 // budget's last key is found digit by digit from the top (radix select: a histogram of the digit over the keys that
 // share the digits found so far), and one pass in the order of the slots writes those above it and, of those equal to
-// it, as many as there is room for.  Keys stay in shared memory where they fit.
+// it, as many as there is room for.  Keys stay in shared memory where they fit.  128 choices among up to 16384 scores 18 us, 2 among 4159 11 us: three passes of
+// additions in shared memory and barriers.
 // ---------------------------------------------------------------------------
 constexpr int kSelThreads = 1024, kSelKeys = 40960, kDigitBits = 11, kBins = 1 << kDigitBits;
 
@@ -358,7 +360,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
 // write begins may be overwritten, and what comes behind is still as it was.  A cluster of kMoveCtas CTAs takes a sequence, head, K or V
 // and a slice of the columns; a round reads the next tokens, up to 64 KB in the shared memory of each CTA, waits until all
 // have read, and writes.  Tokens travel by bulk copies, one thread each: a row of D numbers (or a slice) from where it
-// lay to where it goes.  Slices, that a call of few heads finds all SMs.
+// lay to where it goes.  Slices, that a call of few heads finds all SMs.  16 prompts to 16384 tokens cut to 4096 (8 heads of 128 numbers, 290 MB): 59 us, 4.9 TB/s; with 32 KB
+// a CTA 69 us, with 96 KB 80, with clusters of 4 71.  (One warp for each 32-byte column, in the order of the slots, took 210 us, and 157 where these take 10: 4096 tokens
+// of 2 heads.)
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256, kMoveCtas = 8, kMoveBytes = 65536;
 
