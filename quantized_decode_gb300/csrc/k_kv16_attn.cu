@@ -30,6 +30,7 @@ namespace qd {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
+constexpr int kFewPairs = kRows;  // (row, query head) pairs of a sequence and K/V head in the mean, in calls of few rows
 // Pages of a part at least.  (32 steps with 50 to 500 tokens of their own: 8 pages 43.9 us, 16 41.5, 32 39.6; 64 sequences of 150 to 1500: 85.2, 85.3, 86.8.)
 constexpr int kLeast = 4 * kWarps;
 constexpr int kCutFor = 2 * kCtasPerSm;  // parts for each SM: two for each CTA, which draw them
@@ -486,7 +487,7 @@ Space space_of(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_ro
     // a sequence has rows G / 8 + 1 tiles at most; and cutting them adds one part for each CTA (kv16_cut)
     s.own_items = ((int64_t)n_rows * G / kRows + c.n_seqs) * c.n_kv_heads + kCutFor * n_sm;
     // (for calls of fewer rows too, which may be few where these are many)
-    const int64_t most = few ? s.own_items : ((int64_t)48 * c.n_seqs / kRows + c.n_seqs) * c.n_kv_heads + kCutFor * n_sm;
+    const int64_t most = few ? s.own_items : ((int64_t)kFewPairs * c.n_seqs / kRows + c.n_seqs) * c.n_kv_heads + kCutFor * n_sm;
     s.plan = up(s.own + most * (c.head_dim == 128 ? kPartFloats<128> : kPartFloats<64>) * 4);
     s.wide = up(s.plan + 16 * (1 + (int64_t)n_groups + c.n_seqs));
     int64_t units = n_groups ? kv16_units(n_rows, G, n_groups) : 0;
@@ -541,10 +542,11 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
 }  // namespace
 
 bool kv16_few_rows(const llm_kv16_cache &c, int Hq, int n_rows) {
-    // Rows of a sequence, times heads, where the wide kernel's tiles of 128 begin to pay: as in kv8_few_rows, whose kernels divide the work in the same
-    // way and were measured on both sides.  Items are counted in 32 bits, whatever row_start holds; beyond this the wide kernel.
+    // One tile of 8 pairs, rows times heads, of each sequence in the mean: with two the pages would be gone through twice.  This kernel and the wide one,
+    // behind short prefixes: 8 pairs of 16 sequences to 2000 tokens 28.8 and 32.5 us, 12 pairs 45.4 and 39.2, 14 of 8 to 12000 49.4 and 32.0, 49 of 16 to 8000
+    // 146 and 52; 32 users' steps 36.7 and 51.0.  Items are counted in 32 bits, whatever row_start holds; beyond this the wide kernel.
     const int64_t rows = (int64_t)n_rows * (Hq / c.n_kv_heads);
-    return rows <= (int64_t)48 * c.n_seqs && (rows / 8 + 1) * c.n_seqs * c.n_kv_heads < 1 << 30;
+    return rows <= (int64_t)kFewPairs * c.n_seqs && (rows / 8 + 1) * c.n_seqs * c.n_kv_heads < 1 << 30;
 }
 
 int64_t kv16_attention_workspace(int n_sm, const llm_kv16_cache &c, int n_groups, int Hq, int n_rows) {

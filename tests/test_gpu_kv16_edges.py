@@ -89,6 +89,28 @@ def test_attention_and_weigh_of_a_thousand_sequences(prefix):
     assert c.err.item() == 0
 
 
+@pytest.mark.parametrize("prefix", [None, ([90], [0, 14])])
+def test_drafts_among_steps(prefix):
+    """A few sequences with many rows among many with one: several tiles of rows in the kernel for few."""
+    rng = np.random.default_rng(37)
+    rows = (6, 1, 1, 1, 0, 1, 9, 1, 1, 1, 1, 0, 1, 1)
+    kv = (40, 17, 300, 1, 9, 64, 2000, 5, 90, 31, 32, 0, 700, 8)
+    for dtype, Hq, Hkv, d in (("bf16", 12, 4, 128), ("f16", 8, 2, 64)):
+        c = Cache(rng, dtype, Hkv, d, kv, prefix)
+        q = rand(rng, (sum(rows), Hq, d), dtype, 2.0)
+        out, lse = _attend(c, q, ints(starts(rows)))
+        ref = kv16.attention(*c.host(), c.table, starts(rows), kv, as_f32(q), c.prefix)
+        tol, ltol = attention_bounds(dtype, *ref, 2100)
+        assert np.all(np.abs(as_f32(out) - ref[0]) <= tol) and np.all(np.abs(lse.cpu().numpy() - ref[1]) <= ltol)
+        old = rng.random((len(kv), Hkv, 2000)).astype(np.float32)
+        scores = torch.from_numpy(old.copy()).cuda()
+        assert c.weigh(q, ints(starts(rows)), lse, 1.0, scores) == 0
+        # lse holds the prefix's weight too
+        new, size = kv16.weigh(c.host()[0], c.table, starts(rows), kv, as_f32(q), lse.cpu().numpy(), 1.0, old)
+        assert np.all(np.abs(scores.cpu().numpy() - new) <= weigh_bounds(new, size, 1.0, old, 9 * Hq // Hkv))
+        assert c.err.item() == 0
+
+
 def test_far_pages():
     """Pools of more than 2^32 bytes: the same tokens far up in them give the same results."""
     rng = np.random.default_rng(33)
