@@ -328,10 +328,14 @@ int llm_op_kv16_attention_workspace(const llm_kv16_cache *cache, const llm_kv16_
  * lies in slots that no row of a sequence sees has no influence; of tokens that some
  * rows of a sequence in the call see and others do not, V has to be finite.
  * q, out: as for llm_op_kv8_attention, of the pages' type; lse: fp32 [n_rows][Hq] or
- * NULL; Hq % Hkv == 0, Hq/Hkv <= 8.  Sums and softmax statistics are fp32.  Results do
- * not depend on the run.  workspace: device, 256-byte aligned, zero-filled once before
- * its first use; every call leaves it ready for the next.  Calls that may run at the
- * same time need workspaces of their own.                                          */
+ * NULL; Hq % Hkv == 0, Hq/Hkv <= 8.  Products of q and K are exact, sums and softmax
+ * statistics fp32; the weights of prefixes, and of own tokens where n_rows * Hq/Hkv >
+ * 8 * n_seqs, are rounded to the pages' type before they meet V, the others keep 16 bits
+ * (bf16) or 22 (fp16).  Results do not depend on the run.  Where a wait ran out (1 s; only a
+ * stalled GPU), out and lse are undefined.  workspace: device, 256-byte aligned, zero-filled
+ * once before its first use; every call leaves it ready for the next, whatever its sizes, so
+ * one made for the largest call serves all.  Calls that may run at the same time (two
+ * streams, two graphs) need workspaces of their own.                               */
 int llm_op_kv16_attention(const llm_kv16_cache *cache, const llm_kv16_prefix *prefix, const void *q,
                           int64_t q_stride, const int32_t *row_start, const int32_t *kv_len, int32_t n_rows,
                           int32_t Hq, void *out, float *lse, void *workspace, int64_t workspace_bytes,
@@ -346,7 +350,7 @@ int llm_op_kv16_attention(const llm_kv16_cache *cache, const llm_kv16_prefix *pr
  * for llm_op_kv16_attention; scores: fp32 [n_seqs][Hkv][score_stride] on the device;
  * keep: finite, >= 0 (1 adds up, less forgets, 0 does not look at what was there).  A
  * sequence longer than score_stride is left out.  Sums are fp32.  Results do not depend on
- * the run.                                                                         */
+ * the run.  Where a wait ran out (LLM_ERR_TIMEOUT), scores are NaN or not yet written.  */
 int llm_op_kv16_weigh(const llm_kv16_cache *cache, const void *q, int64_t q_stride, const int32_t *row_start,
                       const int32_t *kv_len, int32_t n_rows, int32_t Hq, const float *lse, float keep,
                       float *scores, int64_t score_stride, int32_t *err, void *stream);

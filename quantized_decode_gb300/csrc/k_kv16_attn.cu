@@ -33,7 +33,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32, kCtasPerSm = 3, kRows = 8;
 constexpr int kFewPairs = kRows;  // (row, query head) pairs of a sequence and K/V head in the mean, in calls of few rows
 // Pages of a part at least.  (32 steps with 50 to 500 tokens of their own: 8 pages 43.9 us, 16 41.5, 32 39.6; 64 sequences of 150 to 1500: 85.2, 85.3, 86.8.)
 constexpr int kLeast = 4 * kWarps;
-constexpr int kCutFor = 2 * kCtasPerSm;  // parts for each SM: two for each CTA, which draw them
+constexpr int kCutFor = kCtasPerSm;  // parts for each SM.  (Twice as many: 65536 tokens of 4 heads 49 us, not 42; 16 sequences of 8192 of 8 heads 56, not 52.)
 constexpr float kLag = 4.f;
 
 // The part of the workspace that has to do with sequences' own tokens in calls of few rows.
@@ -350,12 +350,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
     pdl_wait();  // so that this kernel's end is that of the wide one too
 }
 
-// ---- Partial results joined: 32 (row, query head) pairs of a K/V head to a CTA, that mostly lie next to one another in the results; each
-// warp takes some of the dims, and SLICES CTAs them all.  What the first warp has to look up about the pairs it finds out before the
+// ---- Partial results joined: 32 (row, query head) pairs of a K/V head to a CTA, that mostly lie next to one another in the results; SLICES CTAs share
+// the dims, SPLIT warps of a CTA the results of the same dims.  What the first warp has to look up about the pairs it finds out before the
 // kernels before end.  F: float4s of a thread, N: results read at a time.  (The code is kept short: a kernel's first pass through it waits
 // for its instructions.)
-template <typename P, int D, int F, int N, int SLICES>
-__global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan, const Own own) {
+template <typename P, int D, int F, int N, int SLICES, int SPLIT>
+__global__ void __launch_bounds__(D / 4 / F / SLICES * SPLIT * 32) k_join(const __grid_constant__ Kv16AttnArgs a, const Kv16Plan plan, const Own own) {
+    constexpr int kParts = D / 4 / F / SLICES;  // warps that share the dims
     struct Found {
         const float *o, *top;
         int64_t step, size4;  // floats from part to part, and from d4 to d4
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_c
     __shared__ Found found[2][32];  // of the prefix and of the sequence's own tokens
     const int Hkv = a.c.n_kv_heads, G = a.Hq / Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned block = blockIdx.x / SLICES;
-    const int part = (int)(blockIdx.x % SLICES) * (D / 4 / F / SLICES) + warp;  // of the dims
+    const int part = (int)(blockIdx.x % SLICES) * kParts + warp % kParts, split = warp / kParts;  // of the dims, of the results
     const int64_t pair = (int64_t)(block / (unsigned)Hkv) * 32 + lane, row = pair / G;
     const int head = (int)(block % (unsigned)Hkv), in = (int)(pair - row * G);
     if (warp == 0) {
@@ -415,15 +416,15 @@ __global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_c
         pdl_wait();
     }
     __syncthreads();
-    if (found[0][lane].n < 0) return;
+    const bool skip = found[0][lane].n < 0;  // nothing to write
     float top = -INFINITY, sum = 0.f;
     float4 v[F];
 #pragma unroll
     for (int i = 0; i < F; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     const Found f = found[0][lane], own_f = found[1][lane];
-    const int n = f.n + own_f.n;
+    const int all = skip ? 0 : f.n + own_f.n, begin = all * split / SPLIT, n = all * (split + 1) / SPLIT;
 #pragma unroll 1
-    for (int k0 = 0; k0 < n; k0 += N) {
+    for (int k0 = begin; k0 < n; k0 += N) {
         float t[N];
         float4 x[N][F];
 #pragma unroll
@@ -455,6 +456,30 @@ __global__ void __launch_bounds__(D / 4 / F / SLICES * 32) k_join(const __grid_c
             for (int i = 0; i < F; ++i)
                 v[i] = make_float4(fmaf(x[k][i].x, w, v[i].x), fmaf(x[k][i].y, w, v[i].y), fmaf(x[k][i].z, w, v[i].z), fmaf(x[k][i].w, w, v[i].w));
         }
+    }
+    if (SPLIT > 1) {  // the warps' results, in the order of the parts
+        __shared__ float4 others[SPLIT][kParts][F][32];
+        __shared__ float2 sums[SPLIT][kParts][32];
+        sums[split][warp % kParts][lane] = make_float2(top, sum);
+#pragma unroll
+        for (int i = 0; i < F; ++i) others[split][warp % kParts][i][lane] = v[i];
+        __syncthreads();
+        if (split > 0 || skip) return;
+#pragma unroll 1
+        for (int x = 1; x < SPLIT; ++x) {
+            const float2 t = sums[x][warp % kParts][lane];
+            if (t.y == 0.f) continue;  // (a row that is NaN has a sum of NaN, whatever its top)
+            const float to = fmaxf(top, t.x), k0 = top == to ? 1.f : ex2(top - to), k1 = ex2(t.x - to);
+            top = to;
+            sum = fmaf(sum, k0, t.y * k1);
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                const float4 o = others[x][warp % kParts][i][lane];
+                v[i] = make_float4(fmaf(o.x, k1, v[i].x * k0), fmaf(o.y, k1, v[i].y * k0), fmaf(o.z, k1, v[i].z * k0), fmaf(o.w, k1, v[i].w * k0));
+            }
+        }
+    } else if (skip) {
+        return;
     }
     const int64_t at = row * a.Hq + head * G + in;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -510,12 +535,13 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
     float *wide = (float *)(space + at.wide);
     const Kv16Plan plan = {plan_at, wide};
     const bool few = kv16_few_rows(a.c, a.Hq, a.n_rows);
+    const int64_t pairs = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads), blocks = (pairs + 31) / 32 * a.c.n_kv_heads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     Own own = {};
     if (!few || a.p.n_groups) {
         const cudaError_t e = launch_kv16_wide(s, n_sm, a, !few, plan_at, wide);
         if (e != cudaSuccess) return e;
     }
-    const int64_t pairs = (int64_t)a.n_rows * (a.Hq / a.c.n_kv_heads);
     if (few) {
         auto kernel = k_attend<P, D>;
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kKv8MaxSeqs);
@@ -529,14 +555,15 @@ cudaError_t attend(cudaStream_t s, int n_sm, const Kv16AttnArgs &a) {
         e = launch_behind(kernel, (unsigned)(most < ctas ? most : ctas), kThreads, 4 * (size_t)a.c.n_seqs, s, a, own);
         if (e != cudaSuccess) return e;
     }
-    const int64_t blocks = (pairs + 31) / 32 * a.c.n_kv_heads;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    // few pairs: many threads and CTAs for each, and many results at a time, since what they wait for is the chain of reads
+    // Few pairs: many threads and CTAs for each, since what they wait for is the chain of reads.  (With the warps of a CTA sharing the dims and each reading
+    // all results, ten at a time: 32 users 36.7 us, not 33.5, 65536 tokens of one sequence 84, not 44.)
     auto join = [&](auto kernel, int slices, int threads) {
-        const cudaError_t e = with_wide(kernel);
-        return e != cudaSuccess ? e : launch_behind(kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
+        cudaError_t e = with_wide(kernel);
+        if (e == cudaSuccess) e = launch_behind(kernel, (unsigned)(blocks * slices), (unsigned)threads, 0, s, a, plan, own);
+        if (e != cudaSuccess && few) cudaMemsetAsync(space, 0, 2 * sizeof(int32_t), s);  // as the join would leave the counters
+        return e;
     };
-    return blocks <= n_sm ? join(k_join<P, D, 1, 10, D / 16>, D / 16, 128) : join(k_join<P, D, 4, 3, 1>, 1, D / 16 * 32);
+    return blocks <= n_sm ? join(k_join<P, D, 4, 3, D / 16, 8>, D / 16, 256) : join(k_join<P, D, 4, 3, 1, 1>, 1, D / 16 * 32);
 }
 
 }  // namespace
