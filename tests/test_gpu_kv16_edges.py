@@ -111,6 +111,25 @@ def test_drafts_among_steps(prefix):
         assert c.err.item() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [(3, 1, 1, 1, 1, 1, 1, 1, 1), (40,), (300,)])
+def test_a_key_that_is_not_finite_and_a_row_does_not_see(dtype, rows):
+    """NaN and infinities in the key of a sequence's last token are the business of its last row alone."""
+    rng = np.random.default_rng(38)
+    kv = tuple(r + 50 for r in rows)
+    for prefix in (None, ([70], [0, len(rows)])):
+        c = Cache(rng, dtype, 2, 64, kv, prefix)
+        q, rs = rand(rng, (sum(rows), 4, 64), dtype), ints(starts(rows))
+        out, lse = _attend(c, q, rs)
+        page, slot = (int(x[-1]) for x in kv16.slots(c.table[0], kv[0]))
+        for bad in (float("nan"), float("inf")):
+            c.k[page, :, slot] = bad
+            got, glse = _attend(c, q, rs)
+            keep = [i for i in range(sum(rows)) if i != rows[0] - 1]
+            assert torch.equal(got[keep], out[keep]) and torch.equal(glse[keep], lse[keep])
+            assert bool(got[rows[0] - 1].isnan().all())
+
+
 def test_far_pages():
     """Pools of more than 2^32 bytes: the same tokens far up in them give the same results."""
     rng = np.random.default_rng(33)
