@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_consta
             mbar_wait(&bar, phase, 1000000000ull);
         }
         here = __syncthreads_and(here);
-        cluster_sync();  // everything that this round overwrites has been read
+        cluster_sync();  // everything that is overwritten now has been read
         if (!here) break;
 #pragma unroll
         for (int x = 0; x < kMost; ++x)

@@ -19,9 +19,9 @@
 // beside the wide kernel's, with which it shares the memory's time, and more when those end.  An item leaves a partial result
 // in the workspace, unless it is all that its rows have to see, and k_join puts them together, in a fixed order.
 //
-// Measured: 64 sequences of 150 to 1500 tokens in 4 groups behind 4 prefixes to 12000 (32/8 heads of 128, bf16, 317 MB): 82 us, 3.9 TB/s; of it 57 beside the wide
-// kernel, 13 after it, 10 for the join.  Apart, one kernel after the other, 32 steps behind one prefix take 49 us, beside one another 37 (with the
-// pages two ahead fetched into L2; without 39).
+// Measured: 64 sequences of 150 to 1500 tokens in 4 groups behind 4 prefixes to 12000 (32/8 heads of 128, bf16, 317 MB): 83 us, 3.8 TB/s; of it 57 beside the wide
+// kernel, 13 after it, 10 for the join.  Apart, one kernel after the other, 32 steps behind one prefix took 51.7 us, beside one another 41.5 (33.5 now), with the
+// pages two ahead fetched into L2; without that 43.3.
 #include "kv16_attn.cuh"
 #include "kv16_line.cuh"
 

@@ -15,9 +15,9 @@
 // The maximum that the exponent refers to follows the row's only when that has grown by 2^kLag, so O is rarely rescaled.
 // Weights are rounded to the pages' type once; their sum is taken before.
 //
-// Measured, heads of 128.  8 x 200 rows of 32/8 heads behind 20000 tokens, 0.53 TFLOP: 440 us of the call's 473, 1.2 PFLOP/s.  A block of both tiles
+// Measured, heads of 128.  8 x 200 rows of 32/8 heads behind 20000 tokens, 0.53 TFLOP: 430 us of the call's 467, 1.2 PFLOP/s.  A block of both tiles
 // takes 3300 cycles, of which the MMAs' own time is 2054: those of the scores, with q and K both from shared memory, are bound by what that
-// delivers (8 KB for each 64 cycles of the tensor core).  32 steps of 32/8 heads behind 16384 tokens (67 MB): 25 of 37 us, 8 of them until the first
+// delivers (8 KB for each 64 cycles of the tensor core).  32 steps of 32/8 heads behind 16384 tokens (67 MB): 25 of 33.5 us, 8 of them until the first
 // score (lengths, table and first keys one after another), then 5.6 TB/s, then 4 for the results.
 #include "kv16_attn.cuh"
 #include "kv16_tc.cuh"
