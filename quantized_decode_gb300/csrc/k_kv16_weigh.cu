@@ -6,7 +6,7 @@
 // the operand registers of mma.sync; many (k_weigh_wide) by exponentials and products, on the 5th-generation tensor cores.
 //
 // Measured: one row of each of 8 sequences to 16000 tokens (32/8 heads of 128, 185 MB) 33 us, 5.7 TB/s; two prompts of 4000 rows or so (28/4 heads,
-// 0.13 TFLOP, 5e8 exponentials) 177 us, 0.73 PFLOP/s: a tile of 128 x 128 costs an SM about 1600 cycles, 1050 of them in the MMAs (both
+// 0.13 TFLOP, 5e8 exponentials) 168 us, 0.76 PFLOP/s: a tile of 128 x 128 costs an SM about 1550 cycles, 1050 of them in the MMAs (both
 // operands from shared memory); the rest is the turn of barriers, statistics and sums, and what clusters end unevenly.
 #include "kv16_line.cuh"
 #include "kv16_tc.cuh"
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_weigh(const __grid_con
 // With long prompts a cluster shares a block of tokens, every CTA a part of the tiles, and its first CTA adds up what
 // the others bring through distributed shared memory.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, kSumWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kWideThreads = 320, kStages = 2, kMaxShare = 4;
+constexpr int kTile = 128, kSumWarps = 8, kMmaWarp = 8, kCopyWarp = 9, kWideThreads = 320, kStages = 2, kMaxShare = 2;
 
 struct WideArgs {
     Kv16WeighArgs a;
@@ -188,13 +188,57 @@ struct Bars {
     int abort, stop;
 };
 
-// The n-th item: a sequence, a block of its tokens and a head.
+// The n-th item: a sequence, a block of its tokens and a head.  Of up to 32 sequences the heaviest items come first: blocks lose tiles along a sequence,
+// so how many have more than x is a division for each, and the n-th item's x is found by halving.
 struct WeighItem {
     Kv8Seq s;
     int b, block, head, tile0, tiles;  // tiles of rows that see something of the block
 };
 QD_DEV bool weigh_item(const Kv16WeighArgs &a, int64_t n, int R, WeighItem &it) {
     const int lane = threadIdx.x & 31, Hkv = a.c.n_kv_heads, B = a.c.n_seqs;
+    auto take = [&](const Kv8Seq &s, int l, int b, int block, int head) {  // lane l's sequence
+        it.b = b;
+        it.s.row0 = __shfl_sync(kFullMask, s.row0, l);
+        it.s.rows = __shfl_sync(kFullMask, s.rows, l);
+        it.s.kv = __shfl_sync(kFullMask, s.kv, l);
+        it.block = block;
+        it.head = head;
+        const int first = block * kTile - (it.s.kv - it.s.rows);  // the first row that sees the block's first token
+        it.tile0 = first > 0 ? first / R : 0;
+        it.tiles = (it.s.rows - 1) / R + 1 - it.tile0;
+    };
+    if (B <= 32) {
+        Kv8Seq s = {0, 0, 0, true};
+        if (lane < B) s = weigh_seq(a, lane);
+        const int blocks = s.rows > 0 ? kv8_blocks(s.kv, kTile) : 0, tiles = s.rows > 0 ? (s.rows - 1) / R + 1 : 0;
+        // of this lane's sequence the blocks with more than x tiles, which are its first ones
+        auto above = [&](int x) {
+            if (tiles <= x) return 0;
+            const int64_t rows = (int64_t)(tiles - x) * R + s.kv - s.rows;
+            return (int)min((int64_t)blocks, max((int64_t)0, (rows + kTile - 1) / kTile));
+        };
+        auto all_above = [&](int x) { return (int64_t)__reduce_add_sync(kFullMask, (unsigned)above(x)) * Hkv; };
+        if (n >= all_above(0)) return false;
+        int lo = 0, hi = __reduce_max_sync(kFullMask, tiles);  // more than n items are above lo, no more than n above hi
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (all_above(mid) > n) lo = mid;
+            else hi = mid;
+        }
+        const int before = above(hi), mine = above(lo) - before;  // blocks of this sequence that have hi tiles
+        const int64_t in = n - all_above(hi);
+        int upto = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(kFullMask, upto, m);
+            if (lane >= m) upto += v;
+        }
+        const int l = __ffs(__ballot_sync(kFullMask, in < (int64_t)upto * Hkv)) - 1;
+        const int64_t in_l = in - (int64_t)__shfl_sync(kFullMask, upto - mine, l) * Hkv;
+        const int k = (int)(in_l / Hkv);
+        take(s, l, l, __shfl_sync(kFullMask, before, l) + k, (int)(in_l - (int64_t)k * Hkv));
+        return true;
+    }
     int64_t base = 0;
     for (int i0 = 0; i0 < B; i0 += 32) {
         Kv8Seq s = {0, 0, 0, true};
@@ -210,15 +254,8 @@ QD_DEV bool weigh_item(const Kv16WeighArgs &a, int64_t n, int R, WeighItem &it) 
         if (hit) {
             const int l = __ffs(hit) - 1;
             const int64_t in = n - base - __shfl_sync(kFullMask, upto - items, l);
-            it.b = i0 + l;
-            it.s.row0 = __shfl_sync(kFullMask, s.row0, l);
-            it.s.rows = __shfl_sync(kFullMask, s.rows, l);
-            it.s.kv = __shfl_sync(kFullMask, s.kv, l);
-            it.block = (int)(in / Hkv);
-            it.head = (int)(in - (int64_t)it.block * Hkv);
-            const int first = it.block * kTile - (it.s.kv - it.s.rows);  // the first row that sees the block's first token
-            it.tile0 = first > 0 ? first / R : 0;
-            it.tiles = (it.s.rows - 1) / R + 1 - it.tile0;
+            const int block = (int)(in / Hkv);
+            take(s, l, i0 + l, block, (int)(in - (int64_t)block * Hkv));
             return true;
         }
         base += __shfl_sync(kFullMask, upto, 31);
@@ -333,7 +370,7 @@ __global__ void __maxnreg__(96) k_weigh_wide(const __grid_constant__ WideArgs w)
     };
     auto wait_warp = [&](uint64_t *bar, uint32_t phase) { return __all_sync(kFullMask, wait(bar, phase)) != 0; };
     if (threadIdx.x == 0 && (smem_u32(smem) & 1023)) fail();  // the swizzle goes by the address
-    // The CTA's n-th item: rounds go up and down the clusters, since items get lighter along a sequence.
+    // The CTA's n-th item: rounds go up and down the clusters, since items get lighter.
     auto nth = [&](int n) { return (int64_t)n * clusters + (n & 1 ? clusters - 1 - cluster : cluster); };
     // of an item's tiles this CTA takes every share-th
     auto my_tiles = [&](const WeighItem &it) { return it.tiles > rank ? (it.tiles - rank - 1) / share + 1 : 0; };
@@ -521,8 +558,9 @@ cudaError_t wide(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     w.a = a;
     const int G = a.Hq / a.c.n_kv_heads;
     if (!kv16_page_map(&w.k, a.c.k_pool, a.c) || !kv16_row_map(&w.q, a.q, a.q_stride, a.n_rows, a.Hq, G, kTile / G, D)) return cudaErrorInvalidValue;
-    // Clusters of 4 where a block's rows are 16 tiles or more.  (Two prompts of 4000 rows: one CTA 415 us, two 187, four 185, eight 230.)
-    w.log_share = (int64_t)a.n_rows * G >= (int64_t)16 * kTile * a.c.n_seqs ? 2 : 0;
+    // Clusters of 2 where a block's rows are 16 tiles or more.  (Two prompts of 4000 rows: one CTA 360 us, two 168, four 185; eight, with items in the order of the
+    // sequences, 230.)
+    w.log_share = (int64_t)a.n_rows * G >= (int64_t)16 * kTile * a.c.n_seqs ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kWideThreads);
     cfg.dynamicSmemBytes = kBytes;
@@ -540,7 +578,8 @@ cudaError_t wide(cudaStream_t s, int n_sm, const Kv16WeighArgs &a) {
     int64_t most = 2 * n_sm;
     if (w.log_share > 0) {
         // No more clusters than run at a time, a second round would take as long as the first: two for each place that the device has
-        // for one with an SM to each CTA.  (72; with 76, which 152 SMs seem to hold, two prompts of 4000 rows take 254 us instead of 190.)
+        // for one with an SM to each CTA.  (Of clusters of four 72; with 76, which 152 SMs seem to hold, two prompts of 4000 rows took 254 us instead
+        // of 190.)
         static const int places = [&]() {
             cfg.gridDim = dim3(1u << w.log_share);
             int n = 0;

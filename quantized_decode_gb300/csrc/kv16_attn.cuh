@@ -80,13 +80,6 @@ QD_DEV Kv16Parts kv16_parts(const Kv16Plan &plan, int i, bool prefix, int blocks
     return Kv16Parts{p + ((int64_t)tile * (d / 4) * kTileLanes + lane) * 4, p + 2 * (int64_t)kTileLanes * d + tile * kTileLanes + lane, step * size, n};
 }
 
-// The group of a sequence: its number, or -1; by the whole warp.
-QD_DEV int kv16_group_of(const Kv16AttnArgs &a, int b) {
-    if (a.p.n_groups == 0) return -1;
-    const int g = kv16_seq_of_row(a.p.seq_start, a.p.n_groups, b);
-    return b >= __ldg(a.p.seq_start + g) && b < __ldg(a.p.seq_start + g + 1) ? g : -1;
-}
-
 template <typename P>
 QD_DEV void store_out4(P *p, const float4 &v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(Bits16<P>::pack(v.x, v.y), Bits16<P>::pack(v.z, v.w));
