@@ -1,5 +1,5 @@
 // k_kv16_attn.cu - attention over the 16-bit paged cache behind shared prefixes, for few rows per sequence (decode
-// steps, drafted tokens): the sequences' own tokens, and the join with what the wide kernel made of the prefixes.
+// steps): the sequences' own tokens, and the join with what the wide kernel made of the prefixes.
 //
 // The mathematics, for 8 (row, query head) pairs of one K/V head and a page of 16 tokens, with mma.sync m16n8k16:
 //   S^T[token][row] = K q^T      A = the page's K, B = q of the 8 rows
@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attend(const __grid_co
             const Kv8Seq s = kv16_seq(a.row_start, a.kv_len, a.n_rows, a.c, b);
             return Kv16Line{(s.rows * G + kRows - 1) / kRows * Hkv, kv8_pages(s.kv), s.ok};
         },
-        upto, blockIdx.x == 0 ? a.err : nullptr);
+        upto, s_item[0] == 0 ? a.err : nullptr);
     const bool fits = upto[B - 1] <= own.capacity;  // else row_start falls somewhere
     const int items = fits ? upto[B - 1] : 0;
-    if (s_item[0] == 0) {  // the CTA that has the first item tells k_join about rows and sequences
+    if (s_item[0] == 0) {  // the CTA that has the first item, which may be any, tells k_join about rows and sequences
         for (int i = threadIdx.x; i < a.n_rows; i += kThreads) own.seq_of[i] = -1;
         __syncthreads();
         for (int b = threadIdx.x; b < B; b += kThreads) {
